@@ -34,11 +34,15 @@
  *     gate and up, [H, I] for down).
  *   sh_gate, sh_up [I_shared, H], sh_down [H, I_shared]   act_dtype
  *     BF16 expert matrices (routed and shared) are passed as moe_pack_bf16
- *     lays them out (below); F32 ones row-major as listed.  The caller
+ *     lays them out (below); F32 and FP8 ones row-major as listed.  The caller
  *     states which in moe_weights_t.layout: MOE_LAYOUT_PACKED is required for
- *     BF16 and MXFP4 expert matrices, MOE_LAYOUT_ROWMAJOR for F32 ones; any
+ *     BF16 and MXFP4 expert matrices, MOE_LAYOUT_ROWMAJOR for F32 and FP8; any
  *     other combination is refused with MOE_EINVAL (a zero-initialised
  *     struct says ROWMAJOR, so row-major bf16 weights never reach a kernel).
+ *     FP8 (E4M3 codes, one float scale per 128 x 128 block): row-major codes
+ *     and scales [E, N/128, K/128] in s_gate, s_up, s_down, as
+ *     moe_quant_fp8 makes them; x is quantised in the call (1 x 128 blocks),
+ *     and so is h, from its fp32 values.
  *   topk_idx [T, top_k] int32, topk_w [T, top_k] float
  *
  * Packed MXFP4 (what the kernels read: each wave's weights are whole
@@ -57,8 +61,9 @@
  * of row n = 32*g + 8*(r/4) + 4*c + r%4 at K = 32*s + 8*b .. +7:
  *   [E][N/32][K/32][2][64 lanes][8 bf16].
  *
- * Supported combinations: act F32 with w F32; act BF16 with w BF16 or MXFP4.
- * MXFP4 needs H and I multiples of 128, at most 4096, and no shared expert
+ * Supported combinations: act F32 with w F32; act BF16 with w BF16, MXFP4 or
+ * FP8.  FP8 needs H and I multiples of 128, at most 32768, and no shared
+ * expert (MOE_EINVAL / MOE_EUNSUPPORTED otherwise).  MXFP4 needs H and I multiples of 128, at most 4096, and no shared expert
  * (MOE_EINVAL / MOE_EUNSUPPORTED otherwise).  One pass (chunk) of Tc tokens
  * must keep Tc * H, Tc * E * 8 and rows * max(H, I, I_shared) below 2^31,
  * rows = Tc * top_k (+ Tc with a shared expert); larger passes are refused
@@ -85,7 +90,7 @@
 extern "C" {
 #endif
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2 } moe_dtype_t;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2, MOE_FP8 = 3 } moe_dtype_t;
 
 /* Layout of the expert matrices in moe_weights_t (see Layouts above). */
 enum { MOE_LAYOUT_ROWMAJOR = 0, MOE_LAYOUT_PACKED = 1 };
@@ -125,7 +130,7 @@ typedef struct {
     const void *router_w;
     const float *router_bias;                /* nullable                     */
     const void *w_gate, *w_up, *w_down;      /* codes when w_dtype == MXFP4  */
-    const uint8_t *s_gate, *s_up, *s_down;   /* E8M0, MXFP4 only             */
+    const uint8_t *s_gate, *s_up, *s_down;   /* MXFP4: E8M0; FP8: the floats */
     const void *sh_gate, *sh_up, *sh_down;   /* I_shared > 0 only            */
     int32_t layout;  /* MOE_LAYOUT_* of the expert and shared matrices       */
 } moe_weights_t;
@@ -177,6 +182,117 @@ int moe_route(const moe_shape_t *shape, const moe_weights_t *w,
               const void *x, int32_t *topk_idx, float *topk_w,
               int32_t *counts, int32_t *offsets, int32_t *row_src,
               void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Routing and experts apart --------------------------------------------
+ * The layer in three calls, for routing other than moe_forward's:
+ *   moe_logits  -> moe_select -> moe_experts
+ * (any of them may be replaced by the caller's own: moe_experts takes whatever
+ * routing it is given).  The general rules above hold for them: device
+ * pointers, nothing allocated, nothing read back, asynchronous on `stream`.
+ */
+
+/* The router's logits alone: logits[T, E] (fp32) = x . router_w^T
+ * (+ router_bias).  Only the shape's T, H, E, top_k and act_dtype and the
+ * weights' router_w and router_bias are used (the shape must be valid as a
+ * whole).  x and logits 16-byte aligned. */
+int moe_logits(const moe_shape_t *shape, const moe_weights_t *w, const void *x, float *logits,
+               void *stream);
+
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+/* Selection of experts from logits [T, E]:
+ *   score  s_e = softmax(l)_e over all E, or 1 / (1 + exp(-l_e))
+ *   key    s_e + bias_e (the bias balances the experts' loads: it counts in
+ *          the selection, not in the weights)
+ *   groups n_group > 1: groups of E / n_group consecutive experts, valued by
+ *          their largest key or the sum of their two largest; only experts of
+ *          the topk_group best groups (equal ones: the lower group) remain
+ *   top-k  the k remaining experts by key, descending, equal keys to the lower
+ *          index: topk_idx, in that order
+ *   weights topk_w = s of the selected, divided by their sum if renorm, times
+ *          scale; all 0 where the sum is 0
+ * The order is that of the keys in 64 bits, whatever type the logits have.
+ * An expert is masked by a logit of -inf or NaN or a bias of -inf or NaN: it
+ * ranks behind all others (masked ones by index) and has weight 0, and a masked
+ * logit has no share of the softmax.  A group of masked experts only ranks last.  +inf
+ * counts as the largest finite float. */
+typedef struct {
+    int32_t T;            /* tokens                                             */
+    int32_t E;            /* experts, 1..1024                                   */
+    int32_t top_k;        /* 1..min(E, 16), at most the open groups' experts    */
+    int32_t n_group;      /* 1 = no groups; at most 64, divides E               */
+    int32_t topk_group;   /* 1..n_group                                         */
+    int32_t score;        /* MOE_SCORE_*                                        */
+    int32_t group_score;  /* MOE_GROUP_*                                        */
+    int32_t renorm;       /* nonzero: weights divided by their sum              */
+    int32_t logit_dtype;  /* MOE_F32 or MOE_BF16                                */
+    float scale;          /* factor of the weights                              */
+    int64_t ld;           /* row stride of the logits in elements, 0 = E        */
+} moe_select_t;
+
+/* logits [T, E] (row stride ld), bias [E] float or NULL, topk_idx [T, top_k],
+ * topk_w [T, top_k] or NULL; pointers aligned to their elements. */
+int moe_select(const moe_select_t *select, const void *logits, const float *bias,
+               int32_t *topk_idx, float *topk_w, void *stream);
+
+/* The routed experts with given routing: y_t = sum over j of topk_w[t, j] *
+ * FFN of expert topk_idx[t, j] on x_t, in j order.  Every weight type of
+ * moe_forward; the weights' router_w and router_bias are not used (NULL is
+ * fine) and I_shared must be 0 (MOE_EUNSUPPORTED otherwise).  A slot whose
+ * index is outside 0..E-1 (say -1) is empty: it costs and adds nothing, and a
+ * token with empty slots only gets zeros.  An expert may occur more than once
+ * in a token.  Workspace and chunk_T as for moe_forward; x and y 16-byte
+ * aligned, topk_idx and topk_w 4-byte. */
+int moe_experts(const moe_shape_t *shape, const moe_weights_t *w, const void *x,
+                const int32_t *topk_idx, const float *topk_w, void *y, void *ws,
+                size_t ws_bytes, void *stream);
+
+/* ---- FP8 (E4M3) with block scales ------------------------------------------ */
+
+/* Rows [R, K] to E4M3 codes and float scales, one per block of block_rows x
+ * 128 (1: activations, 128: weights):
+ *   top = max(max |x| over the block, 2^-100), scale = top / 448,
+ *   code = the E4M3 value nearest to 448 x / top, ties to the even one
+ * so x is about code * scale.  The last blocks of a row or column are cut off
+ * at K and R.  NaN elements are passed over by the maximum and get the NaN
+ * code; every code of a block with an infinity is NaN. */
+typedef struct {
+    int32_t R, K;        /* rows and columns                                    */
+    int32_t block_rows;  /* 1 or 128                                            */
+    int32_t src_dtype;   /* MOE_F32 or MOE_BF16                                 */
+    int64_t ld;          /* row stride of x in elements, 0 = K                  */
+} moe_quant_t;
+
+/* codes [R, Kp] bytes, Kp = K rounded up to a multiple of 128, the columns
+ * behind K zero; scales [R, Kp / 128] (block_rows 1) or [R / 128 rounded up,
+ * Kp / 128] (128).  x and scales element aligned, codes 16-byte aligned; the
+ * outputs overlap neither x nor each other.  A stack of matrices [E, N, K]
+ * with N a multiple of 128 is one call with R = E * N. */
+int moe_quant_fp8(const moe_quant_t *quant, const void *x, void *codes, float *scales,
+                  void *stream);
+
+/* Product of such codes, y[m, n] = sum over blocks q of 128 K of sa[m, q] *
+ * sb[n / 128, q] * sum over k in q of a[m, k] * b[n, k]: the sums in fp32, y
+ * rounded once.  With G > 1 the rows of a are grouped: rows offsets[g] ..
+ * offsets[g + 1] - 1 meet matrix b[g] (groups may be empty); rows outside
+ * offsets[0] .. offsets[G] - 1 of y stay as they were.  offsets is a device array, not
+ * decreasing; parts of it outside 0..M are cut off. */
+typedef struct {
+    int32_t M, N, K;     /* rows of a, rows of each b, depth (at most 32768)    */
+    int32_t G;           /* matrices b, 1..65535                                */
+    int32_t out_dtype;   /* MOE_F32 or MOE_BF16                                 */
+    int64_t lda, ldb;    /* row strides in bytes, multiples of 16, 0 = Kp       */
+    int64_t ldy;         /* row stride of y in elements, 0 = N                  */
+} moe_matmul_t;
+
+/* a [M, Kp] codes (Kp = K rounded up to a multiple of 128; the columns behind
+ * K must hold zero codes, as moe_quant_fp8 writes them), sa [M, Kp / 128],
+ * b [G, N, Kp] codes, sb [G, N / 128 rounded up, Kp / 128], offsets [G + 1]
+ * (G = 1: NULL takes all rows), y [M, N].  a and b 16-byte aligned, the others
+ * element aligned; y overlaps neither a nor sa. */
+int moe_matmul_fp8(const moe_matmul_t *matmul, const void *a, const float *sa, const void *b,
+                   const float *sb, const int32_t *offsets, void *y, void *stream);
 
 /* Repack E MXFP4 matrices of N rows and K columns (N a multiple of 16, K of
  * 128) from the OCP row-major form (codes [E, N, K/2], scales [E, N, K/32])

@@ -15,20 +15,25 @@ import os
 from typing import Optional
 
 __all__ = [
-    "MOE_F32", "MOE_BF16", "MOE_MXFP4", "MOE_LAYOUT_ROWMAJOR", "MOE_LAYOUT_PACKED", "MOE_OK",
+    "MOE_F32", "MOE_BF16", "MOE_MXFP4", "MOE_FP8", "MOE_LAYOUT_ROWMAJOR", "MOE_LAYOUT_PACKED", "MOE_OK",
     "MOE_EINVAL", "MOE_EWORKSPACE", "MOE_EUNSUPPORTED", "MOE_EHIP", "MoeError", "moe_shape_t", "moe_weights_t", "make_shape",
     "make_weights", "moe_workspace_bytes", "moe_forward", "moe_forward_noalloc",
     "MOE_NOALLOC_SCRATCH_BYTES", "moe_route", "moe_strerror",
     "moe_last_error", "moe_stage_timing_enable", "moe_stage_timing_read", "moe_pack_bf16",
     "pack_bf16", "moe_pack_mxfp4", "pack_mxfp4", "STAGES", "moe_probe_read", "moe_probe_mfma",
     "moe_probe_gather", "moe_probe_mxfp4",
+    "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_GROUP_MAX", "MOE_GROUP_TOP2", "moe_select_t",
+    "moe_quant_t", "moe_matmul_t", "make_select", "make_quant", "make_matmul", "moe_logits",
+    "moe_select", "moe_experts", "moe_quant_fp8", "quant_fp8", "moe_matmul_fp8",
     "lib_path", "load",
 ]
 
-MOE_F32, MOE_BF16, MOE_MXFP4 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_MXFP4, MOE_FP8 = 0, 1, 2, 3
 MOE_LAYOUT_ROWMAJOR, MOE_LAYOUT_PACKED = 0, 1
 MOE_OK, MOE_EINVAL, MOE_EWORKSPACE, MOE_EUNSUPPORTED, MOE_EHIP = 0, -1, -2, -3, -4
-_DT = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp4": MOE_MXFP4}
+_DT = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp4": MOE_MXFP4, "fp8": MOE_FP8}
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -52,6 +57,22 @@ class moe_weights_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("router_w", "router_bias", "w_gate", "w_up", "w_down", "s_gate", "s_up",
                  "s_down", "sh_gate", "sh_up", "sh_down")] + [("layout", ctypes.c_int32)]
+
+
+class moe_select_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "E", "top_k", "n_group", "topk_group", "score", "group_score", "renorm",
+                 "logit_dtype")] + [("scale", ctypes.c_float), ("ld", ctypes.c_int64)]
+
+
+class moe_quant_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "K", "block_rows", "src_dtype")] + \
+        [("ld", ctypes.c_int64)]
+
+
+class moe_matmul_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "G", "out_dtype")] + \
+        [(n, ctypes.c_int64) for n in ("lda", "ldb", "ldy")]
 
 
 _lib = None
@@ -103,6 +124,16 @@ def load() -> ctypes.CDLL:
                                          ctypes.c_int, P]
         lib.moe_probe_mxfp4.restype = ctypes.c_int
         lib.moe_probe_mxfp4.argtypes = [P, P, ctypes.c_size_t, ctypes.c_int, P, P]
+        lib.moe_logits.restype = ctypes.c_int
+        lib.moe_logits.argtypes = [P, P, P, P, P]
+        lib.moe_select.restype = ctypes.c_int
+        lib.moe_select.argtypes = [P, P, P, P, P, P]
+        lib.moe_experts.restype = ctypes.c_int
+        lib.moe_experts.argtypes = [P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.moe_quant_fp8.restype = ctypes.c_int
+        lib.moe_quant_fp8.argtypes = [P, P, P, P, P]
+        lib.moe_matmul_fp8.restype = ctypes.c_int
+        lib.moe_matmul_fp8.argtypes = [P, P, P, P, P, P, P, P]
         _lib = lib
     return _lib
 
@@ -223,6 +254,131 @@ def pack_mxfp4(codes, scales, stream=None):
     moe_pack_mxfp4(E, N, 2 * K2, codes, scales, out_c, out_s, stream)
     out_c._moe_layout = out_s._moe_layout = "packed"
     return out_c, out_s
+
+
+def make_select(T, E, top_k, score="softmax", n_group=1, topk_group=1, group_score="max", renorm=True,
+                scale=1.0, logits="f32", ld=0) -> moe_select_t:
+    return moe_select_t(T, E, top_k, n_group, topk_group,
+                        {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score],
+                        {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}[group_score], int(renorm),
+                        _DT[logits], scale, ld)
+
+
+def make_quant(R, K, src="bf16", block_rows=1, ld=0) -> moe_quant_t:
+    return moe_quant_t(R, K, block_rows, _DT[src], ld)
+
+
+def make_matmul(M, N, K, G=1, out="bf16", lda=0, ldb=0, ldy=0) -> moe_matmul_t:
+    return moe_matmul_t(M, N, K, G, _DT[out], lda, ldb, ldy)
+
+
+def _dev(t, what: str, elems: int, *dtypes: str) -> Optional[int]:
+    """Device pointer of a tensor of the operators below (None -> NULL),
+    after checking its type, its device (the current one) and that it holds
+    `elems` elements from its pointer on: a strided view is given with its
+    row stride, and what it spans counts."""
+    if t is None:
+        return None
+    if str(t.dtype)[6:] not in dtypes:
+        raise ValueError("%s: dtype %s, expected %s" % (what, t.dtype, " or ".join(dtypes)))
+    if not t.is_cuda:
+        raise ValueError("%s is not on a GPU" % what)
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d"
+                         % (what, t.get_device(), torch.cuda.current_device()))
+    held = t.numel() if t.is_contiguous() else \
+        1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else 0
+    if held < elems:
+        raise ValueError("%s spans %d elements, the call needs %d" % (what, held, elems))
+    return t.data_ptr()
+
+
+_SRC = {MOE_F32: "float32", MOE_BF16: "bfloat16"}
+_CODES = ("float8_e4m3fn", "uint8")
+
+
+def _span(rows: int, ld: int, cols: int) -> int:
+    return (rows - 1) * ld + cols if rows > 0 else 0
+
+
+def moe_logits(shape, weights, x, logits, stream=None) -> None:
+    """The router's logits [T, E] (float32) of x[T, H]."""
+    src = _SRC.get(shape.act_dtype, "bfloat16")
+    _check(load().moe_logits(ctypes.byref(shape), ctypes.byref(weights.c),
+                             _dev(x, "x", shape.T * shape.H, src),
+                             _dev(logits, "logits", shape.T * shape.E, "float32"), _stream(stream)))
+
+
+def moe_select(select, logits, bias, topk_idx, topk_w, stream=None) -> None:
+    """topk_idx, topk_w [T, top_k] of the tokens with these logits (see include/moe.h)."""
+    s = select
+    n = s.T * s.top_k
+    _check(load().moe_select(ctypes.byref(s),
+                             _dev(logits, "logits", _span(s.T, s.ld or s.E, s.E),
+                                  _SRC.get(s.logit_dtype, "float32")),
+                             _dev(bias, "bias", s.E, "float32"),
+                             _dev(topk_idx, "topk_idx", n, "int32"),
+                             _dev(topk_w, "topk_w", n, "float32"), _stream(stream)))
+
+
+def moe_experts(shape, weights, x, topk_idx, topk_w, y, ws, ws_bytes=None, stream=None) -> None:
+    """y[T, H] of the routed experts with given routing (see include/moe.h)."""
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    src = _SRC.get(shape.act_dtype, "bfloat16")
+    n, m = shape.T * shape.H, shape.T * shape.top_k
+    _check(load().moe_experts(ctypes.byref(shape), ctypes.byref(weights.c), _dev(x, "x", n, src),
+                              _dev(topk_idx, "topk_idx", m, "int32"),
+                              _dev(topk_w, "topk_w", m, "float32"), _dev(y, "y", n, src), _ptr(ws),
+                              ws_bytes, _stream(stream)))
+
+
+def moe_quant_fp8(quant, x, codes, scales, stream=None) -> None:
+    """E4M3 codes [R, Kp] and their float32 block scales of x[R, K] (see include/moe.h)."""
+    q = quant
+    kb = -(-q.K // 128)
+    _check(load().moe_quant_fp8(ctypes.byref(q),
+                                _dev(x, "x", _span(q.R, q.ld or q.K, q.K),
+                                     _SRC.get(q.src_dtype, "bfloat16")),
+                                _dev(codes, "codes", q.R * kb * 128, *_CODES),
+                                _dev(scales, "scales", -(-q.R // max(1, q.block_rows)) * kb, "float32"),
+                                _stream(stream)))
+
+
+def quant_fp8(x, block_rows=1, stream=None):
+    """(codes, scales) of a device tensor [R, K] or [E, N, K] (N a multiple of
+    block_rows), bf16 or float32; unit stride along K."""
+    import torch
+    if x.dim() not in (2, 3) or (x.dim() == 3 and x.shape[1] % block_rows):
+        raise ValueError("quant_fp8 takes [R, K], or [E, N, K] with N a multiple of block_rows")
+    if x.dim() == 3 or x.stride(1) != 1 or x.stride(0) < x.shape[1]:
+        x = x.contiguous()
+    lead, K = x.shape[:-1], x.shape[-1]
+    R = x.numel() // max(1, K)
+    kb = -(-K // 128)
+    codes = torch.empty(*lead, kb * 128, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty(*lead[:-1], -(-lead[-1] // block_rows), kb, dtype=torch.float32, device=x.device)
+    src = {v: k for k, v in _SRC.items()}.get(str(x.dtype)[6:], -1)
+    moe_quant_fp8(moe_quant_t(R, K, block_rows, src, x.stride(0) if x.dim() == 2 and R > 1 else 0), x,
+                  codes, scales, stream)
+    return codes, scales
+
+
+def moe_matmul_fp8(matmul, a, sa, b, sb, y, offsets=None, stream=None) -> None:
+    """y[M, N] of the codes a[M, Kp] and b[G, N, Kp] with their block scales
+    (see include/moe.h); the rows of a are split among the b by `offsets`."""
+    m = matmul
+    kb = -(-m.K // 128)
+    kp = kb * 128
+    _check(load().moe_matmul_fp8(ctypes.byref(m),
+                                 _dev(a, "a", _span(m.M, m.lda or kp, kp), *_CODES),
+                                 _dev(sa, "sa", m.M * kb, "float32"),
+                                 _dev(b, "b", _span(m.G * m.N, m.ldb or kp, kp), *_CODES),
+                                 _dev(sb, "sb", m.G * -(-m.N // 128) * kb, "float32"),
+                                 _dev(offsets, "offsets", m.G + 1, "int32"),
+                                 _dev(y, "y", _span(m.M, m.ldy or m.N, m.N),
+                                      _SRC.get(m.out_dtype, "bfloat16")), _stream(stream)))
 
 
 STAGES = ("router", "permute", "gate_up", "down", "combine")

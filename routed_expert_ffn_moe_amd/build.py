@@ -18,7 +18,8 @@ OUT = os.path.join(HERE, "libmoe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["probe.hip", "router.hip", "route_small.hip", "permute.hip", "expert_gemm.hip",
-           "expert_stream.hip", "mxfp4.hip", "moe_api.cpp", "noalloc.hip"]
+           "expert_stream.hip", "mxfp4.hip", "select.hip", "quant_fp8.hip", "matmul_fp8.hip",
+           "experts_given.hip", "moe_api.cpp", "moe_ops.cpp", "noalloc.hip"]
 
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",

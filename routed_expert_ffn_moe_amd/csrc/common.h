@@ -15,6 +15,8 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 namespace moe {
 
+constexpr int FP8_K = 128;  // elements of K under one scale of the FP8 operators
+
 // bf16 <-> fp32.  bf16 values travel as uint16_t bit patterns.
 __device__ __forceinline__ float bf2f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 

@@ -11,7 +11,7 @@
 namespace moe {
 
 enum { ACT_F32 = 0, ACT_BF16 = 1 };
-enum { W_F32 = 0, W_BF16 = 1, W_MXFP4 = 2 };
+enum { W_F32 = 0, W_BF16 = 1, W_MXFP4 = 2, W_FP8 = 3 };
 
 struct RouterArgs {
     const void *x;        // [T, H] act
@@ -154,6 +154,9 @@ struct CombineArgs {
     int T, H, k, shared, act;
 };
 void launch_combine(const CombineArgs &a, hipStream_t st);
+// The same for given routing, where row_of < 0 marks an empty slot (no shared
+// expert): experts_given.hip.
+void launch_combine_given(const CombineArgs &a, hipStream_t st);
 
 // Row-major bf16 [E, N, K] into the packed layout the bf16 GEMMs read
 // (packed_bf16_off in common.h).
@@ -162,6 +165,53 @@ void launch_pack_bf16(int E, int N, int K, const uint16_t *w, uint16_t *out, hip
 // Records `what` as the calling thread's last error (moe_last_error) and
 // returns `code`: for entry points outside moe_api.cpp.
 int api_fail(int code, const char *what);
+int api_check_device();                // MOE_OK on gfx950, else the recorded failure
+int api_launched(const char *what);    // MOE_OK, or MOE_EHIP with the launch error recorded
+
+// Routing from given logits (select.hip).
+struct SelectArgs {
+    const void *logits;  // [T, E], row stride ld elements, bf16 or fp32
+    const float *bias;   // [E] or null
+    int32_t *idx;        // [T, k]
+    float *w;            // [T, k] or null
+    int64_t ld;
+    int T, E, k, n_group, topk_group, softmax, group_top2, renorm, bf16;
+    float scale;
+};
+void launch_select(const SelectArgs &a, hipStream_t st);
+
+// Rows to E4M3 codes [R, 128 * KB] with scales [R, KB] (block_rows 1) or
+// [R / 128 rounded up, KB] (128) (quant_fp8.hip).
+struct QuantArgs {
+    const void *x;  // [R, K], row stride ld elements, bf16 or fp32
+    uint8_t *codes;
+    float *scales;
+    int64_t ld;
+    int R, K, KB, block_rows, bf16;
+};
+void launch_quant_fp8(const QuantArgs &a, hipStream_t st);
+
+// Products of E4M3 codes with block scales (matmul_fp8.hip).
+constexpr int FP8_MAX_K = 32768;  // K whose weight scales fit the kernels' LDS
+struct Fp8Args {
+    const uint8_t *a;        // [rows, K] codes, row stride lda bytes
+    const float *sa;         // [rows, KB]
+    const int32_t *row_tok;  // row of a (and sa) of each grouped row, or null: the same
+    const uint8_t *b0, *b1;  // [G][N, K] codes (b1: up), row stride ldb, group stride bstride
+    const float *s0, *s1;    // [G][N / 128 rounded up, KB], group stride sstride
+    const int32_t *offsets;  // [G + 1] first row of each group, or null: one group
+    const Tile *tiles;       // row tiles from the permutation, or null: from the offsets
+    const int32_t *ntiles;
+    void *y;                 // plain: [rows, N], row stride ldy elements
+    uint8_t *hq;             // SwiGLU: codes of h [rows, N] and their scales [rows, N / 128]
+    float *hs;
+    int64_t lda, ldb, ldy, bstride, sstride;
+    int M, N, KB, G, mtiles, out_f32, vec;  // vec: rows of y allow 16-byte stores
+};
+int fp8_bm(int64_t rows, int groups);                            // rows of a tile
+int64_t fp8_row_tiles(int64_t rows, int groups, int bm);         // upper bound of the row tiles
+void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st);
+void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st);
 
 // Measurement aids (probe.hip): the device's HBM read (sequential and
 // scattered), MXFP4 dequantisation stream and bf16 MFMA ceilings.

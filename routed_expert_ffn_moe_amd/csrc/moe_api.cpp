@@ -73,8 +73,9 @@ int check_shape(const moe_shape_t *s)
     const bool f32 = s->act_dtype == MOE_F32 && s->w_dtype == MOE_F32;
     const bool bf = s->act_dtype == MOE_BF16 && s->w_dtype == MOE_BF16;
     const bool mx = s->act_dtype == MOE_BF16 && s->w_dtype == MOE_MXFP4;
-    if (!f32 && !bf && !mx) {
-        if ((s->act_dtype < 0 || s->act_dtype > 2) || (s->w_dtype < 0 || s->w_dtype > 2))
+    const bool f8 = s->act_dtype == MOE_BF16 && s->w_dtype == MOE_FP8;
+    if (!f32 && !bf && !mx && !f8) {
+        if ((s->act_dtype < 0 || s->act_dtype > 3) || (s->w_dtype < 0 || s->w_dtype > 3))
             return fail(MOE_EINVAL, "unknown dtype");
         return fail(MOE_EUNSUPPORTED, "unsupported dtype combination");
     }
@@ -84,6 +85,12 @@ int check_shape(const moe_shape_t *s)
         return fail(MOE_EUNSUPPORTED, "MXFP4 supports H and I up to 4096");
     if (mx && s->I_shared)
         return fail(MOE_EUNSUPPORTED, "MXFP4 with a shared expert is not supported");
+    if (f8 && (s->H % 128 || s->I % 128))
+        return fail(MOE_EINVAL, "FP8 needs H and I multiples of 128");
+    if (f8 && (s->H > moe::FP8_MAX_K || s->I > moe::FP8_MAX_K))  // weight scales staged in LDS
+        return fail(MOE_EUNSUPPORTED, "FP8 supports H and I up to 32768");
+    if (f8 && s->I_shared)
+        return fail(MOE_EUNSUPPORTED, "FP8 with a shared expert is not supported");
     return MOE_OK;
 }
 
@@ -99,29 +106,39 @@ int check_pass_size(const moe_shape_t *s, int64_t Tc)
     return MOE_OK;
 }
 
-int check_weights(const moe_shape_t *s, const moe_weights_t *w)
+int check_router(const moe_weights_t *w)
 {
     if (!w)
         return fail(MOE_EINVAL, "weights is NULL");
-    if (!w->router_w || !w->w_gate || !w->w_up || !w->w_down)
-        return fail(MOE_EINVAL, "router or expert weight pointer is NULL");
-    if (!aligned16(w->router_w) || !aligned16(w->w_gate) || !aligned16(w->w_up) ||
-        !aligned16(w->w_down))
-        return fail(MOE_EINVAL, "weight pointer not 16-byte aligned");
+    if (!w->router_w)
+        return fail(MOE_EINVAL, "router weight pointer is NULL");
+    if (!aligned16(w->router_w))
+        return fail(MOE_EINVAL, "router weight pointer not 16-byte aligned");
     if (w->router_bias && ((uintptr_t)w->router_bias & 3u))
         return fail(MOE_EINVAL, "router_bias not 4-byte aligned");
-    // bf16 / MXFP4 kernels read the packed layouts only; f32 ones row-major
-    const int want = s->w_dtype == MOE_F32 ? MOE_LAYOUT_ROWMAJOR : MOE_LAYOUT_PACKED;
-    if (w->layout != want)
-        return fail(MOE_EINVAL, s->w_dtype == MOE_F32
-                                    ? "f32 expert matrices must be row-major (layout ROWMAJOR)"
+    return MOE_OK;
+}
+
+int check_experts(const moe_shape_t *s, const moe_weights_t *w)
+{
+    if (!w)
+        return fail(MOE_EINVAL, "weights is NULL");
+    if (!w->w_gate || !w->w_up || !w->w_down)
+        return fail(MOE_EINVAL, "expert weight pointer is NULL");
+    if (!aligned16(w->w_gate) || !aligned16(w->w_up) || !aligned16(w->w_down))
+        return fail(MOE_EINVAL, "expert weight pointer not 16-byte aligned");
+    // bf16 / MXFP4 kernels read the packed layouts only; f32 and FP8 ones row-major
+    const bool rowmajor = s->w_dtype == MOE_F32 || s->w_dtype == MOE_FP8;
+    if (w->layout != (rowmajor ? MOE_LAYOUT_ROWMAJOR : MOE_LAYOUT_PACKED))
+        return fail(MOE_EINVAL, rowmajor
+                                    ? "f32 and FP8 expert matrices must be row-major (layout ROWMAJOR)"
                                     : "bf16/MXFP4 expert matrices must be packed by moe_pack_bf16 / "
                                       "moe_pack_mxfp4 and declared with layout PACKED");
-    if (s->w_dtype == MOE_MXFP4) {
+    if (s->w_dtype == MOE_MXFP4 || s->w_dtype == MOE_FP8) {
         if (!w->s_gate || !w->s_up || !w->s_down)
-            return fail(MOE_EINVAL, "MXFP4 scale pointer is NULL");
+            return fail(MOE_EINVAL, "MXFP4 / FP8 scale pointer is NULL");
         if (!aligned16(w->s_gate) || !aligned16(w->s_up) || !aligned16(w->s_down))
-            return fail(MOE_EINVAL, "MXFP4 scale pointer not 16-byte aligned");
+            return fail(MOE_EINVAL, "MXFP4 / FP8 scale pointer not 16-byte aligned");
     }
     if (s->I_shared > 0) {
         if (!w->sh_gate || !w->sh_up || !w->sh_down)
@@ -132,10 +149,16 @@ int check_weights(const moe_shape_t *s, const moe_weights_t *w)
     return MOE_OK;
 }
 
+int check_weights(const moe_shape_t *s, const moe_weights_t *w)
+{
+    const int rc = check_router(w);
+    return rc ? rc : check_experts(s, w);
+}
+
 // Workspace layout of one pass of Tc tokens.
 struct Layout {
     size_t logits, wts, blk, counts, offsets, row_src, row_tok, row_of, tiles_gu, ntiles, tiles_dc,
-        items_gu, items_dc, h, stage, xq, total;
+        items_gu, items_dc, h, stage, xq, f8_x, f8_sx, f8_sh, total;
     bool has_xq;  // MXFP4 passes routed by router_small: x quantised once per token
     int max_tiles_gu, max_tiles_dc, bm_gu, bm_dc, ntn_gu, ntn_dc, wrows_gu, wrows_dc;
     int64_t logit_floats;  // capacity of the logits area
@@ -169,8 +192,9 @@ Layout layout(const moe_shape_t *s, int Tc)
 {
     Layout L{};
     const moe::ExpertArgs a = expert_shape(s, Tc);
-    L.bm_gu = moe::gemm_bm_gu(a);
-    L.bm_dc = moe::gemm_bm_dc(a);
+    const bool f8 = s->w_dtype == MOE_FP8;
+    L.bm_gu = f8 ? moe::fp8_bm((int64_t)Tc * s->top_k, s->E) : moe::gemm_bm_gu(a);
+    L.bm_dc = f8 ? L.bm_gu : moe::gemm_bm_dc(a);
     L.max_tiles_gu = max_tiles(Tc, s, L.bm_gu);
     L.max_tiles_dc = max_tiles(Tc, s, L.bm_dc);
     L.ntn_gu = moe::stream_ntn(a, true);
@@ -207,8 +231,13 @@ Layout layout(const moe_shape_t *s, int Tc)
     L.tiles_dc = take((size_t)L.max_tiles_dc * sizeof(moe::Tile));
     L.items_gu = take((size_t)L.max_tiles_gu * L.ntn_gu * 16);
     L.items_dc = take((size_t)L.max_tiles_dc * L.ntn_dc * 16);
-    L.h = take((size_t)rows * ldh * esz);
+    L.h = take((size_t)rows * ldh * (f8 ? 1 : esz));  // FP8: codes, their scales below
     L.stage = take((size_t)rows * s->H * esz);
+    if (f8) {  // the token rows as codes, and the scales of x and h
+        L.f8_x = take((size_t)Tc * s->H);
+        L.f8_sx = take((size_t)Tc * (s->H / moe::FP8_K) * 4);
+        L.f8_sh = take((size_t)rows * (s->I / moe::FP8_K) * 4);
+    }
     // decode, verify and other short passes with MXFP4 experts
     const int act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;
     // The router quantising x once for all expert kernels is off unless
@@ -290,6 +319,39 @@ int launched(const char *what)
     return MOE_OK;
 }
 
+// Arguments of the permutation of one pass of n tokens.
+moe::PermuteArgs permute_args(const moe_shape_t *s, int n, const int32_t *idx, char *ws,
+                              const Layout &L)
+{
+    moe::PermuteArgs p{};
+    p.idx = idx;
+    p.blk = (int32_t *)(ws + L.blk);
+    p.counts = (int32_t *)(ws + L.counts);
+    p.offsets = (int32_t *)(ws + L.offsets);
+    p.row_src = (int32_t *)(ws + L.row_src);
+    p.row_tok = (int32_t *)(ws + L.row_tok);
+    p.row_of = (int32_t *)(ws + L.row_of);
+    p.tiles_a = (moe::Tile *)(ws + L.tiles_gu);
+    p.ntiles_a = (int32_t *)(ws + L.ntiles);
+    p.tiles_b = (moe::Tile *)(ws + L.tiles_dc);
+    p.ntiles_b = (int32_t *)(ws + L.ntiles) + 1;
+    p.bm_a = L.bm_gu;
+    p.bm_b = L.bm_dc;
+    p.items_a = L.ntn_gu ? (int4 *)(ws + L.items_gu) : nullptr;
+    p.items_b = L.ntn_dc ? (int4 *)(ws + L.items_dc) : nullptr;
+    p.ntn_a = L.ntn_gu;
+    p.ntn_b = L.ntn_dc;
+    p.max_tiles_a = L.max_tiles_gu;
+    p.max_tiles_b = L.max_tiles_dc;
+    p.wrows_a = L.wrows_gu;
+    p.wrows_b = L.wrows_dc;
+    p.T = n;
+    p.E = s->E;
+    p.k = s->top_k;
+    p.shared = s->I_shared > 0;
+    return p;
+}
+
 // Router and permutation of one pass.
 int route_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, int Tc,
                int32_t *idx, float *wts, char *ws, const Layout &L, hipStream_t st)
@@ -330,33 +392,8 @@ int route_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, int 
     int rc = launched("router");
     if (rc)
         return rc;
-    moe::PermuteArgs p{};
-    p.idx = idx;
-    p.blk = (int32_t *)(ws + L.blk);
-    p.counts = (int32_t *)(ws + L.counts);
-    p.offsets = (int32_t *)(ws + L.offsets);
-    p.row_src = (int32_t *)(ws + L.row_src);
-    p.row_tok = (int32_t *)(ws + L.row_tok);
-    p.row_of = (int32_t *)(ws + L.row_of);
-    p.tiles_a = (moe::Tile *)(ws + L.tiles_gu);
-    p.ntiles_a = (int32_t *)(ws + L.ntiles);
-    p.tiles_b = (moe::Tile *)(ws + L.tiles_dc);
-    p.ntiles_b = (int32_t *)(ws + L.ntiles) + 1;
-    p.bm_a = L.bm_gu;
-    p.bm_b = L.bm_dc;
-    p.items_a = L.ntn_gu ? (int4 *)(ws + L.items_gu) : nullptr;
-    p.items_b = L.ntn_dc ? (int4 *)(ws + L.items_dc) : nullptr;
+    moe::PermuteArgs p = permute_args(s, Tc, idx, ws, L);
     p.hist_done = seg ? 1 : 0;
-    p.ntn_a = L.ntn_gu;
-    p.ntn_b = L.ntn_dc;
-    p.max_tiles_a = L.max_tiles_gu;
-    p.max_tiles_b = L.max_tiles_dc;
-    p.wrows_a = L.wrows_gu;
-    p.wrows_b = L.wrows_dc;
-    p.T = Tc;
-    p.E = s->E;
-    p.k = s->top_k;
-    p.shared = s->I_shared > 0;
     if (small) {
         StageScope sc(1, st);  // top-k and the permutation
         moe::launch_route_small(r, p, st);
@@ -367,9 +404,166 @@ int route_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, int 
     return launched("permute");
 }
 
+// The FP8 experts' two products of one permuted pass: x as codes, gate and up
+// with h as codes, and down into the staging rows.
+int fp8_products(const moe_shape_t *s, const moe_weights_t *w, const void *x, int n, char *ws,
+                 const Layout &L, hipStream_t st)
+{
+    const int KB = s->H / moe::FP8_K, IB = s->I / moe::FP8_K;
+    int rc;
+    {
+        StageScope sc(2, st);
+        moe::QuantArgs q{};
+        q.x = x;
+        q.codes = (uint8_t *)(ws + L.f8_x);
+        q.scales = (float *)(ws + L.f8_sx);
+        q.ld = q.K = s->H;
+        q.R = n;
+        q.KB = KB;
+        q.block_rows = 1;
+        q.bf16 = 1;
+        moe::launch_quant_fp8(q, st);
+        if ((rc = launched("quant_fp8")))
+            return rc;
+        moe::Fp8Args g{};
+        g.a = q.codes;
+        g.sa = q.scales;
+        g.row_tok = (const int32_t *)(ws + L.row_tok);
+        g.b0 = (const uint8_t *)w->w_gate;
+        g.b1 = (const uint8_t *)w->w_up;
+        g.s0 = (const float *)w->s_gate;
+        g.s1 = (const float *)w->s_up;
+        g.offsets = (const int32_t *)(ws + L.offsets);
+        g.tiles = (const moe::Tile *)(ws + L.tiles_gu);
+        g.ntiles = (const int32_t *)(ws + L.ntiles);
+        g.hq = (uint8_t *)(ws + L.h);
+        g.hs = (float *)(ws + L.f8_sh);
+        g.lda = g.ldb = s->H;
+        g.bstride = (int64_t)s->I * s->H;
+        g.sstride = (int64_t)IB * KB;
+        g.M = n * s->top_k;
+        g.N = s->I;
+        g.KB = KB;
+        g.G = s->E;
+        g.mtiles = L.max_tiles_gu;
+        moe::launch_fp8_gate_up(g, L.bm_gu, st);
+        if ((rc = launched("gate_up")))
+            return rc;
+    }
+    StageScope sc(3, st);
+    moe::Fp8Args d{};
+    d.a = (const uint8_t *)(ws + L.h);
+    d.sa = (const float *)(ws + L.f8_sh);
+    d.b0 = (const uint8_t *)w->w_down;
+    d.s0 = (const float *)w->s_down;
+    d.offsets = (const int32_t *)(ws + L.offsets);
+    d.tiles = (const moe::Tile *)(ws + L.tiles_dc);
+    d.ntiles = (const int32_t *)(ws + L.ntiles) + 1;
+    d.y = ws + L.stage;
+    d.lda = d.ldb = s->I;
+    d.ldy = s->H;
+    d.bstride = (int64_t)s->H * s->I;
+    d.sstride = (int64_t)KB * IB;
+    d.M = n * s->top_k;
+    d.N = s->H;
+    d.KB = IB;
+    d.G = s->E;
+    d.mtiles = L.max_tiles_dc;
+    d.vec = 1;
+    moe::launch_fp8_matmul(d, L.bm_dc, st);
+    return launched("down");
+}
+
+// The experts of one permuted pass (Tc: tokens of a full pass) and the combine.
+// With `given` the routing is the caller's, whose slots may be empty.
+int expert_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, void *y, int n, int Tc,
+                const int32_t *idx, const float *wts, char *ws, const Layout &L, bool given,
+                hipStream_t st)
+{
+    int rc;
+    if (s->w_dtype == MOE_FP8) {
+        if ((rc = fp8_products(s, w, x, n, ws, L, st)))
+            return rc;
+    } else {
+        moe::ExpertArgs a = expert_shape(s, n);
+        a.shape_T = Tc;
+        a.x = x;
+        // rows quantised by the short-pass router (route_pass set them up)
+        a.xq = !given && L.has_xq && moe::route_small_ok(n, s->top_k, s->E, s->H, a.act)
+                   ? (const uint8_t *)(ws + L.xq)
+                   : nullptr;
+        a.w_gate = w->w_gate;
+        a.w_up = w->w_up;
+        a.w_down = w->w_down;
+        a.s_gate = w->s_gate;
+        a.s_up = w->s_up;
+        a.s_down = w->s_down;
+        a.sh_gate = w->sh_gate;
+        a.sh_up = w->sh_up;
+        a.sh_down = w->sh_down;
+        a.row_src = (const int32_t *)(ws + L.row_src);
+        a.row_tok = (const int32_t *)(ws + L.row_tok);
+        a.offsets = (const int32_t *)(ws + L.offsets);
+        a.topk_w = wts;
+        a.h = ws + L.h;
+        a.stage = ws + L.stage;
+        a.tiles_gu = (const moe::Tile *)(ws + L.tiles_gu);
+        a.ntiles_gu = (const int32_t *)(ws + L.ntiles);
+        a.tiles_dc = (const moe::Tile *)(ws + L.tiles_dc);
+        a.items_gu = (const int4 *)(ws + L.items_gu);
+        a.items_dc = (const int4 *)(ws + L.items_dc);
+        a.ntiles_dc = (const int32_t *)(ws + L.ntiles) + 1;
+        a.topk_idx = idx;
+        a.row_of = (const int32_t *)(ws + L.row_of);
+        a.y = y;
+        a.max_tiles_gu = L.max_tiles_gu;
+        a.max_tiles_dc = L.max_tiles_dc;
+        {
+            StageScope sc(2, st);
+            moe::launch_gate_up(a, st);
+        }
+        if ((rc = launched("gate_up")))
+            return rc;
+        // decode rows: y straight from the down kernel (which reads every slot)
+        if (!given && moe::down_combine_mxfp4_ok(a)) {
+            {
+                StageScope sc(3, st);
+                moe::launch_down_combine_mxfp4(a, st);
+            }
+            return launched("down");
+        }
+        {
+            StageScope sc(3, st);
+            moe::launch_down(a, st);
+        }
+        if ((rc = launched("down")))
+            return rc;
+    }
+    moe::CombineArgs cb{};
+    cb.stage = ws + L.stage;
+    cb.row_of = (const int32_t *)(ws + L.row_of);
+    cb.topk_w = wts;
+    cb.y = y;
+    cb.T = n;
+    cb.H = s->H;
+    cb.k = s->top_k;
+    cb.shared = s->I_shared > 0;
+    cb.act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;
+    {
+        StageScope sc(4, st);
+        if (given)
+            moe::launch_combine_given(cb, st);
+        else
+            moe::launch_combine(cb, st);
+    }
+    return launched("combine");
+}
+
 }  // namespace
 
 int moe::api_fail(int code, const char *what) { return fail(code, what); }
+int moe::api_check_device() { return check_device(); }
+int moe::api_launched(const char *what) { return launched(what); }
 
 extern "C" {
 
@@ -485,75 +679,7 @@ int moe_forward(const moe_shape_t *s, const moe_weights_t *w, const void *x, voi
         rc = route_pass(s, w, xc, n, idx, wts, wsb, Lw, st);
         if (rc)
             return rc;
-        moe::ExpertArgs a = expert_shape(s, n);
-        a.shape_T = Tc;
-        a.x = xc;
-        // rows quantised by the short-pass router (route_pass set them up)
-        a.xq = Lw.has_xq && moe::route_small_ok(n, s->top_k, s->E, s->H, a.act)
-                   ? (const uint8_t *)(wsb + Lw.xq)
-                   : nullptr;
-        a.w_gate = w->w_gate;
-        a.w_up = w->w_up;
-        a.w_down = w->w_down;
-        a.s_gate = w->s_gate;
-        a.s_up = w->s_up;
-        a.s_down = w->s_down;
-        a.sh_gate = w->sh_gate;
-        a.sh_up = w->sh_up;
-        a.sh_down = w->sh_down;
-        a.row_src = (const int32_t *)(wsb + Lw.row_src);
-        a.row_tok = (const int32_t *)(wsb + Lw.row_tok);
-        a.offsets = (const int32_t *)(wsb + Lw.offsets);
-        a.topk_w = wts;
-        a.h = wsb + Lw.h;
-        a.stage = wsb + Lw.stage;
-        a.tiles_gu = (const moe::Tile *)(wsb + Lw.tiles_gu);
-        a.ntiles_gu = (const int32_t *)(wsb + Lw.ntiles);
-        a.tiles_dc = (const moe::Tile *)(wsb + Lw.tiles_dc);
-        a.items_gu = (const int4 *)(wsb + Lw.items_gu);
-        a.items_dc = (const int4 *)(wsb + Lw.items_dc);
-        a.ntiles_dc = (const int32_t *)(wsb + Lw.ntiles) + 1;
-        a.topk_idx = idx;
-        a.row_of = (const int32_t *)(wsb + Lw.row_of);
-        a.y = yc;
-        a.max_tiles_gu = Lw.max_tiles_gu;
-        a.max_tiles_dc = Lw.max_tiles_dc;
-        {
-            StageScope sc(2, st);
-            moe::launch_gate_up(a, st);
-        }
-        if ((rc = launched("gate_up")))
-            return rc;
-        if (moe::down_combine_mxfp4_ok(a)) {  // decode rows: y straight from the down kernel
-            {
-                StageScope sc(3, st);
-                moe::launch_down_combine_mxfp4(a, st);
-            }
-            if ((rc = launched("down")))
-                return rc;
-            continue;
-        }
-        {
-            StageScope sc(3, st);
-            moe::launch_down(a, st);
-        }
-        if ((rc = launched("down")))
-            return rc;
-        moe::CombineArgs cb{};
-        cb.stage = wsb + Lw.stage;
-        cb.row_of = (const int32_t *)(wsb + Lw.row_of);
-        cb.topk_w = wts;
-        cb.y = yc;
-        cb.T = n;
-        cb.H = s->H;
-        cb.k = s->top_k;
-        cb.shared = s->I_shared > 0;
-        cb.act = a.act;
-        {
-            StageScope sc(4, st);
-            moe::launch_combine(cb, st);
-        }
-        if ((rc = launched("combine")))
+        if ((rc = expert_pass(s, w, xc, yc, n, Tc, idx, wts, wsb, Lw, false, st)))
             return rc;
     }
     return MOE_OK;
@@ -603,6 +729,99 @@ int moe_route(const moe_shape_t *s, const moe_weights_t *w, const void *x, int32
     if (row_src && hipMemcpyAsync(row_src, wsb + L.row_src, (size_t)pairs * 4,
                                   hipMemcpyDeviceToDevice, st) != hipSuccess)
         return launched("copy row_src");
+    return MOE_OK;
+}
+
+int moe_logits(const moe_shape_t *s, const moe_weights_t *w, const void *x, float *logits,
+               void *stream)
+{
+    int rc = check_shape(s);
+    if (rc)
+        return rc;
+    if ((rc = check_router(w)))
+        return rc;
+    if (s->T == 0)
+        return MOE_OK;
+    if (!x || !logits)
+        return fail(MOE_EINVAL, "x or logits is NULL");
+    if (!aligned16(x) || !aligned16(logits))
+        return fail(MOE_EINVAL, "x or logits not 16-byte aligned");
+    if ((rc = check_pass_size(s, s->T)))
+        return rc;
+    if ((rc = check_device()))
+        return rc;
+    moe::RouterArgs r{};
+    r.x = x;
+    r.wr = w->router_w;
+    r.bias = w->router_bias;
+    r.logits = logits;
+    r.T = s->T;
+    r.H = s->H;
+    r.E = s->E;
+    r.k = s->top_k;
+    r.act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;
+    r.nparts = 1;
+    hipStream_t st = (hipStream_t)stream;
+    if (moe::route_small_ok(s->T, s->top_k, s->E, s->H, r.act))
+        moe::launch_router_small(r, st);
+    else
+        moe::launch_router_logits(r, st);
+    return launched("logits");
+}
+
+int moe_experts(const moe_shape_t *s, const moe_weights_t *w, const void *x,
+                const int32_t *topk_idx, const float *topk_w, void *y, void *ws, size_t ws_bytes,
+                void *stream)
+{
+    int rc = check_shape(s);
+    if (rc)
+        return rc;
+    if (s->I_shared > 0)
+        return fail(MOE_EUNSUPPORTED, "moe_experts runs the routed experts only: I_shared must be 0");
+    if ((rc = check_experts(s, w)))
+        return rc;
+    if (s->T == 0)
+        return MOE_OK;
+    if (!x || !y || !topk_idx || !topk_w)
+        return fail(MOE_EINVAL, "x, y, topk_idx or topk_w is NULL");
+    if (!aligned16(x) || !aligned16(y) || ((uintptr_t)topk_idx & 3u) || ((uintptr_t)topk_w & 3u))
+        return fail(MOE_EINVAL, "x or y not 16-byte, topk_idx or topk_w not 4-byte aligned");
+    const int Tc = pass_tokens(s);
+    if ((rc = check_pass_size(s, Tc)))
+        return rc;
+    const Layout L = layout(s, Tc);
+    if (!ws || ((uintptr_t)ws & 255u))
+        return fail(MOE_EINVAL, "workspace NULL or not 256-byte aligned");
+    if (ws_bytes < L.total)
+        return fail(MOE_EWORKSPACE, "workspace too small");
+    if ((rc = check_device()))
+        return rc;
+    hipStream_t st = (hipStream_t)stream;
+    char *wsb = (char *)ws;
+    const int64_t esz = s->act_dtype == MOE_F32 ? 4 : 2;
+    std::unique_lock<std::mutex> tlock(g_timing.mu, std::defer_lock);
+    if (g_timing.on) {
+        tlock.lock();
+        g_timing.calls++;
+    }
+    for (int c0 = 0; c0 < s->T; c0 += Tc) {
+        const int n = std::min(Tc, s->T - c0);
+        const char *xc = (const char *)x + (int64_t)c0 * s->H * esz;
+        char *yc = (char *)y + (int64_t)c0 * s->H * esz;
+        const int32_t *idx = topk_idx + (int64_t)c0 * s->top_k;
+        const float *wts = topk_w + (int64_t)c0 * s->top_k;
+        Layout Lw = L;
+        Lw.max_tiles_gu = max_tiles(n, s, L.bm_gu);
+        Lw.max_tiles_dc = max_tiles(n, s, L.bm_dc);
+        {
+            StageScope sc(1, st);
+            moe::launch_permute(permute_args(s, n, idx, wsb, Lw), st);
+        }
+        if ((rc = launched("permute")))
+            return rc;
+        if ((rc = expert_pass(s, w, xc, yc, n, Tc, idx, wts, wsb, Lw, true, st)))
+            return rc;
+    }
     return MOE_OK;
 }
 

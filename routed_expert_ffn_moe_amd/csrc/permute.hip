@@ -35,6 +35,14 @@ __device__ __forceinline__ void wave_lds_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
+// Expert of pair p, or -1 if its slot is empty (an index outside 0..E-1: given
+// routing may leave slots empty) or p is behind the last pair.
+__device__ __forceinline__ int pair_expert(const int32_t *__restrict__ idx, int p, int n_pairs, int E)
+{
+    const int e = p < n_pairs ? idx[p] : -1;
+    return (unsigned)e < (unsigned)E ? e : -1;
+}
+
 int permute_blocks(int n_pairs)
 {
     return (n_pairs + PAIRS_PER_BLOCK - 1) / PAIRS_PER_BLOCK;
@@ -51,10 +59,9 @@ __global__ __launch_bounds__(256) void permute_hist(const int32_t *__restrict__ 
     const int base = blockIdx.x * PAIRS_PER_BLOCK;
     for (int i = threadIdx.x; i < PAIRS_PER_BLOCK; i += 256) {
         int p = base + i;
-        if (p < n_pairs) {
-            int e = idx[p];
+        const int e = pair_expert(idx, p, n_pairs, E);
+        if (e >= 0)
             atomicAdd(&cnt[e], 1);
-        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 256)
@@ -112,7 +119,7 @@ __device__ __forceinline__ void scan_groups(
 #pragma unroll
             for (int i = 0; i < PB; ++i) {
                 const int p = p0 + 1024 * i;
-                ev[i] = p < n_pairs ? idx[p] : -1;
+                ev[i] = pair_expert(idx, p, n_pairs, E);
             }
 #pragma unroll
             for (int i = 0; i < PB; ++i)
@@ -292,7 +299,7 @@ __device__ __forceinline__ void place_block(const int32_t *__restrict__ idx,
     __shared__ int32_t s_wsum[16];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int p = b * PAIRS_PER_BLOCK + tid;
-    const int e = p < n_pairs ? idx[p] : -1;
+    const int e = pair_expert(idx, p, n_pairs, E);
     constexpr int SCH = 16;
     // column sums over all blocks (the expert's rows) and over those before b
     int tot = 0, pre = 0;
@@ -351,6 +358,8 @@ __device__ __forceinline__ void place_block(const int32_t *__restrict__ idx,
         row_src[pos] = p;
         row_tok[pos] = p / k;
         row_of[p] = pos;
+    } else if (p < n_pairs) {
+        row_of[p] = -1;
     }
     // shared-expert rows follow the routed ones, in token order
     if (shared && b == 0) {
@@ -405,7 +414,7 @@ __global__ __launch_bounds__(256) void permute_scatter(const int32_t *__restrict
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         const int p = base + 64 * i + lane;
-        ev[i] = p < n_pairs ? idx[p] : -1;
+        ev[i] = pair_expert(idx, p, n_pairs, E);
     }
     for (int i = threadIdx.x; i < 4 * E; i += 256)
         run[i] = 0;
@@ -449,6 +458,8 @@ __global__ __launch_bounds__(256) void permute_scatter(const int32_t *__restrict
             row_of[p] = pos;
             if (rank == 0)
                 wrun[e] += __popcll(match);
+        } else if (p < n_pairs) {
+            row_of[p] = -1;
         }
         wave_lds_sync();
     }
