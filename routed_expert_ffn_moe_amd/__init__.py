@@ -272,78 +272,130 @@ def make_matmul(M, N, K, G=1, out="bf16", lda=0, ldb=0, ldy=0) -> moe_matmul_t:
     return moe_matmul_t(M, N, K, G, _DT[out], lda, ldb, ldy)
 
 
-def _dev(t, what: str, elems: int, *dtypes: str) -> Optional[int]:
-    """Device pointer of a tensor of the operators below (None -> NULL),
-    after checking its type, its device (the current one) and that it holds
-    `elems` elements from its pointer on: a strided view is given with its
-    row stride, and what it spans counts."""
+# The operators below check what they are given (these calls are short: the
+# ordinary tensor is passed after four comparisons).
+
+def _types():
+    """Element types by moe_dtype_t, once torch is there (load() imports it)."""
+    global _SRC, _F32, _I32, _CODES
+    import torch
+    _SRC = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16,)}
+    _F32, _I32 = (torch.float32,), (torch.int32,)
+    _CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+_SRC = _F32 = _I32 = _CODES = None
+_device = _raw_stream = None
+
+
+def _begin(stream):
+    """(library, current device, stream handle) of a call."""
+    global _device, _raw_stream
+    lib = _lib
+    if lib is None:
+        lib = load()
+    if _device is None:
+        import torch
+        _types()
+        _device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -1
+        # the current stream's handle without building a Stream object
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    dev = _device()
+    if stream is None:
+        if dev < 0:
+            return lib, dev, None
+        return lib, dev, _raw_stream(dev) if _raw_stream else _stream(None)
+    return lib, dev, _stream(stream)
+
+
+def _mat(t, what, rows, cols, ld, types, dev) -> Optional[int]:
+    """Device pointer of a tensor that a call reads or writes as `rows` rows
+    of `cols` elements, `ld` apart (None -> NULL): of one of `types`, on the
+    current device, and laid out so - dense, or 2-D with that row stride."""
     if t is None:
         return None
-    if str(t.dtype)[6:] not in dtypes:
-        raise ValueError("%s: dtype %s, expected %s" % (what, t.dtype, " or ".join(dtypes)))
+    if t.dtype in types and t.get_device() == dev and ld == cols and t.is_contiguous() and \
+            t.numel() == rows * cols and dev >= 0:
+        return t.data_ptr()
+    return _mat_checked(t, what, rows, cols, ld, types, dev)
+
+
+def _mat_checked(t, what, rows, cols, ld, types, dev):
+    if t.dtype not in types:
+        raise ValueError("%s: dtype %s, expected %s" % (what, t.dtype, " or ".join(map(str, types))))
     if not t.is_cuda:
         raise ValueError("%s is not on a GPU" % what)
-    import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s is on cuda:%d, the current device is cuda:%d"
-                         % (what, t.get_device(), torch.cuda.current_device()))
-    held = t.numel() if t.is_contiguous() else \
-        1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else 0
-    if held < elems:
-        raise ValueError("%s spans %d elements, the call needs %d" % (what, held, elems))
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (what, t.get_device(), dev))
+    if rows <= 0 or cols <= 0:
+        return t.data_ptr()
+    need = (rows - 1) * ld + cols
+    if t.dim() == 2 and rows > 1:
+        # also a wider or longer tensor whose rows begin where the call's do
+        ok = t.stride(0) == ld and (t.stride(1) == 1 or t.shape[1] == 1) and t.shape[1] >= cols
+        held = t.stride(0) * (t.shape[0] - 1) + t.shape[1]
+    else:
+        ok = t.is_contiguous() or (t.dim() == 2 and t.stride(1) == 1)
+        held = t.numel()
+    if not ok:
+        raise ValueError("%s: strides %s, the call takes rows of %d elements, %d apart"
+                         % (what, tuple(t.stride()), cols, ld))
+    if held < need:
+        raise ValueError("%s holds %d elements, the call needs %d" % (what, held, need))
     return t.data_ptr()
-
-
-_SRC = {MOE_F32: "float32", MOE_BF16: "bfloat16"}
-_CODES = ("float8_e4m3fn", "uint8")
-
-
-def _span(rows: int, ld: int, cols: int) -> int:
-    return (rows - 1) * ld + cols if rows > 0 else 0
 
 
 def moe_logits(shape, weights, x, logits, stream=None) -> None:
     """The router's logits [T, E] (float32) of x[T, H]."""
-    src = _SRC.get(shape.act_dtype, "bfloat16")
-    _check(load().moe_logits(ctypes.byref(shape), ctypes.byref(weights.c),
-                             _dev(x, "x", shape.T * shape.H, src),
-                             _dev(logits, "logits", shape.T * shape.E, "float32"), _stream(stream)))
+    lib, dev, st = _begin(stream)
+    s = shape
+    _check(lib.moe_logits(ctypes.byref(s), ctypes.byref(weights.c),
+                          _mat(x, "x", s.T, s.H, s.H, _SRC.get(s.act_dtype, _CODES), dev),
+                          _mat(logits, "logits", s.T, s.E, s.E, _F32, dev), st))
 
 
 def moe_select(select, logits, bias, topk_idx, topk_w, stream=None) -> None:
     """topk_idx, topk_w [T, top_k] of the tokens with these logits (see include/moe.h)."""
+    lib, dev, st = _begin(stream)
     s = select
-    n = s.T * s.top_k
-    _check(load().moe_select(ctypes.byref(s),
-                             _dev(logits, "logits", _span(s.T, s.ld or s.E, s.E),
-                                  _SRC.get(s.logit_dtype, "float32")),
-                             _dev(bias, "bias", s.E, "float32"),
-                             _dev(topk_idx, "topk_idx", n, "int32"),
-                             _dev(topk_w, "topk_w", n, "float32"), _stream(stream)))
+    T, E, k = s.T, s.E, s.top_k
+    rc = lib.moe_select(ctypes.byref(s),
+                        _mat(logits, "logits", T, E, s.ld or E, _SRC.get(s.logit_dtype, _F32), dev),
+                        _mat(bias, "bias", 1, E, E, _F32, dev),
+                        _mat(topk_idx, "topk_idx", T, k, k, _I32, dev),
+                        _mat(topk_w, "topk_w", T, k, k, _F32, dev), st)
+    if rc:
+        _check(rc)
 
 
 def moe_experts(shape, weights, x, topk_idx, topk_w, y, ws, ws_bytes=None, stream=None) -> None:
     """y[T, H] of the routed experts with given routing (see include/moe.h)."""
+    lib, dev, st = _begin(stream)
+    s = shape
+    T, H, k = s.T, s.H, s.top_k
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    src = _SRC.get(shape.act_dtype, "bfloat16")
-    n, m = shape.T * shape.H, shape.T * shape.top_k
-    _check(load().moe_experts(ctypes.byref(shape), ctypes.byref(weights.c), _dev(x, "x", n, src),
-                              _dev(topk_idx, "topk_idx", m, "int32"),
-                              _dev(topk_w, "topk_w", m, "float32"), _dev(y, "y", n, src), _ptr(ws),
-                              ws_bytes, _stream(stream)))
+    src = _SRC.get(s.act_dtype, _CODES)
+    rc = lib.moe_experts(ctypes.byref(s), ctypes.byref(weights.c), _mat(x, "x", T, H, H, src, dev),
+                         _mat(topk_idx, "topk_idx", T, k, k, _I32, dev),
+                         _mat(topk_w, "topk_w", T, k, k, _F32, dev), _mat(y, "y", T, H, H, src, dev),
+                         _ptr(ws), ws_bytes, st)
+    if rc:
+        _check(rc)
 
 
 def moe_quant_fp8(quant, x, codes, scales, stream=None) -> None:
     """E4M3 codes [R, Kp] and their float32 block scales of x[R, K] (see include/moe.h)."""
+    lib, dev, st = _begin(stream)
     q = quant
-    kb = -(-q.K // 128)
-    _check(load().moe_quant_fp8(ctypes.byref(q),
-                                _dev(x, "x", _span(q.R, q.ld or q.K, q.K),
-                                     _SRC.get(q.src_dtype, "bfloat16")),
-                                _dev(codes, "codes", q.R * kb * 128, *_CODES),
-                                _dev(scales, "scales", -(-q.R // max(1, q.block_rows)) * kb, "float32"),
-                                _stream(stream)))
+    R, K = q.R, q.K
+    kb = -(-K // 128)
+    rc = lib.moe_quant_fp8(ctypes.byref(q),
+                           _mat(x, "x", R, K, q.ld or K, _SRC.get(q.src_dtype, _CODES), dev),
+                           _mat(codes, "codes", R, kb * 128, kb * 128, _CODES, dev),
+                           _mat(scales, "scales", -(-R // max(1, q.block_rows)), kb, kb, _F32, dev), st)
+    if rc:
+        _check(rc)
 
 
 def quant_fp8(x, block_rows=1, stream=None):
@@ -359,7 +411,7 @@ def quant_fp8(x, block_rows=1, stream=None):
     kb = -(-K // 128)
     codes = torch.empty(*lead, kb * 128, dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty(*lead[:-1], -(-lead[-1] // block_rows), kb, dtype=torch.float32, device=x.device)
-    src = {v: k for k, v in _SRC.items()}.get(str(x.dtype)[6:], -1)
+    src = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(x.dtype, -1)
     moe_quant_fp8(moe_quant_t(R, K, block_rows, src, x.stride(0) if x.dim() == 2 and R > 1 else 0), x,
                   codes, scales, stream)
     return codes, scales
@@ -368,17 +420,19 @@ def quant_fp8(x, block_rows=1, stream=None):
 def moe_matmul_fp8(matmul, a, sa, b, sb, y, offsets=None, stream=None) -> None:
     """y[M, N] of the codes a[M, Kp] and b[G, N, Kp] with their block scales
     (see include/moe.h); the rows of a are split among the b by `offsets`."""
+    lib, dev, st = _begin(stream)
     m = matmul
+    M, N, G = m.M, m.N, m.G
     kb = -(-m.K // 128)
     kp = kb * 128
-    _check(load().moe_matmul_fp8(ctypes.byref(m),
-                                 _dev(a, "a", _span(m.M, m.lda or kp, kp), *_CODES),
-                                 _dev(sa, "sa", m.M * kb, "float32"),
-                                 _dev(b, "b", _span(m.G * m.N, m.ldb or kp, kp), *_CODES),
-                                 _dev(sb, "sb", m.G * -(-m.N // 128) * kb, "float32"),
-                                 _dev(offsets, "offsets", m.G + 1, "int32"),
-                                 _dev(y, "y", _span(m.M, m.ldy or m.N, m.N),
-                                      _SRC.get(m.out_dtype, "bfloat16")), _stream(stream)))
+    rc = lib.moe_matmul_fp8(ctypes.byref(m), _mat(a, "a", M, kp, m.lda or kp, _CODES, dev),
+                            _mat(sa, "sa", M, kb, kb, _F32, dev),
+                            _mat(b, "b", G * N, kp, m.ldb or kp, _CODES, dev),
+                            _mat(sb, "sb", G * -(-N // 128), kb, kb, _F32, dev),
+                            _mat(offsets, "offsets", 1, G + 1, G + 1, _I32, dev),
+                            _mat(y, "y", M, N, m.ldy or N, _SRC.get(m.out_dtype, _CODES), dev), st)
+    if rc:
+        _check(rc)
 
 
 STAGES = ("router", "permute", "gate_up", "down", "combine")

@@ -12,6 +12,14 @@ constexpr int FP8_BLOCK = FP8_K;              // elements of K under one scale
 constexpr float FP8_MAX = 448.0f;             // largest E4M3 value
 constexpr float FP8_TINY = 7.888609e-31f;     // 2^-100, smallest block maximum a scale is made from
 
+// Two values rounded to bf16 (to nearest even, by the conversion instruction).
+__device__ __forceinline__ uint32_t cvt_bf2(float a, float b)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf16x2));
+}
+
 // Divisor of one block: codes are round-to-nearest-even of 448 x / top.  The
 // product by 448 comes first and the quotient is refined to the correctly
 // rounded one for every quotient that fp32 can hold (one residual step on
@@ -80,16 +88,20 @@ __device__ __forceinline__ float row16_max(float v)
 // bits of mantissa, take the FP8 instruction, and fp32 results the bf16 one on
 // the same codes: every product is exact there and the sum is fp32's, at half
 // the rate.
+typedef intx8 Fp8Raw;  // the codes as they are read: one register tuple, as the instruction takes it
+
+__device__ __forceinline__ Fp8Raw fp8_raw(uint4 lo, uint4 hi)
+{
+    return Fp8Raw{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
 template <bool EXACT>
 struct Fp8Frag;
 
 template <>
 struct Fp8Frag<false> {
     intx8 v;
-    __device__ __forceinline__ void set(uint4 lo, uint4 hi)
-    {
-        v = intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-    }
+    __device__ __forceinline__ Fp8Frag(Fp8Raw r) : v(r) {}
 };
 
 __device__ __forceinline__ floatx4 mfma_fp8(const Fp8Frag<false> &a, const Fp8Frag<false> &b)
@@ -100,18 +112,17 @@ __device__ __forceinline__ floatx4 mfma_fp8(const Fp8Frag<false> &a, const Fp8Fr
 template <>
 struct Fp8Frag<true> {
     bf16x8 v[4];
-    __device__ __forceinline__ void set(uint4 lo, uint4 hi)
+    __device__ __forceinline__ Fp8Frag(Fp8Raw w)
     {
         typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * q + j], 1.0f, false);
-                const bf16x2 r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * q + j], 1.0f, true);
+                const bf16x2 u = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * q + j], 1.0f, true);
                 v[q][4 * j] = p[0], v[q][4 * j + 1] = p[1];
-                v[q][4 * j + 2] = r[0], v[q][4 * j + 3] = r[1];
+                v[q][4 * j + 2] = u[0], v[q][4 * j + 3] = u[1];
             }
     }
 };
@@ -155,6 +166,13 @@ __device__ __forceinline__ void dma_wait_barrier()
 {
     static_assert(N >= 0 && N < 64, "the counter holds 6 bits");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Waits for this wave's LDS operations, then for the workgroup; copies and
+// loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void *p)

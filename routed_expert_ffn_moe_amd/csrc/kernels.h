@@ -208,7 +208,7 @@ struct Fp8Args {
     int64_t lda, ldb, ldy, bstride, sstride;
     int M, N, KB, G, mtiles, out_f32, vec;  // vec: rows of y allow 16-byte stores
 };
-int fp8_bm(int64_t rows, int groups);                            // rows of a tile
+int fp8_bm(int64_t rows, int groups, int64_t cols);              // rows of a tile
 int64_t fp8_row_tiles(int64_t rows, int groups, int bm);         // upper bound of the row tiles
 void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st);
 void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st);

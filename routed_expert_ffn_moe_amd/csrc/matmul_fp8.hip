@@ -13,13 +13,22 @@
 // lane then holds one row of y, whose scale is one register, and adjacent
 // columns, which it stores as whole words.
 //
-// A workgroup of WN x WM waves owns BR = 16 * NBW * WN weight rows and BM = 16 *
-// MB * WM rows of a.  Both operands go to LDS by asynchronous copies (row-major
-// rows of 128 bytes are whole cache lines, so the weights need no packing),
-// ST stages deep; a stage also holds the rows' scales.  In LDS the 16-byte
-// pieces of a row are rotated (XOR) by the row, so that the 16 rows a fragment
-// read touches fall on distinct banks, and the weight rows lie in the order
-// in which a lane's results come out adjacent.
+// A workgroup of WN x WM waves owns BR = 16 * NBW * WN weight rows and BM rows of
+// a.  Both operands go to LDS by asynchronous copies (row-major rows of 128
+// bytes are whole cache lines, so the weights need no packing; the pattern
+// alone streams 6.1 TB/s), ST stages of 128 K deep.  In LDS the 16-byte pieces
+// of a row are rotated (XOR) by the row, so that the 16 rows a fragment read
+// touches fall on distinct banks (no conflicts counted), and the weight rows
+// lie in the order in which a lane's results come out adjacent.  The rows'
+// scales are copied a few blocks of K at a time: one 4-byte copy per row and
+// block fetched as many cache lines as the weights themselves.
+//
+// Bound by memory where groups have few rows (the copies alone take 85% of the
+// time of the 128-row experts' gate+up), by the matrix cores and the FMAs beside
+// them for one matrix of many rows: 8192 x 4096 x 4096 in 136 us, 2.0 PFLOP/s
+// (the MFMA and its scaling FMAs alone reach 2.5 in registers).
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
@@ -34,123 +43,193 @@ constexpr int MAX_KB = FP8_MAX_K / FP8_BLOCK;  // scale blocks along K whose wei
 
 enum { EPI_PLAIN = 0, EPI_SWIGLU = 1 };
 
-// The tile of index mt along the rows: its group and rows [row0, end).
-struct Rows {
-    int g, row0, end;
-};
-
-// Row tile mt of grouped rows: groups' tiles follow each other.  Every wave
-// finds it from the offsets, 64 groups a step; offsets outside 0..M or out of
-// order are cut to the rows that exist.  g = -1 behind the last tile.
-template <int BM>
-__device__ __forceinline__ Rows find_rows(const int32_t *__restrict__ offsets, int G, int M, int mt)
+// A value of read-only memory at a uniform address: a scalar load, whose wait
+// does not touch the copies in flight.
+template <class T>
+__device__ __forceinline__ T uniform_load(const T *p)
 {
-    const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int g0 = 0; g0 < G; g0 += 64) {
-        const int g = g0 + lane;
-        int lo = 0, n = 0;
-        if (g < G) {
-            lo = min(max(offsets[g], 0), M);
-            n = max(min(offsets[g + 1], M) - lo, 0);
-        }
-        const int nt = (n + BM - 1) / BM;
-        const int inc = wave_scan_add(nt);
-        const uint64_t hit = __ballot(base + inc > mt);
-        if (hit) {
-            const int l = __ffsll((unsigned long long)hit) - 1;
-            const int before = base + __builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(nt, l);
-            const int glo = __builtin_amdgcn_readlane(lo, l);
-            return Rows{g0 + l, glo + (mt - before) * BM, glo + __builtin_amdgcn_readlane(n, l)};
-        }
-        base += __builtin_amdgcn_readlane(inc, 63);
-    }
-    return Rows{-1, 0, 0};
+    return *(const __attribute__((address_space(4))) T *)(uintptr_t)p;
 }
 
-template <int NBW, int MB, int WN, int WM, int ST, int EPI>
-struct Cfg {
-    static constexpr int NW = WN * WM, BR = 16 * NBW * WN, BM = 16 * MB * WM;
-    static constexpr int COLS = EPI == EPI_SWIGLU ? BR / 2 : BR;  // output columns of a tile
-    static constexpr int WI = BR / 8 / NW;                        // weight copies of a wave and stage
-    static constexpr int TI = BM / 8 < NW ? 1 : BM / 8 / NW;      // row copies
-    static constexpr int L = WI + TI + 1;                         // all, with the scales
-    static constexpr int SROWS = BM < 64 ? 64 : BM;
-    static constexpr int STAGE = (BR + BM) * FP8_BLOCK + SROWS * 4;
-    static constexpr int NSB = EPI == EPI_SWIGLU ? 2 : (BR + 127) / 128;  // weight scale rows of a tile
-    static constexpr int LDS = ST * STAGE + NSB * MAX_KB * 4;
-    static_assert(BR / 8 % NW == 0 && (BM / 8 < NW || BM / 8 % NW == 0), "copies divide among the waves");
-    static_assert(EPI != EPI_SWIGLU || (COLS == 128 && NBW % 2 == 0), "a tile of h is one scale block wide");
-    static_assert(LDS <= 163840, "LDS of one workgroup");
-    static_assert(WN * BM * 4 <= ST * STAGE, "the block maxima reuse the stages");
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Buffer of the bytes from p on; an offset of DROP is out of its range, where
+// stores do nothing.
+constexpr int DROP = (int)0x80000000;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(void *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(p, 0, 0x7FFFFFFF, 0x00027000);
+}
+
+// A tile: rows [row0, row0 + nrows) of group g (g = -1: none), columns from n0.
+struct Where {
+    int g, row0, nrows, n0, q;
 };
 
-template <int NBW, int MB, int WN, int WM, int ST, int EPI, bool EXACT>
+// Row tile mt of grouped rows.  The tiles of group g take the numbers from
+// offsets[g] / BM + g on, at most offsets[g + 1] / BM + g: a number's group is
+// found by bisection without a sum over the groups before it (the numbers that
+// a group leaves over are empty tiles).  Offsets outside 0..M are cut off.
+template <int BM>
+__device__ __forceinline__ Where find_rows(const int32_t *offsets, int G, int M, int mt)
+{
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int first = min(max(uniform_load(offsets + mid), 0), M) / BM + mid;
+        if (first <= mt)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int a = min(max(uniform_load(offsets + lo), 0), M);
+    const int b = min(uniform_load(offsets + lo + 1), M);
+    const int m = mt - (a / BM + lo), row0 = a + m * BM;
+    if (m < 0 || row0 >= b)
+        return Where{-1, 0, 0, 0, 0};
+    return Where{lo, row0, min(BM, b - row0), 0, 0};
+}
+
+template <int NBW, int BM_, int WN, int WM, int ST, int EPI>
+struct Cfg {
+    static constexpr int NW = WN * WM, BR = 16 * NBW * WN, BM = BM_;
+    static constexpr int MB = (BM / 16 + WM - 1) / WM;            // row blocks of a wave
+    static constexpr int COLS = EPI == EPI_SWIGLU ? BR / 2 : BR;  // output columns of a tile
+    static constexpr int WI = BR / 8 / NW;                        // weight copies of a wave and stage
+    static constexpr int TI = (BM / 8 + NW - 1) / NW;             // row copies (some twice)
+    static constexpr int L = WI + TI;                             // both
+    static constexpr int STAGE = (BR + BM) * FP8_BLOCK;
+    // Scales of the rows: CH blocks of K at a time, three such chunks
+    static constexpr int CH = BM > 128 && ST > 2 ? 2 : 4;
+    static constexpr int CP = (BM * CH + 63) / 64;                // copies of a chunk
+    static constexpr int CI = (CP + NW - 1) / NW;                 // those of a wave (some twice)
+    static constexpr int CHUNK = CP * 256;
+    // Scales of the weights, of two tiles
+    static constexpr int NSB = EPI == EPI_SWIGLU ? 2 : (BR + 127) / 128;  // rows of them
+    static constexpr int SIDE = EPI == EPI_SWIGLU ? WN * BM * 4 : 0;      // block maxima / next rows
+    static constexpr int KBC = ST * STAGE + 3 * CHUNK + 2 * NSB * MAX_KB * 4 + SIDE <= 163840
+                                   ? MAX_KB : MAX_KB / 2;
+    static constexpr int O_CHUNK = ST * STAGE, O_W = O_CHUNK + 3 * CHUNK,
+                         O_SIDE = O_W + 2 * NSB * KBC * 4, LDS = O_SIDE + SIDE;
+    static constexpr int OCC = 163840 / LDS;                      // workgroups of a CU
+    // Stores of a wave and tile (EPI_PLAIN: bf16 in whole words; more otherwise)
+    static constexpr int NS = EPI == EPI_SWIGLU ? 2 * MB : MB * (NBW / 2);
+    // Depth from which a tile's last stages are multiplied while the next
+    // tile's first ones are copied (its rows are known by then).
+    static constexpr int DEEP = 2 * ST - 1;
+    static_assert(BR / 8 % NW == 0, "weight copies divide among the waves");
+    static_assert(EPI != EPI_SWIGLU || (COLS == 128 && NBW % 2 == 0), "a tile of h is one scale block wide");
+    static_assert(LDS <= 163840, "LDS of one workgroup");
+    static_assert(ST >= 2 && ST <= 4, "chunks of scales in use or under way: three");
+    static_assert((ST - 1) * L + NS < 64 && NBW % 2 == 0, "the counter of outstanding operations holds 63");
+};
+
+// Persistent workgroups.  The consumer multiplies stage after stage of its
+// tile; the producer (the same waves) is ST stages ahead and goes on to the
+// next tile, so that a tile's epilogue and its first latency overlap with
+// copies.
+template <int NBW, int BM, int WN, int WM, int ST, int EPI, bool EXACT>
 __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
 {
-    using C = Cfg<NBW, MB, WN, WM, ST, EPI>;
+    using C = Cfg<NBW, BM, WN, WM, ST, EPI>;
+    constexpr int MB = C::MB;
+    constexpr bool GATHER = EPI == EPI_SWIGLU;  // rows of a through row_tok
     __shared__ __attribute__((aligned(256))) uint8_t smem[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = w % WN, wm = w / WN;
-
-    // ---- this workgroup's tile, dealt out in contiguous runs per XCD ------
-    const int ntn = (p.N + C::COLS - 1) / C::COLS;
-    int mtiles = p.mtiles;
-    if (p.tiles)
-        mtiles = min(mtiles, *p.ntiles);
-    const int total = mtiles * ntn, per = (total + 7) / 8;
-    const int id = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= per || id >= total)
-        return;
-    const int mt = id / ntn, n0 = (id - mt * ntn) * C::COLS;
-    Rows r;
-    if (p.tiles) {
-        const Tile t = p.tiles[mt];
-        r = Rows{t.g, t.row0, p.offsets[t.g + 1]};
-    } else if (p.offsets) {
-        r = find_rows<C::BM>(p.offsets, p.G, p.M, mt);
-        if (r.g < 0)
-            return;
-    } else {
-        r = Rows{0, mt * C::BM, p.M};
-    }
-    const int g = __builtin_amdgcn_readfirstlane(r.g), row0 = __builtin_amdgcn_readfirstlane(r.row0);
-    const int nrows = min(C::BM, __builtin_amdgcn_readfirstlane(r.end) - row0);
-
-    // ---- copy addresses: uniform bases that advance along K, lane offsets --
-    const int sub = lane >> 3, slot = lane & 7;
-    const int64_t gb = (int64_t)g * p.bstride, gs = (int64_t)g * p.sstride;
-    uint32_t woff[C::WI], toff[C::TI], soff;
-#pragma unroll
-    for (int i = 0; i < C::WI; ++i) {
-        const int rr = (w * C::WI + i) * 8 + sub, m = rr & 15, c = rr >> 4;
-        const int own = c / NBW, cb = c - own * NBW;
-        constexpr int HB = EPI == EPI_SWIGLU ? NBW / 2 : NBW;
-        const int n = n0 + own * (HB * 16) + (m >> 2) * (4 * HB) + (cb % HB) * 4 + (m & 3);
-        woff[i] = (uint32_t)((int64_t)min(n, p.N - 1) * p.ldb) + ((slot ^ (m >> 1)) << 4);
-    }
-#pragma unroll
-    for (int i = 0; i < C::TI; ++i) {
-        const int rr = ((w * C::TI + i) % (C::BM / 8)) * 8 + sub;
-        const int at = min(rr, nrows - 1);
-        const int64_t row = p.row_tok ? p.row_tok[row0 + at] : at;
-        toff[i] = (uint32_t)(row * p.lda) + ((slot ^ ((rr >> 1) & 7)) << 4);
-    }
-    constexpr int SW = C::SROWS / 64;  // waves whose copies fill the scales
-    {
-        const int at = min((w % SW) * 64 + lane, nrows - 1);
-        const int64_t row = p.row_tok ? p.row_tok[row0 + at] : at;
-        soff = (uint32_t)(row * p.KB * 4);
-    }
-    const uint8_t *ga = p.a + (p.row_tok ? 0 : (int64_t)row0 * p.lda);
-    const float *gsa = p.sa + (p.row_tok ? 0 : (int64_t)row0 * p.KB);
-    const uint8_t *gw0 = p.b0 + gb, *gw1 = EPI == EPI_SWIGLU ? p.b1 + gb : nullptr;
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+    const int KB = p.KB;
 
-    auto issue = [&](int s) {
-        const uint32_t st = lds + (uint32_t)(s % ST) * C::STAGE;
-        const int64_t k = (int64_t)s * FP8_BLOCK;
+    // ---- tiles: contiguous runs per XCD, dealt in turn to its workgroups ----
+    const int ntn = (p.N + C::COLS - 1) / C::COLS;
+    const int mtiles = p.tiles ? min(p.mtiles, uniform_load(p.ntiles)) : p.mtiles;
+    const int total = mtiles * ntn, per = (total + 7) / 8;
+    const int first = ((int)blockIdx.x & 7) * per, step_q = (int)gridDim.x >> 3;
+    auto find = [&](int q) {
+        for (; q < per && first + q < total; q += step_q) {
+            const int id = first + q, mt = id / ntn, nt = id - mt * ntn;
+            Where t;
+            if (p.tiles) {
+                const int g = uniform_load(&p.tiles[mt].g), row0 = uniform_load(&p.tiles[mt].row0);
+                t = Where{g, row0, min(C::BM, uniform_load(p.offsets + g + 1) - row0), 0, 0};
+            } else if (p.offsets) {
+                t = find_rows<C::BM>(p.offsets, p.G, p.M, mt);
+            } else {
+                t = Where{0, mt * C::BM, min(C::BM, p.M - mt * C::BM), 0, 0};
+            }
+            t.n0 = nt * C::COLS;
+            t.q = q;
+            if (t.g >= 0)
+                return t;
+        }
+        return Where{-1, 0, 0, 0, q};
+    };
+
+    // ---- producer: uniform bases that advance along K, lane offsets ---------
+    uint32_t woff[C::WI], toff[C::TI], soff[C::CI];
+    const uint8_t *ga, *gw0, *gw1;
+    const float *gsa;
+    int pk = 0, pq = 0, pc = 0, pt = 0;  // next stage of the tile; stages, chunks and tiles begun
+    auto aim = [&](const Where &t, bool rows_in_lds) {
+        int ln = lane;  // hidden from the compiler: kept over the loops, what depends on it would
+        asm volatile("" : "+v"(ln));  // take fifty registers
+        const int sub = ln >> 3, slot = ln & 7;
+        const int64_t gb = (int64_t)t.g * p.bstride;
+        gw0 = p.b0 + gb;
+        gw1 = EPI == EPI_SWIGLU ? p.b1 + gb : nullptr;
+        ga = p.a + (GATHER ? 0 : (int64_t)t.row0 * p.lda);
+        gsa = p.sa + (GATHER ? 0 : (int64_t)t.row0 * KB);
+        auto row_of = [&](int rr) -> int64_t {
+            const int at = min(rr, t.nrows - 1);
+            if (!GATHER)
+                return at;
+            return rows_in_lds ? ((const int *)(smem + C::O_SIDE))[at] : p.row_tok[t.row0 + at];
+        };
+#pragma unroll
+        for (int i = 0; i < C::WI; ++i) {
+            const int rr = (w * C::WI + i) * 8 + sub, m = rr & 15, c = rr >> 4;
+            const int own = c / NBW, cb = c - own * NBW;
+            constexpr int HB = EPI == EPI_SWIGLU ? NBW / 2 : NBW;
+            const int n = t.n0 + own * (HB * 16) + (m >> 2) * (4 * HB) + (cb % HB) * 4 + (m & 3);
+            woff[i] = (uint32_t)((int64_t)min(n, p.N - 1) * p.ldb) + ((slot ^ (m >> 1)) << 4);
+        }
+#pragma unroll
+        for (int i = 0; i < C::TI; ++i) {
+            const int rr = ((w * C::TI + i) % (C::BM / 8)) * 8 + sub;
+            toff[i] = (uint32_t)(row_of(rr) * p.lda) + ((slot ^ ((rr >> 1) & 7)) << 4);
+        }
+#pragma unroll
+        for (int i = 0; i < C::CI; ++i) {
+            const int rr = ((w * C::CI + i) % C::CP) * (64 / C::CH) + ln / C::CH;
+            soff[i] = (uint32_t)(row_of(rr) * KB);
+        }
+        // the tile's weight scales
+        const int64_t gs = (int64_t)t.g * p.sstride;
+        const int np = (KB + 63) / 64;  // pieces of 64 blocks
+        for (int i = w; i < C::NSB * np; i += C::NW) {
+            const int q = i / np, at = (i - q * np) * 64;
+            const float *src = EPI == EPI_SWIGLU && q ? p.s1 : p.s0;
+            const int nb = EPI == EPI_SWIGLU ? t.n0 >> 7 : min((t.n0 >> 7) + q, ((p.N + 127) >> 7) - 1);
+            dma4(src + gs + (int64_t)nb * KB, (uint32_t)min(at + ln, KB - 1) * 4,
+                 lds + C::O_W + (uint32_t)(((pt & 1) * C::NSB + q) * C::KBC + at) * 4);
+        }
+        ++pt;
+        pk = 0;
+    };
+    auto issue = [&]() {
+        const uint32_t st = lds + (uint32_t)(pq % ST) * C::STAGE;
+        const int64_t k = (int64_t)pk * FP8_BLOCK;
+        if (pk % C::CH == 0) {  // the scales of this stage and the CH - 1 behind it
+            const int kb = min(pk + lane % C::CH, KB - 1);
+#pragma unroll
+            for (int i = 0; i < C::CI; ++i)
+                dma4(gsa, (soff[i] + kb) * 4,
+                     lds + C::O_CHUNK + (uint32_t)(pc % 3) * C::CHUNK +
+                         (uint32_t)((w * C::CI + i) % C::CP) * 256u);
+            ++pc;
+        }
 #pragma unroll
         for (int i = 0; i < C::WI; ++i) {
             const uint8_t *base = gw0;
@@ -162,24 +241,32 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         for (int i = 0; i < C::TI; ++i)
             dma16(ga + k, toff[i],
                   st + C::BR * 128u + (uint32_t)((w * C::TI + i) % (C::BM / 8)) * 1024u);
-        dma4(gsa + s, soff, st + (C::BR + C::BM) * 128u + (uint32_t)(w % SW) * 256u);
+        ++pk;
+        ++pq;
     };
 
-    const int KB = p.KB;
-#pragma unroll
-    for (int s = 0; s < ST - 1; ++s)
-        if (s < KB)
-            issue(s);
+    Where cur = find((int)blockIdx.x >> 3);
+    if (cur.g < 0)
+        return;
+    const bool deep = KB >= C::DEEP;  // uniform in the grid
+    const int o0 = l16 * 128 + ((lg ^ (l16 >> 1)) << 4), o1 = o0 ^ 64;
+    const int nsb = EPI == EPI_SWIGLU ? 0 : (wn * NBW * 16) >> 7;
+    aim(cur, false);
+    for (int s = 0; s < ST && s < KB; ++s)
+        issue();
 
-    // ---- the tile's weight scales -----------------------------------------
-    float *s_w = (float *)(smem + ST * C::STAGE);
-    const int nb0 = n0 >> 7;
-    for (int i = tid; i < C::NSB * KB; i += 64 * C::NW) {
-        const int q = i / KB, k = i - q * KB;
-        if constexpr (EPI == EPI_SWIGLU)
-            s_w[q * MAX_KB + k] = (q ? p.s1 : p.s0)[gs + (int64_t)nb0 * KB + k];
-        else
-            s_w[q * MAX_KB + k] = p.s0[gs + (int64_t)min(nb0 + q, ((p.N + 127) >> 7) - 1) * KB + k];
+    int cq = 0, cc = 0, ct = 0;  // consumer: stages, chunks and tiles done
+    bool stored = false;  // NS stores (at least) were issued behind this tile's first ST stages
+    for (;;) {
+    const Where next = find(cur.q + step_q);
+    const bool go_on = next.g >= 0, ahead = go_on && deep;
+    const int row0 = cur.row0, nrows = cur.nrows, n0 = cur.n0;
+    // the next tile's rows, for the producer: behind this tile's first stages
+    if (GATHER && ahead) {
+        constexpr int RI = (C::BM + 63) / 64;
+        if (w < RI)
+            dma4(p.row_tok + next.row0, (uint32_t)min(w * 64 + lane, next.nrows - 1) * 4,
+                 lds + C::O_SIDE + (uint32_t)w * 256u);
     }
 
     floatx4 acc[NBW][MB];
@@ -189,176 +276,311 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         for (int m = 0; m < MB; ++m)
             acc[c][m] = floatx4{0, 0, 0, 0};
 
-    const int o0 = l16 * 128 + ((lg ^ (l16 >> 1)) << 4), o1 = o0 ^ 64;
-    const int nsb = EPI == EPI_SWIGLU ? 0 : (wn * NBW * 16) >> 7;
-    for (int s = 0; s < KB; ++s) {
-        // stage s has arrived for every wave, and every wave is done with the
-        // stage that the next copies overwrite
-        if (s + ST - 2 < KB)
-            dma_wait_barrier<(ST - 2) * C::L>();
-        else
-            dma_wait_barrier<0>();
-        if (s + ST - 1 < KB)
-            issue(s + ST - 1);
-        const uint8_t *st = smem + (s % ST) * C::STAGE;
-        const uint8_t *wt = st + wn * (NBW * 2048), *tt = st + C::BR * 128 + wm * (MB * 2048);
-        const float *ts = (const float *)(st + (C::BR + C::BM) * 128) + wm * (MB * 16);
-        Fp8Frag<EXACT> A[NBW];
+    // Fragments and scales of stage s of this tile.  (The copies that a wave
+    // waits for include scales now and then: counting as if there were none
+    // only waits for a few copies more.)
+    struct Weights {
+        Fp8Raw v[NBW];
+        float s0, s1;
+    };
+    struct Block {
+        Fp8Raw v;
+        float s;
+    };
+    const float *s_w = (const float *)(smem + C::O_W) + ((ct & 1) * C::NSB + nsb) * C::KBC;
+    auto load_weights = [&](Weights &a, int s) {
+        const uint8_t *wt = smem + ((cq + s) % ST) * C::STAGE + wn * (NBW * 2048);
 #pragma unroll
         for (int c = 0; c < NBW; ++c)
-            A[c].set(*(const uint4 *)(wt + c * 2048 + o0), *(const uint4 *)(wt + c * 2048 + o1));
-        const float sw0 = s_w[nsb * MAX_KB + s], sw1 = EPI == EPI_SWIGLU ? s_w[MAX_KB + s] : 0.0f;
+            a.v[c] = fp8_raw(*(const uint4 *)(wt + c * 2048 + o0), *(const uint4 *)(wt + c * 2048 + o1));
+        a.s0 = s_w[s];
+        a.s1 = EPI == EPI_SWIGLU ? s_w[C::KBC + s] : 0.0f;
+    };
+    auto load_block = [&](Block &b, int s, int m) {
+        const uint8_t *st = smem + ((cq + s) % ST) * C::STAGE + C::BR * 128;
+        const uint8_t *tt = st + (m * WM + wm) * 2048;
+        b.v = fp8_raw(*(const uint4 *)(tt + o0), *(const uint4 *)(tt + o1));
+        b.s = ((const float *)(smem + C::O_CHUNK + ((cc + s / C::CH) % 3) * C::CHUNK))[
+            ((m * WM + wm) * 16 + l16) * C::CH + s % C::CH];
+    };
+
+    // The K loop over the first NM of the wave's MB row blocks (the others hold
+    // no rows of this tile).  A block's fragment is read while the one before
+    // it is multiplied.  Behind the MFMAs of a stage's last block, while they
+    // run, the workgroup turns to the next stage: everything of it has arrived
+    // for every wave, every wave is done reading this one (whose buffer takes
+    // the stage that is ST further), and the next weights and first block are
+    // read.  The sums of a block are scaled and added while the next block's
+    // MFMAs run (LAG), where there are registers for it.
+    constexpr bool LAG = MB < 8;
+    auto kloop = [&](auto nm) {
+        constexpr int NM = decltype(nm)::value;
+        Weights wf;
+        Block bf[2];
+        floatx4 t[NBW];  // the last block's sums, not yet scaled
+        float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            Fp8Frag<EXACT> B;
-            B.set(*(const uint4 *)(tt + m * 2048 + o0), *(const uint4 *)(tt + m * 2048 + o1));
-            const float sr = ts[m * 16 + l16];
-            const float f0 = sr * sw0, f1 = sr * sw1;
+        for (int c = 0; c < NBW; ++c)
+            t[c] = floatx4{0, 0, 0, 0};
+        auto join = [&](int m) {
 #pragma unroll
             for (int c = 0; c < NBW; ++c) {
-                const floatx4 t = mfma_fp8(A[c], B);
-                const float f = EPI == EPI_SWIGLU && c >= NBW / 2 ? f1 : f0;
+                const float f = EPI == EPI_SWIGLU && c >= NBW / 2 ? t1 : t0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[c][m][i] = fmaf(t[i], f, acc[c][m][i]);
+                    acc[c][m][i] = fmaf(t[c][i], f, acc[c][m][i]);
+                // here, not behind the next branch, up to which every sum of
+                // the stage would stay in a register
+                asm volatile("" : "+v"(acc[c][m]));
             }
-        }
+        };
+        // MORE: 2 = the tile's stage s + ST is copied, 1 = the next tile's
+        // stages are (if `ahead`), 0 = the tile's last stage
+        auto step = [&](int s, auto more) {
+            constexpr int MORE = decltype(more)::value;
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                if (m + 1 < NM)
+                    load_block(bf[(m + 1) & 1], s, m + 1);
+                const Fp8Frag<EXACT> B(bf[m & 1].v);
+                floatx4 n[NBW];
+#pragma unroll
+                for (int c = 0; c < NBW; ++c)
+                    n[c] = mfma_fp8(Fp8Frag<EXACT>(wf.v[c]), B);
+                const float f0 = bf[m & 1].s * wf.s0, f1 = bf[m & 1].s * wf.s1;
+                if (m + 1 == NM && MORE) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (MORE != 2 && !ahead)
+                        dma_wait_barrier<0>();
+                    else if (s < ST - 1 && stored)  // the stores of the tile before are newer
+                        dma_wait_barrier<(ST - 2) * C::L + C::NS>();
+                    else if (ST == 3 && (s + 2 < KB ? s + 2 : s + 2 - KB) % C::CH == 0)
+                        dma_wait_barrier<(ST - 2) * C::L + C::CI>();  // stage s + 2 holds scales
+                    else
+                        dma_wait_barrier<(ST - 2) * C::L>();
+                    load_weights(wf, s + 1);
+                    load_block(bf[0], s + 1, 0);
+                    if (MORE == 2 || ahead)
+                        issue();
+                }
+                if (LAG)
+                    join(m ? m - 1 : NM - 1);
+#pragma unroll
+                for (int c = 0; c < NBW; ++c)
+                    t[c] = n[c];
+                t0 = f0;
+                t1 = f1;
+                if (!LAG)
+                    join(m);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (stored)
+            dma_wait_barrier<(ST - 1) * C::L + C::NS>();
+        else if (KB >= ST)
+            dma_wait_barrier<(ST - 1) * C::L>();
+        else
+            dma_wait_barrier<0>();
+        load_weights(wf, 0);
+        load_block(bf[0], 0, 0);
+        int s = 0;
+        for (; s + ST < KB; ++s)
+            step(s, std::integral_constant<int, 2>{});
+        if (ahead)
+            aim(next, true);
+        for (; s + 1 < KB; ++s)
+            step(s, std::integral_constant<int, 1>{});
+        step(s, std::integral_constant<int, 0>{});
+        if (LAG)
+            join(NM - 1);
+    };
+    const int act = ((nrows + 15) / 16 - wm + WM - 1) / WM;  // the wave's row blocks with rows
+    constexpr int HALF = (MB + 1) / 2;
+    if (act > HALF) {
+        if (MB > 4 && act < MB)  // a tile of 16 * MB * WM - 16 rows, or as many
+            kloop(std::integral_constant<int, MB - 1>{});
+        else
+            kloop(std::integral_constant<int, MB>{});
+    } else {
+        kloop(std::integral_constant<int, HALF>{});
     }
+    lds_barrier();  // every wave is done with this tile's last stage
+    if (ahead)
+        issue();
 
+    __builtin_amdgcn_sched_barrier(0);
+    int e16 = l16, eg = lg;  // hidden as in aim()
+    asm volatile("" : "+v"(e16), "+v"(eg));
+    // Stores go through a buffer descriptor of the tile's rows: lanes without a
+    // row (or columns) store out of its range, which drops them, so that each
+    // wave issues the same number of stores and the waits above can count them.
     if constexpr (EPI == EPI_PLAIN) {
-        const int n = n0 + wn * (NBW * 16) + lg * (4 * NBW);
-        const bool whole = p.vec && n + 4 * NBW <= p.N;
+        const int n = n0 + wn * (NBW * 16) + eg * (4 * NBW);
+        const int esz = p.out_f32 ? 4 : 2;
+        const int pitch = (int)p.ldy * esz;  // checked by the host where p.vec
+        const auto rsrc = tile_rsrc((char *)p.y + (int64_t)row0 * p.ldy * esz);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            const int rr = (wm * MB + m) * 16 + l16;
-            if (rr >= nrows)
-                continue;
-            const int64_t at = (int64_t)(row0 + rr) * p.ldy + n;
-            if (p.out_f32) {
-                float *y = (float *)p.y + at;
+            const int rr = (m * WM + wm) * 16 + e16;
+            if (p.vec) {
+                const int at = rr < nrows && n < p.N ? rr * pitch + n * esz : DROP;
+                if (p.out_f32) {
 #pragma unroll
-                for (int c = 0; c < NBW; ++c) {
-                    if (whole)
-                        *(floatx4 *)(y + 4 * c) = acc[c][m];
-                    else
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n + 4 * c + i < p.N)
-                                y[4 * c + i] = acc[c][m][i];
-                }
-            } else {
-                uint16_t *y = (uint16_t *)p.y + at;
-                uint32_t v[2 * NBW];
-#pragma unroll
-                for (int c = 0; c < NBW; ++c) {
-                    v[2 * c] = pack_bf2(acc[c][m][0], acc[c][m][1]);
-                    v[2 * c + 1] = pack_bf2(acc[c][m][2], acc[c][m][3]);
-                }
-                if (whole) {
-                    if constexpr (NBW % 2 == 0) {
-#pragma unroll
-                        for (int c = 0; c < NBW; c += 2)
-                            *(uint4 *)(y + 4 * c) = uint4{v[2 * c], v[2 * c + 1], v[2 * c + 2], v[2 * c + 3]};
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < NBW; ++c)
-                            *(uint2 *)(y + 4 * c) = uint2{v[2 * c], v[2 * c + 1]};
-                    }
+                    for (int c = 0; c < NBW; ++c)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            __builtin_bit_cast(u32x4, acc[c][m]), rsrc, at, 16 * c, 0);
                 } else {
+                    uint32_t v[2 * NBW];
 #pragma unroll
-                    for (int i = 0; i < 4 * NBW; ++i)
-                        if (n + i < p.N)
-                            y[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+                    for (int c = 0; c < NBW; ++c) {
+                        v[2 * c] = cvt_bf2(acc[c][m][0], acc[c][m][1]);
+                        v[2 * c + 1] = cvt_bf2(acc[c][m][2], acc[c][m][3]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < NBW; c += 2)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            u32x4{v[2 * c], v[2 * c + 1], v[2 * c + 2], v[2 * c + 3]}, rsrc, at, 8 * c, 0);
                 }
+            } else if (rr < nrows) {
+                const int64_t at = (int64_t)(row0 + rr) * p.ldy + n;
+#pragma unroll
+                for (int c = 0; c < NBW; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (n + 4 * c + i >= p.N)
+                            continue;
+                        if (p.out_f32)
+                            ((float *)p.y)[at + 4 * c + i] = acc[c][m][i];
+                        else
+                            ((uint16_t *)p.y)[at + 4 * c + i] = (uint16_t)cvt_bf2(acc[c][m][i], 0.0f);
+                    }
             }
         }
     } else {
         // h = silu(gate) * up, its block maximum over the tile's 128 columns
         // (4 lanes of a wave, then the waves), and its codes
         constexpr int HB = NBW / 2;
-        float *s_max = (float *)smem;  // [WN][BM]
-        __syncthreads();               // every wave is done with the last stage
+        float *s_max = (float *)(smem + C::O_SIDE);  // [WN][BM] (the next rows have been read)
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
+            if ((m * WM + wm) * 16 >= BM)  // uniform: a block that the tile does not have
+                continue;
             float mx = 0.0f;
 #pragma unroll
             for (int c = 0; c < HB; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float z = acc[c][m][i];
-                    const float h = z / (1.0f + expf(-z)) * acc[c + HB][m][i];
+                    const float h = silu(z) * acc[c + HB][m][i];
                     acc[c][m][i] = h;
                     mx = fmaxf(mx, fabsf(h));
                 }
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32));
-            if (lg == 0)
-                s_max[wn * C::BM + (wm * MB + m) * 16 + l16] = mx;
+            if (eg == 0)
+                s_max[wn * BM + (m * WM + wm) * 16 + e16] = mx;
         }
-        __syncthreads();
+        lds_barrier();
+        const auto rh = tile_rsrc(p.hq + (int64_t)row0 * p.N);
+        const auto rs = tile_rsrc(p.hs + (int64_t)row0 * (p.N >> 7));
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            const int rr = (wm * MB + m) * 16 + l16;
-            float mx = s_max[rr];
+            const int rr = (m * WM + wm) * 16 + e16, at = min(rr, BM - 1);
+            float mx = s_max[at];
 #pragma unroll
             for (int i = 1; i < WN; ++i)
-                mx = fmaxf(mx, s_max[i * C::BM + rr]);
-            if (rr >= nrows)
-                continue;
+                mx = fmaxf(mx, s_max[i * BM + at]);
             const Fp8Block q = fp8_block(mx);
-            uint8_t *h = p.hq + (int64_t)(row0 + rr) * p.N + n0 + wn * (HB * 16) + lg * (4 * HB);
-#pragma unroll
-            for (int c = 0; c < HB; ++c)
-                *(uint32_t *)(h + 4 * c) = fp8x4(acc[c][m][0], acc[c][m][1], acc[c][m][2], acc[c][m][3], q);
-            if (wn == 0 && lg == 0)
-                p.hs[(int64_t)(row0 + rr) * (p.N >> 7) + (n0 >> 7)] = q.scale;
+            static_assert(HB == 2, "a lane holds 8 columns of h");
+            __builtin_amdgcn_raw_buffer_store_b64(
+                u32x2{fp8x4(acc[0][m][0], acc[0][m][1], acc[0][m][2], acc[0][m][3], q),
+                      fp8x4(acc[1][m][0], acc[1][m][1], acc[1][m][2], acc[1][m][3], q)},
+                rh, rr < nrows ? rr * p.N + n0 + wn * (HB * 16) + eg * (4 * HB) : DROP, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(
+                __float_as_uint(q.scale), rs,
+                rr < nrows && wn == 0 && eg == 0 ? (rr * (p.N >> 7) + (n0 >> 7)) * 4 : DROP, 0, 0);
         }
+        lds_barrier();  // s_max is free again
+    }
+
+    __builtin_amdgcn_sched_barrier(0);
+    if (!go_on)
+        break;
+    cq += KB;
+    cc += (KB + C::CH - 1) / C::CH;
+    ++ct;
+    cur = next;
+    stored = deep && (EPI == EPI_SWIGLU || p.vec);
+    if (!deep) {  // few stages: no copies under way between tiles
+        aim(cur, false);
+        for (int s = 0; s < ST && s < KB; ++s)
+            issue();
+    }
     }
 }
 
-template <int NBW, int MB, int WN, int WM, int ST, int EPI>
+template <int NBW, int BM, int WN, int WM, int ST, int EPI>
 void launch_cfg(const Fp8Args &p, hipStream_t st)
 {
-    using C = Cfg<NBW, MB, WN, WM, ST, EPI>;
-    const int64_t ntn = (p.N + C::COLS - 1) / C::COLS;
-    const unsigned grid = (unsigned)((p.mtiles * ntn + 7) / 8 * 8);
+    using C = Cfg<NBW, BM, WN, WM, ST, EPI>;
+    const int64_t tiles = (int64_t)p.mtiles * ((p.N + C::COLS - 1) / C::COLS);
+    const unsigned grid = (unsigned)(std::min<int64_t>(tiles, 256 * C::OCC) + 7) / 8 * 8;
     if (EPI == EPI_PLAIN && p.out_f32)
-        fp8_tile<NBW, MB, WN, WM, ST, EPI, EPI == EPI_PLAIN><<<grid, 64 * C::NW, 0, st>>>(p);
+        fp8_tile<NBW, BM, WN, WM, ST, EPI, EPI == EPI_PLAIN><<<grid, 64 * C::NW, 0, st>>>(p);
     else
-        fp8_tile<NBW, MB, WN, WM, ST, EPI, false><<<grid, 64 * C::NW, 0, st>>>(p);
+        fp8_tile<NBW, BM, WN, WM, ST, EPI, false><<<grid, 64 * C::NW, 0, st>>>(p);
 }
 
 }  // namespace
 
-int fp8_bm(int64_t rows, int groups)
+// Rows of a tile.  Grouped rows (the rows of an expert): the weights of a group
+// stream from memory once per row tile, so one tile should take all of a
+// group's rows, 1.4 standard deviations of a balanced routing above the mean,
+// up to the 144 rows whose three stages fill LDS (T=8192 over 384 experts, 128
+// rows each: gate+up 1650 us with tiles of 144 rows, 1860 with 128, which a
+// second tile follows for half of the experts).  Groups of more rows are bound
+// by the matrix cores and take the largest tiles.  One matrix: the largest
+// tiles that still give every CU one (8192 x 4096 x 4096: 144 us with 256 rows,
+// 163 with 128).
+int fp8_bm(int64_t rows, int groups, int64_t cols)
 {
-    const int64_t per = rows / (groups > 0 ? groups : 1);
-    return per <= 16 ? 16 : per <= 48 ? 32 : per <= 96 ? 64 : 128;
+    if (groups > 1) {
+        const double per = (double)rows / groups, want = per + 1.4 * std::sqrt(per);
+        for (int bm : {16, 32, 64, 96, 144})
+            if (want <= bm)
+                return bm;
+        return per < 192 ? 128 : 256;
+    }
+    for (int bm : {256, 128, 64})
+        if (rows > bm / 2 && (rows + bm - 1) / bm * ((cols + 255) / 256) >= 256)
+            return bm;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 int64_t fp8_row_tiles(int64_t rows, int groups, int bm)
 {
-    return (rows + bm - 1) / bm + (groups > 1 ? std::min<int64_t>(groups, rows) : 0);
+    return groups > 1 ? rows / bm + groups : (rows + bm - 1) / bm;
 }
 
-void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st)
+namespace {
+
+template <int EPI>
+void launch_bm(const Fp8Args &p, int bm, hipStream_t st)
 {
     switch (bm) {
-    case 16: launch_cfg<2, 1, 4, 1, 4, EPI_PLAIN>(p, st); break;
-    case 32: launch_cfg<4, 2, 4, 1, 3, EPI_PLAIN>(p, st); break;
-    case 64: launch_cfg<4, 4, 4, 1, 3, EPI_PLAIN>(p, st); break;
-    default: launch_cfg<4, 8, 4, 1, 3, EPI_PLAIN>(p, st); break;
+    case 16: launch_cfg<4, 16, 4, 1, 4, EPI>(p, st); break;
+    case 32: launch_cfg<4, 32, 4, 2, 4, EPI>(p, st); break;
+    case 64: launch_cfg<4, 64, 4, 2, 3, EPI>(p, st); break;
+    case 96: launch_cfg<4, 96, 4, 2, 3, EPI>(p, st); break;
+    case 128: launch_cfg<4, 128, 4, 2, 3, EPI>(p, st); break;
+    case 144: launch_cfg<4, 144, 4, 2, 3, EPI>(p, st); break;
+    default: launch_cfg<4, 256, 4, 2, 2, EPI>(p, st); break;
     }
 }
 
-void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st)
-{
-    switch (bm) {
-    case 16: launch_cfg<4, 1, 4, 1, 4, EPI_SWIGLU>(p, st); break;
-    case 32: launch_cfg<4, 2, 4, 1, 3, EPI_SWIGLU>(p, st); break;
-    case 64: launch_cfg<4, 4, 4, 1, 3, EPI_SWIGLU>(p, st); break;
-    default: launch_cfg<4, 8, 4, 1, 3, EPI_SWIGLU>(p, st); break;
-    }
-}
+}  // namespace
+
+void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st) { launch_bm<EPI_PLAIN>(p, bm, st); }
+void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st) { launch_bm<EPI_SWIGLU>(p, bm, st); }
 
 }  // namespace moe

@@ -193,7 +193,7 @@ Layout layout(const moe_shape_t *s, int Tc)
     Layout L{};
     const moe::ExpertArgs a = expert_shape(s, Tc);
     const bool f8 = s->w_dtype == MOE_FP8;
-    L.bm_gu = f8 ? moe::fp8_bm((int64_t)Tc * s->top_k, s->E) : moe::gemm_bm_gu(a);
+    L.bm_gu = f8 ? moe::fp8_bm((int64_t)Tc * s->top_k, s->E, s->H) : moe::gemm_bm_gu(a);
     L.bm_dc = f8 ? L.bm_gu : moe::gemm_bm_dc(a);
     L.max_tiles_gu = max_tiles(Tc, s, L.bm_gu);
     L.max_tiles_dc = max_tiles(Tc, s, L.bm_dc);

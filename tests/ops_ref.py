@@ -140,8 +140,9 @@ def experts(x, wg, sg, wu, su, wd, sd, idx, w):
         u, du = product(xv[t], matrix_value(wu[e], su[e]), True)
         sig = torch.sigmoid(g)
         h = g * sig * u
-        # silu' <= 1.1; exponential, sum, quotient and two products: 8 roundings at most
-        dh = 1.1 * dg * u.abs() + (g * sig).abs() * du + 1.1 * dg * du + 8 * U32 * h.abs()
+        # silu' <= 1.1; exponential, sum, reciprocal (2 units each) and two products: 8 roundings, and the
+        # exponential's argument -g log2(e), off by 2^-24 of itself, moves it by |g| 2^-24
+        dh = 1.1 * dg * u.abs() + (g * sig).abs() * du + 1.1 * dg * du + (8 + g.abs()) * U32 * h.abs()
         qh, sh, v = quant(h)
         _, step, off = e4m3_grid(v)
         # error of the quotient: that of h and of the block's maximum, and 4 roundings
