@@ -19,6 +19,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["probe.hip", "router.hip", "route_small.hip", "permute.hip", "expert_gemm.hip",
            "expert_stream.hip", "mxfp4.hip", "select.hip", "quant_fp8.hip", "matmul_fp8.hip",
+           "matmul_fp8_small.hip",
            "experts_given.hip", "moe_api.cpp", "moe_ops.cpp", "noalloc.hip"]
 
 FLAGS = [

@@ -1,22 +1,27 @@
 // The combine of experts run with given routing: y_t = sum_j w[t, j] *
 // stage[row of (t, j)] in j order, fp32 sum, rounded once, as in moe_forward;
 // an empty slot (row_of < 0) adds nothing whatever its weight, and a token
-// with empty slots only gets zeros.
+// with empty slots only gets zeros.  Rows of the FP8 experts are half values
+// under an exponent for each 16 columns (fp8.h).
 #include "common.h"
+#include "fp8.h"
 #include "kernels.h"
 
 namespace moe {
 
 namespace {
 
+enum { ROWS_F32 = 0, ROWS_BF16 = 1, ROWS_FP8 = 2 };
+
 // 16 bytes of one output row per thread, the rows' pieces loaded together.
-template <int KM, bool BF16>
+template <int KM, int ROWS>
 __global__ __launch_bounds__(256) void combine_given(const void *__restrict__ stage,
                                                      const int32_t *__restrict__ row_of,
                                                      const float *__restrict__ topk_w,
+                                                     const uint8_t *__restrict__ exps,
                                                      void *__restrict__ y, int T, int H, int k)
 {
-    constexpr int W = BF16 ? 8 : 4;  // columns of a thread
+    constexpr int W = ROWS == ROWS_F32 ? 4 : 8;  // columns of a thread
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int per_row = H / W;
     if (i >= (int64_t)T * per_row)
@@ -31,10 +36,14 @@ __global__ __launch_bounds__(256) void combine_given(const void *__restrict__ st
         w[j] = j < k ? topk_w[t * k + j] : 0.0f;
     }
     uint4 v[KM];
+    uint32_t ex[KM];
 #pragma unroll
     for (int j = 0; j < KM; ++j)
-        if (row[j] >= 0)
-            v[j] = *(const uint4 *)((const char *)stage + ((int64_t)row[j] * H + c) * (BF16 ? 2 : 4));
+        if (row[j] >= 0) {
+            v[j] = *(const uint4 *)((const char *)stage + ((int64_t)row[j] * H + c) * (16 / W));
+            if constexpr (ROWS == ROWS_FP8)
+                ex[j] = exps[((int64_t)row[j] * H + c) >> 4];
+        }
     float acc[W];
 #pragma unroll
     for (int q = 0; q < W; ++q)
@@ -46,7 +55,13 @@ __global__ __launch_bounds__(256) void combine_given(const void *__restrict__ st
         const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if constexpr (BF16) {
+            if constexpr (ROWS == ROWS_FP8) {
+                typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+                const half2 hv = __builtin_bit_cast(half2, u[q]);
+                const float f = stage_unpack(ex[j]);
+                acc[2 * q] = fmaf(w[j], (float)hv[0] * f, acc[2 * q]);
+                acc[2 * q + 1] = fmaf(w[j], (float)hv[1] * f, acc[2 * q + 1]);
+            } else if constexpr (ROWS == ROWS_BF16) {
                 acc[2 * q] = fmaf(w[j], __uint_as_float(u[q] << 16), acc[2 * q]);
                 acc[2 * q + 1] = fmaf(w[j], __uint_as_float(u[q] & 0xFFFF0000u), acc[2 * q + 1]);
             } else {
@@ -54,24 +69,31 @@ __global__ __launch_bounds__(256) void combine_given(const void *__restrict__ st
             }
         }
     }
-    if constexpr (BF16)
+    if constexpr (ROWS == ROWS_FP8)
+        *(uint4 *)((uint16_t *)y + t * H + c) = uint4{cvt_bf2(acc[0], acc[1]), cvt_bf2(acc[2], acc[3]),
+                                                      cvt_bf2(acc[4], acc[5]), cvt_bf2(acc[6], acc[7])};
+    else if constexpr (ROWS == ROWS_BF16)
         *(uint4 *)((uint16_t *)y + t * H + c) = uint4{pack_bf2(acc[0], acc[1]), pack_bf2(acc[2], acc[3]),
                                                       pack_bf2(acc[4], acc[5]), pack_bf2(acc[6], acc[7])};
     else
         *(float4 *)((float *)y + t * H + c) = float4{acc[0], acc[1], acc[2], acc[3]};
 }
 
-template <bool BF16>
+template <int ROWS>
 void launch_typed(const CombineArgs &a, hipStream_t st)
 {
-    const int64_t n = (int64_t)a.T * (a.H / (BF16 ? 8 : 4));
+    const int64_t n = (int64_t)a.T * (a.H / (ROWS == ROWS_F32 ? 4 : 8));
     const unsigned wgs = (unsigned)((n + 255) / 256);
+    auto run = [&](auto km) {
+        combine_given<decltype(km)::value, ROWS>
+            <<<wgs, 256, 0, st>>>(a.stage, a.row_of, a.topk_w, a.exps, a.y, a.T, a.H, a.k);
+    };
     if (a.k <= 4)
-        combine_given<4, BF16><<<wgs, 256, 0, st>>>(a.stage, a.row_of, a.topk_w, a.y, a.T, a.H, a.k);
+        run(std::integral_constant<int, 4>{});
     else if (a.k <= 8)
-        combine_given<8, BF16><<<wgs, 256, 0, st>>>(a.stage, a.row_of, a.topk_w, a.y, a.T, a.H, a.k);
+        run(std::integral_constant<int, 8>{});
     else
-        combine_given<16, BF16><<<wgs, 256, 0, st>>>(a.stage, a.row_of, a.topk_w, a.y, a.T, a.H, a.k);
+        run(std::integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -80,10 +102,12 @@ void launch_combine_given(const CombineArgs &a, hipStream_t st)
 {
     if (a.T == 0)
         return;
-    if (a.act == ACT_BF16)
-        launch_typed<true>(a, st);
+    if (a.exps)
+        launch_typed<ROWS_FP8>(a, st);
+    else if (a.act == ACT_BF16)
+        launch_typed<ROWS_BF16>(a, st);
     else
-        launch_typed<false>(a, st);
+        launch_typed<ROWS_F32>(a, st);
 }
 
 }  // namespace moe

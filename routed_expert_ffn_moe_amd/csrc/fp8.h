@@ -60,6 +60,31 @@ __device__ __forceinline__ uint32_t fp8x4(float x0, float x1, float x2, float x3
     return (uint32_t)v;
 }
 
+// Staging rows of the FP8 experts' outputs: half precision under one exponent
+// byte for each 16 columns, the largest of their finite values scaled to
+// [2^14, 2^15).  2^-11 relative where bf16 rows, of the same size, are 2^-8
+// off: the sum over a token's slots then adds no error that shows next to the
+// rounding of y to bf16 (with bf16 rows it was as large again).  Infinities and
+// NaN stay what they are.
+constexpr uint32_t STAGE_MIN_EXP = 15;  // keeps both factors normal
+
+__device__ __forceinline__ uint32_t stage_exponent(float v)
+{
+    const uint32_t e = (__float_as_uint(v) >> 23) & 0xFF;
+    return e == 0xFF ? 0 : e;
+}
+
+// 2^(141 - e) and 2^(e - 141) of a biased exponent e.
+__device__ __forceinline__ float stage_pack(uint32_t e) { return __uint_as_float((268 - e) << 23); }
+__device__ __forceinline__ float stage_unpack(uint32_t e) { return __uint_as_float((e - 14) << 23); }
+
+__device__ __forceinline__ uint32_t cvt_half2(float a, float b)
+{
+    typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, half2));
+}
+
 // Largest value over each row of 16 lanes, in all of them (row rotations).
 __device__ __forceinline__ float row16_max(float v)
 {

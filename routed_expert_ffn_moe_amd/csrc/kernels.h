@@ -152,6 +152,7 @@ struct CombineArgs {
     const float *topk_w;
     void *y;
     int T, H, k, shared, act;
+    const uint8_t *exps;  // launch_combine_given: exponents of FP8 staging rows, or null
 };
 void launch_combine(const CombineArgs &a, hipStream_t st);
 // The same for given routing, where row_of < 0 marks an empty slot (no shared
@@ -203,6 +204,7 @@ struct Fp8Args {
     const Tile *tiles;       // row tiles from the permutation, or null: from the offsets
     const int32_t *ntiles;
     void *y;                 // plain: [rows, N], row stride ldy elements
+    uint8_t *exps;           // staging rows (y of half values): an exponent per 16 columns, or null
     uint8_t *hq;             // SwiGLU: codes of h [rows, N] and their scales [rows, N / 128]
     float *hs;
     int64_t lda, ldb, ldy, bstride, sstride;
@@ -212,6 +214,22 @@ int fp8_bm(int64_t rows, int groups, int64_t cols);              // rows of a ti
 int64_t fp8_row_tiles(int64_t rows, int groups, int bm);         // upper bound of the row tiles
 void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st);
 void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st);
+// Few rows (matmul_fp8_small.hip): one matrix of few tiles, and the whole of
+// the FP8 experts for decode rows with given routing.
+bool fp8_split_ok(const Fp8Args &p);
+void launch_fp8_split(const Fp8Args &p, hipStream_t st);
+struct Fp8Decode {
+    const uint16_t *x;                       // [T, H] bf16
+    const uint8_t *w_gate, *w_up, *w_down;   // [E, I, H], [E, H, I] codes
+    const float *s_gate, *s_up, *s_down;     // their scales
+    const int32_t *idx;                      // [T, k]; outside 0..E-1: an empty slot
+    const float *topk_w;                     // [T, k]
+    float *h;                                // [T * k, I] workspace
+    uint16_t *y;                             // [T, H] bf16
+    int T, H, E, k, I;
+};
+bool fp8_decode_ok(int T, int H, int k, int I);
+void launch_fp8_decode(const Fp8Decode &p, hipStream_t st);
 
 // Measurement aids (probe.hip): the device's HBM read (sequential and
 // scattered), MXFP4 dequantisation stream and bf16 MFMA ceilings.

@@ -41,7 +41,8 @@ namespace {
 
 constexpr int MAX_KB = FP8_MAX_K / FP8_BLOCK;  // scale blocks along K whose weight scales fit LDS
 
-enum { EPI_PLAIN = 0, EPI_SWIGLU = 1 };
+// Results as they are, h = silu(gate) * up as codes, or staging rows (fp8.h).
+enum { EPI_PLAIN = 0, EPI_SWIGLU = 1, EPI_STAGE = 2 };
 
 // A value of read-only memory at a uniform address: a scalar load, whose wait
 // does not touch the copies in flight.
@@ -114,7 +115,7 @@ struct Cfg {
                          O_SIDE = O_W + 2 * NSB * KBC * 4, LDS = O_SIDE + SIDE;
     static constexpr int OCC = 163840 / LDS;                      // workgroups of a CU
     // Stores of a wave and tile (EPI_PLAIN: bf16 in whole words; more otherwise)
-    static constexpr int NS = EPI == EPI_SWIGLU ? 2 * MB : MB * (NBW / 2);
+    static constexpr int NS = EPI == EPI_SWIGLU ? 2 * MB : EPI == EPI_STAGE ? 3 * MB : MB * (NBW / 2);
     // Depth from which a tile's last stages are multiplied while the next
     // tile's first ones are copied (its rows are known by then).
     static constexpr int DEEP = 2 * ST - 1;
@@ -456,6 +457,33 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
                     }
             }
         }
+    } else if constexpr (EPI == EPI_STAGE) {
+        static_assert(NBW == 4, "a lane holds the 16 columns under one exponent");
+        const int n = n0 + wn * 64 + eg * 16;
+        const auto rsrc = tile_rsrc((uint16_t *)p.y + (int64_t)row0 * p.N);
+        const auto rexp = tile_rsrc(p.exps + (int64_t)row0 * (p.N / 16));
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            const int rr = (m * WM + wm) * 16 + e16;
+            uint32_t ex = STAGE_MIN_EXP;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ex = max(ex, stage_exponent(acc[c][m][i]));
+            const float f = stage_pack(ex);
+            uint32_t v[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                v[2 * c] = cvt_half2(acc[c][m][0] * f, acc[c][m][1] * f);
+                v[2 * c + 1] = cvt_half2(acc[c][m][2] * f, acc[c][m][3] * f);
+            }
+            const bool in = rr < nrows && n < p.N;
+            const int at = in ? (rr * p.N + n) * 2 : DROP;
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, rsrc, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[4], v[5], v[6], v[7]}, rsrc, at, 16, 0);
+            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)ex, rexp, in ? (rr * p.N + n) / 16 : DROP, 0, 0);
+        }
     } else {
         // h = silu(gate) * up, its block maximum over the tile's 128 columns
         // (4 lanes of a wave, then the waves), and its codes
@@ -510,7 +538,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
     cc += (KB + C::CH - 1) / C::CH;
     ++ct;
     cur = next;
-    stored = deep && (EPI == EPI_SWIGLU || p.vec);
+    stored = deep && (EPI != EPI_PLAIN || p.vec);
     if (!deep) {  // few stages: no copies under way between tiles
         aim(cur, false);
         for (int s = 0; s < ST && s < KB; ++s)
@@ -580,7 +608,15 @@ void launch_bm(const Fp8Args &p, int bm, hipStream_t st)
 
 }  // namespace
 
-void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st) { launch_bm<EPI_PLAIN>(p, bm, st); }
+void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st)
+{
+    if (p.exps)
+        launch_bm<EPI_STAGE>(p, bm, st);
+    else if (fp8_split_ok(p))
+        launch_fp8_split(p, st);
+    else
+        launch_bm<EPI_PLAIN>(p, bm, st);
+}
 void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st) { launch_bm<EPI_SWIGLU>(p, bm, st); }
 
 }  // namespace moe

@@ -1,0 +1,320 @@
+// The FP8 products of few rows, where there are too few tiles for the kernel
+// in matmul_fp8.hip to fill the chip and a call is a matter of latency: K is
+// split over the waves of a workgroup, which read their fragments straight
+// from memory and meet once in LDS.
+//
+//  fp8_split        one matrix of few tiles: wave sums over every KS-th block of
+//                   K, joined in wave order.
+//  fp8_pair_gate_up decode rows of the experts (T <= 8): one workgroup per
+//                   (token, slot) pair and 16 columns of h, no permutation;
+//                   the pair's x is quantised on the way.
+//  fp8_token_down   their down projections and the combine: one workgroup per
+//                   token and 16 columns of y, h quantised on the way.
+//
+// The decode kernels pass the sums of single blocks of K through LDS and join
+// them in K order with the same FMAs as the tile kernel, and round each
+// slot's row as its staging row would be: y has the same bits whichever path
+// a pass takes.
+#include <algorithm>
+
+#include "common.h"
+#include "fp8.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+// Fragment of a 16-row block at block kb of K: lane (l16, lg) holds pieces lg
+// and lg + 4 of its row's 128 bytes, as in the tile kernel.
+__device__ __forceinline__ Fp8Raw frag_at(const uint8_t *row, int kb, int lg)
+{
+    const uint8_t *p = row + (int64_t)kb * FP8_BLOCK + lg * 16;
+    return fp8_raw(*(const uint4 *)p, *(const uint4 *)(p + 64));
+}
+
+// NB weight and MB row blocks a wave; KS waves along K, 8 / KS along the columns.
+template <int NB, int MB, int KS, bool EXACT>
+__global__ __launch_bounds__(512) void fp8_split(Fp8Args p)
+{
+    constexpr int WN = 8 / KS, BN = 16 * NB * WN, BM = 16 * MB, LD = BN + 1;
+    __shared__ float s_acc[KS][BM * LD];
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), ks = w % KS, wn = w / KS;
+    const int ntn = (p.N + BN - 1) / BN;
+    const int mt = blockIdx.x / ntn, n0 = (blockIdx.x - mt * ntn) * BN, row0 = mt * BM;
+    const int nw = n0 + wn * NB * 16;  // the wave's first column
+
+    const uint8_t *wr[NB], *ar[MB];
+    const float *sr[MB];
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+        wr[c] = p.b0 + (int64_t)min(nw + c * 16 + l16, p.N - 1) * p.ldb;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        const int64_t r = min(row0 + m * 16 + l16, p.M - 1);
+        ar[m] = p.a + r * p.lda;
+        sr[m] = p.sa + r * p.KB;
+    }
+    const float *sw = p.s0 + (int64_t)min(nw >> 7, ((p.N + 127) >> 7) - 1) * p.KB;
+    floatx4 acc[NB][MB];
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+            acc[c][m] = floatx4{0, 0, 0, 0};
+    // U blocks of K in flight
+    constexpr int U = NB * MB <= 1 ? 4 : NB * MB <= 4 ? 2 : 1;
+    for (int k0 = ks; k0 < p.KB; k0 += KS * U) {
+        Fp8Raw A[U][NB], B[U][MB];
+        float fw[U], fr[U][MB];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = min(k0 + u * KS, p.KB - 1);
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+                A[u][c] = frag_at(wr[c], kb, lg);
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                B[u][m] = frag_at(ar[m], kb, lg);
+                fr[u][m] = sr[m][kb];
+            }
+            // a block behind the last one is the last one again, with a scale
+            // of 0 (no branch, behind which its loads would be moved)
+            fw[u] = k0 + u * KS < p.KB ? sw[kb] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                const Fp8Frag<EXACT> b(B[u][m]);
+                const float f = fr[u][m] * fw[u];
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    const floatx4 t = mfma_fp8(Fp8Frag<EXACT>(A[u][c]), b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[c][m][i] = fmaf(t[i], f, acc[c][m][i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s_acc[ks][(m * 16 + l16) * LD + (wn * NB + c) * 16 + lg * 4 + i] = acc[c][m][i];
+    __syncthreads();
+    const int rows = min(BM, p.M - row0), cols = min(BN, p.N - n0);
+    for (int i = tid; i < rows * BN; i += 512) {
+        const int r = i / BN, c = i - r * BN;
+        if (c >= cols)
+            continue;
+        float v = s_acc[0][r * LD + c];
+#pragma unroll
+        for (int k = 1; k < KS; ++k)
+            v += s_acc[k][r * LD + c];
+        const int64_t at = (int64_t)(row0 + r) * p.ldy + n0 + c;
+        if (p.out_f32)
+            ((float *)p.y)[at] = v;
+        else
+            ((uint16_t *)p.y)[at] = (uint16_t)cvt_bf2(v, 0.0f);
+    }
+}
+
+template <int NB, int MB, int KS>
+void launch_split(const Fp8Args &p, hipStream_t st)
+{
+    constexpr int BN = 16 * NB * (8 / KS), BM = 16 * MB;
+    const unsigned grid = (unsigned)(((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN));
+    if (p.out_f32)
+        fp8_split<NB, MB, KS, true><<<grid, 512, 0, st>>>(p);
+    else
+        fp8_split<NB, MB, KS, false><<<grid, 512, 0, st>>>(p);
+}
+
+// ---- decode rows of the experts ------------------------------------------------
+
+// The codes of 128 values, two a lane, as the fragment of a one-row operand:
+// the row in column 0 of the MFMA, zeros elsewhere.  `buf`: 128 bytes of LDS of
+// this wave's own.
+__device__ __forceinline__ Fp8Raw one_row_frag(float x0, float x1, uint8_t *buf, int lane, float &scale)
+{
+    float m = row16_max(fmaxf(fabsf(x0), fabsf(x1)));
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const Fp8Block q = fp8_block(m);
+    scale = q.scale;
+    ((uint16_t *)buf)[lane] =
+        (uint16_t)__builtin_amdgcn_cvt_pk_fp8_f32(fp8_quot(x0, q), fp8_quot(x1, q), 0, false);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    const int lg = lane >> 4;
+    Fp8Raw f = fp8_raw(*(const uint4 *)(buf + lg * 16), *(const uint4 *)(buf + 64 + lg * 16));
+    if (lane & 15)
+        f = Fp8Raw{0, 0, 0, 0, 0, 0, 0, 0};
+    return f;
+}
+
+constexpr int GW = 8;  // waves of fp8_pair_gate_up
+
+__global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
+{
+    extern __shared__ float s_t[];  // [2][KB][16] sums of blocks, then [KB] scales of x
+    __shared__ __attribute__((aligned(16))) uint8_t s_code[GW][FP8_BLOCK];
+    const int pair = blockIdx.x / (p.I / 16), n0 = (blockIdx.x - pair * (p.I / 16)) * 16;
+    const int e = p.idx[pair];
+    if ((unsigned)e >= (unsigned)p.E)  // uniform: an empty slot
+        return;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int KB = p.H / FP8_BLOCK;
+    float *s_x = s_t + 2 * KB * 16;
+    const int64_t mat = (int64_t)e * p.I * p.H + (int64_t)(n0 + l16) * p.H;
+    const uint16_t *x = p.x + (int64_t)(pair / p.k) * p.H;
+    constexpr int U = 2;  // blocks of K in flight
+    for (int k0 = w; k0 < KB; k0 += GW * U) {
+        Fp8Raw G[U], V[U];
+        uint32_t xv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = min(k0 + u * GW, KB - 1);
+            xv[u] = *(const uint32_t *)(x + kb * FP8_BLOCK + lane * 2);
+            G[u] = frag_at(p.w_gate + mat, kb, lg);
+            V[u] = frag_at(p.w_up + mat, kb, lg);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = k0 + u * GW;
+            if (kb >= KB)  // uniform
+                break;
+            float sx;
+            const Fp8Frag<false> B(one_row_frag(__uint_as_float(xv[u] << 16),
+                                                __uint_as_float(xv[u] & 0xFFFF0000u), s_code[w], lane, sx));
+            const floatx4 g = mfma_fp8(Fp8Frag<false>(G[u]), B), v = mfma_fp8(Fp8Frag<false>(V[u]), B);
+            if (l16 == 0) {
+                *(floatx4 *)(s_t + kb * 16 + lg * 4) = g;
+                *(floatx4 *)(s_t + (KB + kb) * 16 + lg * 4) = v;
+            }
+            if (lane == 0)
+                s_x[kb] = sx;
+        }
+    }
+    __syncthreads();
+    if (w)
+        return;
+    // lanes 0..15: gate, 16..31: up, in K order
+    const int m = (lane >> 4) & 1;
+    const float *sw = (m ? p.s_up : p.s_gate) + ((int64_t)e * (p.I >> 7) + (n0 >> 7)) * KB;
+    float acc = 0.0f;
+    for (int kb = 0; kb < KB; ++kb)
+        acc = fmaf(s_t[(m * KB + kb) * 16 + l16], s_x[kb] * sw[kb], acc);
+    const float up = __shfl(acc, l16 + 16);
+    if (lane < 16)
+        p.h[(int64_t)pair * p.I + n0 + lane] = silu(acc) * up;
+}
+
+constexpr int DW = 16;  // waves of fp8_token_down, and most slots of a token
+
+__global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
+{
+    extern __shared__ float s_t[];  // [k][KB][16] sums of blocks, then [k][KB] scales of h
+    __shared__ __attribute__((aligned(16))) uint8_t s_code[DW][FP8_BLOCK];
+    __shared__ float s_o[DW][16];
+    const int t = blockIdx.x / (p.H / 16), n0 = (blockIdx.x - t * (p.H / 16)) * 16;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int KB = p.I / FP8_BLOCK, units = p.k * KB;
+    float *s_h = s_t + units * 16;
+    constexpr int U = 2;  // units in flight
+    for (int u0 = w; u0 < units; u0 += DW * U) {
+        Fp8Raw W[U];
+        float2 hv[U];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = min(u0 + u * DW, units - 1), j = q / KB, kb = q - j * KB;
+            const int e = p.idx[t * p.k + j];
+            live[u] = u0 + u * DW < units && (unsigned)e < (unsigned)p.E;
+            if (live[u]) {  // uniform
+                hv[u] = *(const float2 *)(p.h + (int64_t)(t * p.k + j) * p.I + kb * FP8_BLOCK + lane * 2);
+                W[u] = frag_at(p.w_down + ((int64_t)e * p.H + n0 + l16) * p.I, kb, lg);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!live[u])
+                continue;
+            const int q = u0 + u * DW;
+            float sh;
+            const Fp8Frag<false> B(one_row_frag(hv[u].x, hv[u].y, s_code[w], lane, sh));
+            const floatx4 o = mfma_fp8(Fp8Frag<false>(W[u]), B);
+            if (l16 == 0)
+                *(floatx4 *)(s_t + q * 16 + lg * 4) = o;
+            if (lane == 0)
+                s_h[q] = sh;
+        }
+    }
+    __syncthreads();
+    // wave j: slot j's 16 outputs in K order, rounded as a staging row is
+    if (w < p.k) {
+        const int e = p.idx[t * p.k + w];
+        if ((unsigned)e < (unsigned)p.E) {
+            const float *sw = p.s_down + ((int64_t)e * (p.H >> 7) + (n0 >> 7)) * KB;
+            float acc = 0.0f;
+            for (int kb = 0; kb < KB; ++kb)
+                acc = fmaf(s_t[(w * KB + kb) * 16 + l16], s_h[w * KB + kb] * sw[kb], acc);
+            uint32_t ex = stage_exponent(acc);
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1)
+                ex = max(ex, (uint32_t)__shfl_xor((int)ex, d));
+            ex = max(ex, STAGE_MIN_EXP);
+            if (lane < 16)
+                s_o[w][lane] = (float)(_Float16)(acc * stage_pack(ex)) * stage_unpack(ex);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        float y = 0.0f;
+        for (int j = 0; j < p.k; ++j)
+            if ((unsigned)p.idx[t * p.k + j] < (unsigned)p.E)
+                y = fmaf(p.topk_w[t * p.k + j], s_o[j][threadIdx.x], y);
+        p.y[(int64_t)t * p.H + n0 + threadIdx.x] = (uint16_t)cvt_bf2(y, 0.0f);
+    }
+}
+
+}  // namespace
+
+// One matrix whose 64-row tiles of 256 columns would leave CUs without work.
+bool fp8_split_ok(const Fp8Args &p)
+{
+    return !p.tiles && !p.offsets && (int64_t)((p.M + 63) / 64) * ((p.N + 255) / 256) < 256;
+}
+
+void launch_fp8_split(const Fp8Args &p, hipStream_t st)
+{
+    if (p.M <= 16)
+        launch_split<1, 1, 8>(p, st);
+    else if (p.M <= 32)
+        launch_split<2, 2, 8>(p, st);
+    else
+        launch_split<2, 4, 4>(p, st);
+}
+
+// Decode rows: LDS holds a block sum for each unit of work.
+bool fp8_decode_ok(int T, int H, int k, int I)
+{
+    return T <= 8 && H / FP8_BLOCK <= 256 && (int64_t)k * (I / FP8_BLOCK) <= 512;
+}
+
+void launch_fp8_decode(const Fp8Decode &p, hipStream_t st)
+{
+    const int kb = p.H / FP8_BLOCK, units = p.k * (p.I / FP8_BLOCK);
+    fp8_pair_gate_up<<<(unsigned)(p.T * p.k * (p.I / 16)), 64 * GW, (size_t)kb * 33 * 4, st>>>(p);
+    fp8_token_down<<<(unsigned)(p.T * (p.H / 16)), 64 * DW, (size_t)units * 17 * 4, st>>>(p);
+}
+
+}  // namespace moe

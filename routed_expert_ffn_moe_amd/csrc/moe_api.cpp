@@ -158,7 +158,7 @@ int check_weights(const moe_shape_t *s, const moe_weights_t *w)
 // Workspace layout of one pass of Tc tokens.
 struct Layout {
     size_t logits, wts, blk, counts, offsets, row_src, row_tok, row_of, tiles_gu, ntiles, tiles_dc,
-        items_gu, items_dc, h, stage, xq, f8_x, f8_sx, f8_sh, total;
+        items_gu, items_dc, h, stage, xq, f8_x, f8_sx, f8_sh, f8_exp, total;
     bool has_xq;  // MXFP4 passes routed by router_small: x quantised once per token
     int max_tiles_gu, max_tiles_dc, bm_gu, bm_dc, ntn_gu, ntn_dc, wrows_gu, wrows_dc;
     int64_t logit_floats;  // capacity of the logits area
@@ -186,6 +186,13 @@ int max_tiles(int64_t Tc, const moe_shape_t *s, int bm)
     if (s->I_shared > 0)
         n += cdiv(Tc, bm);
     return (int)n;
+}
+
+// Passes of few rows with FP8 experts (Tc: tokens of a full pass) go pair by
+// pair: gate and up into fp32 rows of h, then down and the combine.
+bool fp8_decode(const moe_shape_t *s, int Tc)
+{
+    return s->w_dtype == MOE_FP8 && moe::fp8_decode_ok(Tc, s->H, s->top_k, s->I);
 }
 
 Layout layout(const moe_shape_t *s, int Tc)
@@ -231,12 +238,14 @@ Layout layout(const moe_shape_t *s, int Tc)
     L.tiles_dc = take((size_t)L.max_tiles_dc * sizeof(moe::Tile));
     L.items_gu = take((size_t)L.max_tiles_gu * L.ntn_gu * 16);
     L.items_dc = take((size_t)L.max_tiles_dc * L.ntn_dc * 16);
-    L.h = take((size_t)rows * ldh * (f8 ? 1 : esz));  // FP8: codes, their scales below
+    // FP8: codes, their scales below; the fp32 rows of decode passes
+    L.h = take((size_t)rows * ldh * (!f8 ? esz : fp8_decode(s, Tc) ? 4 : 1));
     L.stage = take((size_t)rows * s->H * esz);
     if (f8) {  // the token rows as codes, and the scales of x and h
         L.f8_x = take((size_t)Tc * s->H);
         L.f8_sx = take((size_t)Tc * (s->H / moe::FP8_K) * 4);
         L.f8_sh = take((size_t)rows * (s->I / moe::FP8_K) * 4);
+        L.f8_exp = take((size_t)rows * (s->H / 16));  // exponents of the staging rows
     }
     // decode, verify and other short passes with MXFP4 experts
     const int act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;
@@ -460,6 +469,7 @@ int fp8_products(const moe_shape_t *s, const moe_weights_t *w, const void *x, in
     d.tiles = (const moe::Tile *)(ws + L.tiles_dc);
     d.ntiles = (const int32_t *)(ws + L.ntiles) + 1;
     d.y = ws + L.stage;
+    d.exps = (uint8_t *)(ws + L.f8_exp);
     d.lda = d.ldb = s->I;
     d.ldy = s->H;
     d.bstride = (int64_t)s->H * s->I;
@@ -474,6 +484,31 @@ int fp8_products(const moe_shape_t *s, const moe_weights_t *w, const void *x, in
     return launched("down");
 }
 
+int fp8_decode_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, void *y, int n,
+                    const int32_t *idx, const float *wts, char *ws, const Layout &L, hipStream_t st)
+{
+    StageScope sc(2, st);
+    moe::Fp8Decode d{};
+    d.x = (const uint16_t *)x;
+    d.w_gate = (const uint8_t *)w->w_gate;
+    d.w_up = (const uint8_t *)w->w_up;
+    d.w_down = (const uint8_t *)w->w_down;
+    d.s_gate = (const float *)w->s_gate;
+    d.s_up = (const float *)w->s_up;
+    d.s_down = (const float *)w->s_down;
+    d.idx = idx;
+    d.topk_w = wts;
+    d.h = (float *)(ws + L.h);
+    d.y = (uint16_t *)y;
+    d.T = n;
+    d.H = s->H;
+    d.E = s->E;
+    d.k = s->top_k;
+    d.I = s->I;
+    moe::launch_fp8_decode(d, st);
+    return launched("fp8 decode");
+}
+
 // The experts of one permuted pass (Tc: tokens of a full pass) and the combine.
 // With `given` the routing is the caller's, whose slots may be empty.
 int expert_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, void *y, int n, int Tc,
@@ -481,6 +516,8 @@ int expert_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, voi
                 hipStream_t st)
 {
     int rc;
+    if (fp8_decode(s, Tc))
+        return fp8_decode_pass(s, w, x, y, n, idx, wts, ws, L, st);
     if (s->w_dtype == MOE_FP8) {
         if ((rc = fp8_products(s, w, x, n, ws, L, st)))
             return rc;
@@ -549,9 +586,10 @@ int expert_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, voi
     cb.k = s->top_k;
     cb.shared = s->I_shared > 0;
     cb.act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;
+    cb.exps = s->w_dtype == MOE_FP8 ? (const uint8_t *)(ws + L.f8_exp) : nullptr;
     {
         StageScope sc(4, st);
-        if (given)
+        if (given || cb.exps)
             moe::launch_combine_given(cb, st);
         else
             moe::launch_combine(cb, st);
@@ -810,6 +848,11 @@ int moe_experts(const moe_shape_t *s, const moe_weights_t *w, const void *x,
         char *yc = (char *)y + (int64_t)c0 * s->H * esz;
         const int32_t *idx = topk_idx + (int64_t)c0 * s->top_k;
         const float *wts = topk_w + (int64_t)c0 * s->top_k;
+        if (fp8_decode(s, Tc)) {  // straight from the pairs, no permutation
+            if ((rc = fp8_decode_pass(s, w, xc, yc, n, idx, wts, wsb, L, st)))
+                return rc;
+            continue;
+        }
         Layout Lw = L;
         Lw.max_tiles_gu = max_tiles(n, s, L.bm_gu);
         Lw.max_tiles_dc = max_tiles(n, s, L.bm_dc);
