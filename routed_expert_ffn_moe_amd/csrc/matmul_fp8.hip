@@ -614,6 +614,8 @@ void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st)
         launch_bm<EPI_STAGE>(p, bm, st);
     else if (fp8_split_ok(p))
         launch_fp8_split(p, st);
+    else if (!p.offsets && bm == 64 && (int64_t)p.mtiles * ((p.N + 255) / 256) < 256)
+        launch_cfg<2, 64, 2, 2, 3, EPI_PLAIN>(p, st);  // tiles of 64 columns, to fill the chip
     else
         launch_bm<EPI_PLAIN>(p, bm, st);
 }

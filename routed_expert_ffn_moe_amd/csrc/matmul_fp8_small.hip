@@ -159,11 +159,32 @@ __device__ __forceinline__ Fp8Raw one_row_frag(float x0, float x1, uint8_t *buf,
     return f;
 }
 
+// One output from the sums of its KB blocks (16 apart) and their scales, in K order.
+__device__ __forceinline__ float chain(const float *t, const float *f, int KB)
+{
+    float acc = 0.0f;
+    int kb = 0;
+    for (; kb + 8 <= KB; kb += 8) {
+        float tv[8], fv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // the reads in flight together
+            tv[i] = t[(kb + i) * 16];
+            fv[i] = f[kb + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc = fmaf(tv[i], fv[i], acc);
+    }
+    for (; kb < KB; ++kb)
+        acc = fmaf(t[kb * 16], f[kb], acc);
+    return acc;
+}
+
 constexpr int GW = 8;  // waves of fp8_pair_gate_up
 
 __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
 {
-    extern __shared__ float s_t[];  // [2][KB][16] sums of blocks, then [KB] scales of x
+    extern __shared__ float s_t[];  // [2][KB][16] sums of blocks, then [2][KB] their scales
     __shared__ __attribute__((aligned(16))) uint8_t s_code[GW][FP8_BLOCK];
     const int pair = blockIdx.x / (p.I / 16), n0 = (blockIdx.x - pair * (p.I / 16)) * 16;
     const int e = p.idx[pair];
@@ -172,19 +193,23 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KB = p.H / FP8_BLOCK;
-    float *s_x = s_t + 2 * KB * 16;
+    float *s_f = s_t + 2 * KB * 16;
+    const int64_t sc = ((int64_t)e * (p.I >> 7) + (n0 >> 7)) * KB;
     const int64_t mat = (int64_t)e * p.I * p.H + (int64_t)(n0 + l16) * p.H;
     const uint16_t *x = p.x + (int64_t)(pair / p.k) * p.H;
     constexpr int U = 2;  // blocks of K in flight
     for (int k0 = w; k0 < KB; k0 += GW * U) {
         Fp8Raw G[U], V[U];
         uint32_t xv[U];
+        float fg[U], fv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = min(k0 + u * GW, KB - 1);
             xv[u] = *(const uint32_t *)(x + kb * FP8_BLOCK + lane * 2);
             G[u] = frag_at(p.w_gate + mat, kb, lg);
             V[u] = frag_at(p.w_up + mat, kb, lg);
+            fg[u] = p.s_gate[sc + kb];
+            fv[u] = p.s_up[sc + kb];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -199,19 +224,18 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
                 *(floatx4 *)(s_t + kb * 16 + lg * 4) = g;
                 *(floatx4 *)(s_t + (KB + kb) * 16 + lg * 4) = v;
             }
-            if (lane == 0)
-                s_x[kb] = sx;
+            if (lane == 0) {
+                s_f[kb] = sx * fg[u];
+                s_f[KB + kb] = sx * fv[u];
+            }
         }
     }
     __syncthreads();
     if (w)
         return;
-    // lanes 0..15: gate, 16..31: up, in K order
+    // lanes 0..15: gate, 16..31: up
     const int m = (lane >> 4) & 1;
-    const float *sw = (m ? p.s_up : p.s_gate) + ((int64_t)e * (p.I >> 7) + (n0 >> 7)) * KB;
-    float acc = 0.0f;
-    for (int kb = 0; kb < KB; ++kb)
-        acc = fmaf(s_t[(m * KB + kb) * 16 + l16], s_x[kb] * sw[kb], acc);
+    const float acc = chain(s_t + m * KB * 16 + l16, s_f + m * KB, KB);
     const float up = __shfl(acc, l16 + 16);
     if (lane < 16)
         p.h[(int64_t)pair * p.I + n0 + lane] = silu(acc) * up;
@@ -221,19 +245,24 @@ constexpr int DW = 16;  // waves of fp8_token_down, and most slots of a token
 
 __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
 {
-    extern __shared__ float s_t[];  // [k][KB][16] sums of blocks, then [k][KB] scales of h
+    extern __shared__ float s_t[];  // [k][KB][16] sums of blocks, then [k][KB] their scales
     __shared__ __attribute__((aligned(16))) uint8_t s_code[DW][FP8_BLOCK];
-    __shared__ float s_o[DW][16];
+    __shared__ float s_o[DW][16], s_w[DW];
+    __shared__ int s_live[DW];
     const int t = blockIdx.x / (p.H / 16), n0 = (blockIdx.x - t * (p.H / 16)) * 16;
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KB = p.I / FP8_BLOCK, units = p.k * KB;
-    float *s_h = s_t + units * 16;
-    constexpr int U = 2;  // units in flight
+    float *s_f = s_t + units * 16;
+    // this wave's slot of the combine, loaded early
+    const int my_e = w < p.k ? p.idx[t * p.k + w] : -1;
+    const float my_w = w < p.k ? p.topk_w[t * p.k + w] : 0.0f;
+    constexpr int U = 4;  // units in flight
     for (int u0 = w; u0 < units; u0 += DW * U) {
         Fp8Raw W[U];
         float2 hv[U];
         bool live[U];
+        float fw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int q = min(u0 + u * DW, units - 1), j = q / KB, kb = q - j * KB;
@@ -242,6 +271,7 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
             if (live[u]) {  // uniform
                 hv[u] = *(const float2 *)(p.h + (int64_t)(t * p.k + j) * p.I + kb * FP8_BLOCK + lane * 2);
                 W[u] = frag_at(p.w_down + ((int64_t)e * p.H + n0 + l16) * p.I, kb, lg);
+                fw[u] = p.s_down[((int64_t)e * (p.H >> 7) + (n0 >> 7)) * KB + kb];
             }
         }
 #pragma unroll
@@ -255,53 +285,52 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
             if (l16 == 0)
                 *(floatx4 *)(s_t + q * 16 + lg * 4) = o;
             if (lane == 0)
-                s_h[q] = sh;
+                s_f[q] = sh * fw[u];
         }
     }
     __syncthreads();
-    // wave j: slot j's 16 outputs in K order, rounded as a staging row is
-    if (w < p.k) {
-        const int e = p.idx[t * p.k + w];
-        if ((unsigned)e < (unsigned)p.E) {
-            const float *sw = p.s_down + ((int64_t)e * (p.H >> 7) + (n0 >> 7)) * KB;
-            float acc = 0.0f;
-            for (int kb = 0; kb < KB; ++kb)
-                acc = fmaf(s_t[(w * KB + kb) * 16 + l16], s_h[w * KB + kb] * sw[kb], acc);
-            uint32_t ex = stage_exponent(acc);
+    // wave j: slot j's 16 outputs, rounded as a staging row is
+    const bool mine = (unsigned)my_e < (unsigned)p.E;
+    if (mine) {
+        const float acc = chain(s_t + w * KB * 16 + l16, s_f + w * KB, KB);
+        uint32_t ex = stage_exponent(acc);
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1)
-                ex = max(ex, (uint32_t)__shfl_xor((int)ex, d));
-            ex = max(ex, STAGE_MIN_EXP);
-            if (lane < 16)
-                s_o[w][lane] = (float)(_Float16)(acc * stage_pack(ex)) * stage_unpack(ex);
-        }
+        for (int d = 1; d < 16; d <<= 1)
+            ex = max(ex, (uint32_t)__shfl_xor((int)ex, d));
+        ex = max(ex, STAGE_MIN_EXP);
+        if (lane < 16)
+            s_o[w][lane] = (float)(_Float16)(acc * stage_pack(ex)) * stage_unpack(ex);
+    }
+    if (lane == 0) {
+        s_live[w] = mine;
+        s_w[w] = my_w;
     }
     __syncthreads();
     if (threadIdx.x < 16) {
         float y = 0.0f;
         for (int j = 0; j < p.k; ++j)
-            if ((unsigned)p.idx[t * p.k + j] < (unsigned)p.E)
-                y = fmaf(p.topk_w[t * p.k + j], s_o[j][threadIdx.x], y);
+            if (s_live[j])
+                y = fmaf(s_w[j], s_o[j][threadIdx.x], y);
         p.y[(int64_t)t * p.H + n0 + threadIdx.x] = (uint16_t)cvt_bf2(y, 0.0f);
     }
 }
 
 }  // namespace
 
-// One matrix whose 64-row tiles of 256 columns would leave CUs without work.
+// One matrix of few rows.  (A wave's fragment reads fetch 38 bytes a
+// nanosecond per CU from the caches, copies to LDS 130, so rows that many
+// columns share are better copied: 601 x 2050 x 776 took 15 us this way.)
 bool fp8_split_ok(const Fp8Args &p)
 {
-    return !p.tiles && !p.offsets && (int64_t)((p.M + 63) / 64) * ((p.N + 255) / 256) < 256;
+    return !p.tiles && !p.offsets && p.M <= 32 && (p.N + 255) / 256 < 256;
 }
 
 void launch_fp8_split(const Fp8Args &p, hipStream_t st)
 {
     if (p.M <= 16)
         launch_split<1, 1, 8>(p, st);
-    else if (p.M <= 32)
-        launch_split<2, 2, 8>(p, st);
     else
-        launch_split<2, 4, 4>(p, st);
+        launch_split<2, 2, 8>(p, st);
 }
 
 // Decode rows: LDS holds a block sum for each unit of work.
@@ -313,7 +342,7 @@ bool fp8_decode_ok(int T, int H, int k, int I)
 void launch_fp8_decode(const Fp8Decode &p, hipStream_t st)
 {
     const int kb = p.H / FP8_BLOCK, units = p.k * (p.I / FP8_BLOCK);
-    fp8_pair_gate_up<<<(unsigned)(p.T * p.k * (p.I / 16)), 64 * GW, (size_t)kb * 33 * 4, st>>>(p);
+    fp8_pair_gate_up<<<(unsigned)(p.T * p.k * (p.I / 16)), 64 * GW, (size_t)kb * 34 * 4, st>>>(p);
     fp8_token_down<<<(unsigned)(p.T * (p.H / 16)), 64 * DW, (size_t)units * 17 * 4, st>>>(p);
 }
 

@@ -10,7 +10,11 @@
 //
 // The order is that of the keys in 64 bits: 256 experts a token leave gaps
 // between neighbouring keys that fp32 rounding (6e-8 near 1) closes for about
-// one token in ten thousand, and another expert would run.
+// one token in ten thousand, and another expert would run.  So a token is
+// routed in fp32 and the gaps that its selection rests on are checked against
+// the bound of the fp32 keys' errors; the few tokens with a gap too small (1%
+// with a bias, none without one unless the scores saturate) are routed again
+// in 64 bits.
 //
 // An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is
 // masked: it ranks behind every other one (among masked ones by index) and
@@ -18,9 +22,11 @@
 // as the largest finite value.  Where the selected scores sum to 0 all
 // weights are 0.
 //
-// One wave per token.
+// One wave per token.  Bound by its instructions: the k selection rounds are a
+// wave maximum each.  T=8192, E=384, bias: all in 64 bits 25 us.
 #include "common.h"
 #include "kernels.h"
+#include "topk.h"
 
 namespace moe {
 
@@ -65,14 +71,20 @@ __device__ __forceinline__ float logit_at(const void *l, int64_t i)
     return BF16 ? bf2f(((const uint16_t *)l)[i]) : ((const float *)l)[i];
 }
 
-template <int PER, bool BF16>
-__global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
+__device__ __forceinline__ void wave_lds_sync()
 {
-    extern __shared__ double s_key[];  // [waves][E], grouped selection only
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int t = blockIdx.x * SEL_WAVES + wv;
-    if (t >= a.T)  // uniform in the wave; no workgroup barrier below
-        return;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
+constexpr float LARGEST = 3.4028234e38f;
+
+// Token t in 64 bits: lane r < k ends with the expert of rank r and its weight.
+template <int PER, bool BF16>
+__device__ __forceinline__ void select_exact(const SelectArgs &a, int t, double *row, int &my_e, float &my_w)
+{
+    const int lane = threadIdx.x & 63;
     double key[PER], sc[PER];
     float l[PER];
     bool masked[PER];
@@ -82,7 +94,7 @@ __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
         const int e = lane + 64 * i;
         l[i] = e < a.E ? logit_at<BF16>(a.logits, (int64_t)t * a.ld + e) : -INFINITY;
         masked[i] = !(l[i] > -INFINITY);
-        l[i] = fminf(l[i], 3.4028234e38f);
+        l[i] = fminf(l[i], LARGEST);
         if (!masked[i])
             mx = fmaxf(mx, l[i]);
     }
@@ -108,7 +120,7 @@ __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
         const int e = lane + 64 * i;
         const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
         masked[i] |= !(b > -INFINITY);
-        key[i] = masked[i] ? -INFINITY : sc[i] + (double)fminf(b, 3.4028234e38f);
+        key[i] = masked[i] ? -INFINITY : sc[i] + (double)fminf(b, LARGEST);
         sc[i] = masked[i] ? 0.0 : sc[i];
     }
     uint32_t taken = 0;  // slots of this lane that cannot be selected
@@ -117,14 +129,11 @@ __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
         if (lane + 64 * i >= a.E)
             taken |= 1u << i;
     if (a.n_group > 1) {
-        double *row = s_key + (int64_t)wv * a.E;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (lane + 64 * i < a.E)
                 row[lane + 64 * i] = key[i];
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+        wave_lds_sync();
         const int gs = a.E / a.n_group;
         double val = -INFINITY;
         if (lane < a.n_group) {
@@ -150,7 +159,7 @@ __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
             if (!((open >> ((lane + 64 * i) / gs & 63)) & 1))
                 taken |= 1u << i;
     }
-    int my_e = 0;
+    my_e = 0;
     double my_s = 0.0, sum = 0.0;
     for (int r = 0; r < a.k; ++r) {
         double k = -INFINITY;
@@ -178,11 +187,185 @@ __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
             my_s = s;
         }
     }
+    const double d = a.renorm ? (sum > 0.0 ? my_s / sum : 0.0) : my_s;
+    my_w = (float)(d * (double)a.scale);
+}
+
+// Twice the bound of a fp32 key's error, in units of 2^-24.  Sigmoid: the
+// exponential's argument is off by |l| (s (1 - s) |l| <= 0.23 in the score), the
+// exponential and the reciprocal by 2 each.  Softmax: difference and argument
+// 2 |l - m| (p |l - m| <= 0.37), the exponential 2, the products 2, and the sum
+// over the experts: their own errors weighted by p (2 |l - m| averages to
+// 2 ln 1024 = 14 at most, and 2) and at most 23 additions.  Below 64 together,
+// with the key's own sum.
+__device__ __forceinline__ float key_slack(float k) { return 0x1p-17f * fmaxf(1.0f, fabsf(k)); }
+
+// Whether the keys in 64 bits of two logits l > m (no bias) are sure to differ:
+// their ratio is 1 + (l - m) (1 - s) at least, s = 0 for softmax, against 2^-52
+// roundings, and neither may underflow.  `top`: the largest logit, for softmax.
+__device__ __forceinline__ bool logits_apart(float l, float m, float top, bool softmax)
+{
+    const float d = l - m;
+    return softmax ? d > 1e-13f && m - top > -600.0f : d * __expf(-fmaxf(l, 0.0f)) > 1e-13f && m > -600.0f;
+}
+
+// Token t in fp32; false if a gap is too small to be sure of the order.
+template <int PER, bool BF16>
+__device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *row, int &my_e, float &my_w)
+{
+    const int lane = threadIdx.x & 63;
+    const bool bias = a.bias != nullptr;
+    const bool grouped = a.n_group > 1;
+    // scores of all experts: for keys with a bias, sums of two keys, and the
+    // softmax's own weights
+    const bool all_scores = bias || (grouped && a.group_top2);
+    float l[PER], key[PER];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 64 * i;
+        const float v = e < a.E ? logit_at<BF16>(a.logits, (int64_t)t * a.ld + e) : -INFINITY;
+        l[i] = v > -INFINITY ? fminf(v, LARGEST) : -INFINITY;
+        top = fmaxf(top, l[i]);
+    }
+    float inv_z = 0.0f;
+    if (a.softmax) {
+        top = key_value(wave_max_u32(order_key(top)));
+        if (all_scores || !a.renorm) {
+            float z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                z += l[i] > -INFINITY ? __expf(l[i] - top) : 0.0f;
+#pragma unroll
+            for (int d = 32; d; d >>= 1)
+                z += __shfl_xor(z, d);
+            inv_z = z > 0.0f ? 1.0f / z : 0.0f;
+        }
+    }
+    auto score = [&](float v) {
+        return a.softmax ? __expf(v - top) * inv_z : __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+    };
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 64 * i;
+        key[i] = l[i];
+        if (bias) {
+            const float b = e < a.E ? a.bias[e] : 0.0f;
+            key[i] = l[i] > -INFINITY && b > -INFINITY ? score(l[i]) + fminf(b, LARGEST) : -INFINITY;
+        }
+    }
+    bool sure = true;
+    uint64_t open = ~0ull;
+    const int gs = a.E / a.n_group;
+    if (grouped) {
+        // a group's two largest keys: `per` lanes a group, then their halves joined
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 64 * i < a.E)
+                row[lane + 64 * i] = key[i];
+        wave_lds_sync();
+        const int sh = 31 - __clz(64 / a.n_group), per = 1 << sh;
+        const int g = lane >> sh;
+        float m1 = -INFINITY, m2 = -INFINITY;
+        if (g < a.n_group)
+            for (int i = lane & (per - 1); i < gs; i += per) {
+                const float v = row[g * gs + i];
+                m2 = fmaxf(m2, fminf(m1, v));
+                m1 = fmaxf(m1, v);
+            }
+        for (int d = 1; d < per; d <<= 1) {
+            const float o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+            m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+            m1 = fmaxf(m1, o1);
+        }
+        float val = m1;
+        if (a.group_top2) {
+            if (!bias && m1 > -INFINITY)
+                val = score(m1);
+            if (m2 > -INFINITY)
+                val += bias ? m2 : score(m2);
+        }
+        wave_lds_sync();
+        if (g < a.n_group && (lane & (per - 1)) == 0)
+            row[g] = val;
+        wave_lds_sync();
+        // rank by counting; lane g < n_group for group g
+        const float mine = lane < a.n_group ? row[lane] : -INFINITY;
+        int rank = 0;
+        for (int j = 0; j < a.n_group; ++j) {
+            const float o = row[j];
+            rank += o > mine || (o == mine && j < lane) ? 1 : 0;
+        }
+        const bool in = lane < a.n_group && rank < a.topk_group;
+        open = __ballot(in);
+        // the gap between the last open and the first closed group
+        const float lo = -key_value(wave_max_u32(order_key(in ? -mine : -INFINITY)));
+        const float hi = key_value(wave_max_u32(order_key(lane < a.n_group && !in ? mine : -INFINITY)));
+        if (hi > -INFINITY)  // (groups of masked experts only are in order)
+            sure = a.group_top2 ? lo - hi > 2.0f * key_slack(fmaxf(fabsf(lo), fabsf(hi)))
+                   : bias       ? lo - hi > key_slack(fmaxf(fabsf(lo), fabsf(hi)))
+                                : logits_apart(lo, hi, top, a.softmax);
+    }
+    uint32_t ok[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 64 * i;
+        ok[i] = e < a.E && (!grouped || (open >> (e / gs & 63)) & 1) ? order_key(key[i]) : 0u;
+    }
+    // one more than k: the gap behind the last one
+    uint32_t my_k;
+    wave_topk_keys<PER>(ok, min(a.k + 1, a.E), my_e, my_k);
+    const bool have = my_k != 0u;
+    const float kv = have ? key_value(my_k) : -INFINITY;
+    float lv = kv, bv = 0.0f;
+    if (bias && lane <= a.k && have) {
+        lv = logit_at<BF16>(a.logits, (int64_t)t * a.ld + my_e);
+        lv = lv > -INFINITY ? fminf(lv, LARGEST) : -INFINITY;
+        bv = a.bias[my_e];
+    }
+    const float nk = __shfl_down(kv, 1), nl = __shfl_down(lv, 1), nb = __shfl_down(bv, 1);
+    bool fine = true;
+    if (lane < a.k && nk > -INFINITY)
+        fine = (lv == nl && bv == nb) ||
+               (bias ? kv - nk > key_slack(kv) : logits_apart(kv, nk, top, a.softmax));
+    sure &= __all(fine);
+    // weights; a masked expert (key -inf) has none
+    const bool live = lane < a.k && kv > -INFINITY;
+    float s;
+    if (a.softmax) {
+        const float base = a.renorm ? key_value(wave_max_u32(order_key(live ? lv : -INFINITY))) : top;
+        s = live ? expf(lv - base) * (a.renorm ? 1.0f : inv_z) : 0.0f;
+    } else {
+        s = live ? 1.0f / (1.0f + expf(-lv)) : 0.0f;
+    }
+    if (a.renorm) {
+        float sum = s;
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1)
+            sum += __shfl_xor(sum, d);
+        s = sum > 0.0f ? s / sum : 0.0f;
+    }
+    my_w = s * a.scale;
+    return sure;
+}
+
+template <int PER, bool BF16>
+__global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
+{
+    extern __shared__ double s_key[];  // [waves][E], grouped selection only
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int t = blockIdx.x * SEL_WAVES + wv;
+    if (t >= a.T)  // uniform in the wave; no workgroup barrier below
+        return;
+    double *row = s_key + (int64_t)wv * a.E;
+    int my_e;
+    float my_w;
+    if (!select_fast<PER, BF16>(a, t, (float *)row, my_e, my_w))  // uniform
+        select_exact<PER, BF16>(a, t, row, my_e, my_w);
     if (lane < a.k) {
-        const double d = a.renorm ? (sum > 0.0 ? my_s / sum : 0.0) : my_s;
         a.idx[(int64_t)t * a.k + lane] = my_e;
         if (a.w)
-            a.w[(int64_t)t * a.k + lane] = (float)(d * (double)a.scale);
+            a.w[(int64_t)t * a.k + lane] = my_w;
     }
 }
 
@@ -210,6 +393,8 @@ void launch_select(const SelectArgs &a, hipStream_t st)
         launch_per<2>(a, st);
     else if (per <= 4)
         launch_per<4>(a, st);
+    else if (per <= 6)
+        launch_per<6>(a, st);
     else if (per <= 8)
         launch_per<8>(a, st);
     else

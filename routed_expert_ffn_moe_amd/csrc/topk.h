@@ -51,25 +51,21 @@ __device__ __forceinline__ int wave_min_i32(int v)
     return __builtin_amdgcn_readlane(m, 63);
 }
 
-// Top-k of one token's router logits, selected by one wave.  Lane l holds
-// logits l, l+64, ... (E <= 64*PER) in val, sorted once into descending
-// order.  k rounds each take the best remaining (logit, expert) pair of the
-// wave, the head of one lane's list: larger logit first, equal logits by
-// lower expert index; NaN ranks as -inf.  So the pairs come out in rank
+// Top-k of one token's keys (order_key, 0 for what cannot be selected), by
+// one wave.  Lane l holds the keys of experts l, l+64, ..., sorted once into
+// descending order.  k rounds each take the best remaining (logit, expert) pair of the
+// wave, the head of one lane's list: larger key first, equal keys by
+// lower expert index.  So the pairs come out in rank
 // order: lane r < k ends with the expert of rank r in my_e and its key in
 // my_k (the other lanes with 0).
 template <int PER>
-__device__ __forceinline__ void wave_topk_select(const float (&val)[PER], int E, int k, int &my_e,
-                                                 uint32_t &my_k)
+__device__ __forceinline__ void wave_topk_keys(uint32_t (&key)[PER], int k, int &my_e, uint32_t &my_k)
 {
     const int lane = threadIdx.x & 63;
-    uint32_t key[PER];  // 0 for the slots past E: below every logit
     int slot[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        key[i] = lane + 64 * i < E ? order_key(val[i]) : 0u;
+    for (int i = 0; i < PER; ++i)
         slot[i] = i;
-    }
     // this lane's list in selection order (odd-even transposition sort; a
     // later slot moves ahead only with a strictly larger key)
 #pragma unroll
@@ -110,6 +106,19 @@ __device__ __forceinline__ void wave_topk_select(const float (&val)[PER], int E,
             key[PER - 1] = 0u;
         }
     }
+}
+
+// The same for logits (E <= 64*PER): NaN ranks as -inf.
+template <int PER>
+__device__ __forceinline__ void wave_topk_select(const float (&val)[PER], int E, int k, int &my_e,
+                                                 uint32_t &my_k)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t key[PER];  // 0 for the slots past E: below every logit
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        key[i] = lane + 64 * i < E ? order_key(val[i]) : 0u;
+    wave_topk_keys<PER>(key, k, my_e, my_k);
 }
 
 // The weights of a selection (wave_topk_select's my_e, my_k): the softmax
