@@ -240,8 +240,8 @@ int moe_select(const moe_select_t *select, const void *logits, const float *bias
  * FFN of expert topk_idx[t, j] on x_t, in j order.  Every weight type of
  * moe_forward; the weights' router_w and router_bias are not used (NULL is
  * fine) and I_shared must be 0 (MOE_EUNSUPPORTED otherwise).  A slot whose
- * index is outside 0..E-1 (say -1) is empty: it costs and adds nothing, and a
- * token with empty slots only gets zeros.  An expert may occur more than once
+ * index is outside 0..E-1 (say -1) is empty: it adds nothing, whatever its
+ * weight, and a token with empty slots only gets zeros.  An expert may occur more than once
  * in a token.  Workspace and chunk_T as for moe_forward; x and y 16-byte
  * aligned, topk_idx and topk_w 4-byte. */
 int moe_experts(const moe_shape_t *shape, const moe_weights_t *w, const void *x,

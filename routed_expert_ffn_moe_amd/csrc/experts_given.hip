@@ -2,7 +2,7 @@
 // stage[row of (t, j)] in j order, fp32 sum, rounded once, as in moe_forward;
 // an empty slot (row_of < 0) adds nothing whatever its weight, and a token
 // with empty slots only gets zeros.  Rows of the FP8 experts are half values
-// under an exponent for each 16 columns (fp8.h).
+// under an exponent for each 8 columns (fp8.h).
 #include "common.h"
 #include "fp8.h"
 #include "kernels.h"
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void combine_given(const void *__restrict__ st
         if (row[j] >= 0) {
             v[j] = *(const uint4 *)((const char *)stage + ((int64_t)row[j] * H + c) * (16 / W));
             if constexpr (ROWS == ROWS_FP8)
-                ex[j] = exps[((int64_t)row[j] * H + c) >> 4];
+                ex[j] = exps[((int64_t)row[j] * H + c) >> 3];
         }
     float acc[W];
 #pragma unroll

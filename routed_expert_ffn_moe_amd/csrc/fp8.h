@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t fp8x4(float x0, float x1, float x2, float x3
 }
 
 // Staging rows of the FP8 experts' outputs: half precision under one exponent
-// byte for each 16 columns, the largest of their finite values scaled to
+// byte for each 8 columns, the largest of their finite values scaled to
 // [2^14, 2^15).  2^-11 relative where bf16 rows, of the same size, are 2^-8
 // off: the sum over a token's slots then adds no error that shows next to the
 // rounding of y to bf16 (with bf16 rows it was as large again).  Infinities and

@@ -204,7 +204,7 @@ struct Fp8Args {
     const Tile *tiles;       // row tiles from the permutation, or null: from the offsets
     const int32_t *ntiles;
     void *y;                 // plain: [rows, N], row stride ldy elements
-    uint8_t *exps;           // staging rows (y of half values): an exponent per 16 columns, or null
+    uint8_t *exps;           // staging rows (y of half values): an exponent per 8 columns, or null
     uint8_t *hq;             // SwiGLU: codes of h [rows, N] and their scales [rows, N / 128]
     float *hs;
     int64_t lda, ldb, ldy, bstride, sstride;

@@ -458,31 +458,35 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
             }
         }
     } else if constexpr (EPI == EPI_STAGE) {
-        static_assert(NBW == 4, "a lane holds the 16 columns under one exponent");
+        static_assert(NBW == 4, "a lane holds the columns under two exponents");
         const int n = n0 + wn * 64 + eg * 16;
         const auto rsrc = tile_rsrc((uint16_t *)p.y + (int64_t)row0 * p.N);
-        const auto rexp = tile_rsrc(p.exps + (int64_t)row0 * (p.N / 16));
+        const auto rexp = tile_rsrc(p.exps + (int64_t)row0 * (p.N / 8));
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int rr = (m * WM + wm) * 16 + e16;
-            uint32_t ex = STAGE_MIN_EXP;
+            uint32_t ex[2], v[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int h = 0; h < 2; ++h) {
+                ex[h] = STAGE_MIN_EXP;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ex = max(ex, stage_exponent(acc[c][m][i]));
-            const float f = stage_pack(ex);
-            uint32_t v[8];
+                for (int c = 2 * h; c < 2 * h + 2; ++c)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                v[2 * c] = cvt_half2(acc[c][m][0] * f, acc[c][m][1] * f);
-                v[2 * c + 1] = cvt_half2(acc[c][m][2] * f, acc[c][m][3] * f);
+                    for (int i = 0; i < 4; ++i)
+                        ex[h] = max(ex[h], stage_exponent(acc[c][m][i]));
+                const float f = stage_pack(ex[h]);
+#pragma unroll
+                for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                    v[2 * c] = cvt_half2(acc[c][m][0] * f, acc[c][m][1] * f);
+                    v[2 * c + 1] = cvt_half2(acc[c][m][2] * f, acc[c][m][3] * f);
+                }
             }
             const bool in = rr < nrows && n < p.N;
             const int at = in ? (rr * p.N + n) * 2 : DROP;
             __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, rsrc, at, 0, 0);
             __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[4], v[5], v[6], v[7]}, rsrc, at, 16, 0);
-            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)ex, rexp, in ? (rr * p.N + n) / 16 : DROP, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(ex[0] | ex[1] << 8), rexp,
+                                                  in ? (rr * p.N + n) / 8 : DROP, 0, 0);
         }
     } else {
         // h = silu(gate) * up, its block maximum over the tile's 128 columns

@@ -9,7 +9,7 @@
 //                   (token, slot) pair and 16 columns of h, no permutation;
 //                   the pair's x is quantised on the way.
 //  fp8_token_down   their down projections and the combine: one workgroup per
-//                   token and 16 columns of y, h quantised on the way.
+//                   token and 8 columns of y, h quantised on the way.
 //
 // The decode kernels pass the sums of single blocks of K through LDS and join
 // them in K order with the same FMAs as the tile kernel, and round each
@@ -159,7 +159,8 @@ __device__ __forceinline__ Fp8Raw one_row_frag(float x0, float x1, uint8_t *buf,
     return f;
 }
 
-// One output from the sums of its KB blocks (16 apart) and their scales, in K order.
+// One output from the sums of its KB blocks (N apart) and their scales, in K order.
+template <int N>
 __device__ __forceinline__ float chain(const float *t, const float *f, int KB)
 {
     float acc = 0.0f;
@@ -168,7 +169,7 @@ __device__ __forceinline__ float chain(const float *t, const float *f, int KB)
         float tv[8], fv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // the reads in flight together
-            tv[i] = t[(kb + i) * 16];
+            tv[i] = t[(kb + i) * N];
             fv[i] = f[kb + i];
         }
 #pragma unroll
@@ -176,7 +177,7 @@ __device__ __forceinline__ float chain(const float *t, const float *f, int KB)
             acc = fmaf(tv[i], fv[i], acc);
     }
     for (; kb < KB; ++kb)
-        acc = fmaf(t[kb * 16], f[kb], acc);
+        acc = fmaf(t[kb * N], f[kb], acc);
     return acc;
 }
 
@@ -187,46 +188,53 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
     extern __shared__ float s_t[];  // [2][KB][16] sums of blocks, then [2][KB] their scales
     __shared__ __attribute__((aligned(16))) uint8_t s_code[GW][FP8_BLOCK];
     const int pair = blockIdx.x / (p.I / 16), n0 = (blockIdx.x - pair * (p.I / 16)) * 16;
-    const int e = p.idx[pair];
-    if ((unsigned)e >= (unsigned)p.E)  // uniform: an empty slot
-        return;
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KB = p.H / FP8_BLOCK;
+    const uint16_t *x = p.x + (int64_t)(pair / p.k) * p.H;
+    constexpr int U = 2;  // blocks of K in flight
+    uint32_t xv[U];       // under way with the expert's number
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        xv[u] = *(const uint32_t *)(x + min(w + u * GW, KB - 1) * FP8_BLOCK + lane * 2);
+    const int e = p.idx[pair];
+    if ((unsigned)e >= (unsigned)p.E)  // uniform: an empty slot
+        return;
     float *s_f = s_t + 2 * KB * 16;
     const int64_t sc = ((int64_t)e * (p.I >> 7) + (n0 >> 7)) * KB;
     const int64_t mat = (int64_t)e * p.I * p.H + (int64_t)(n0 + l16) * p.H;
-    const uint16_t *x = p.x + (int64_t)(pair / p.k) * p.H;
-    constexpr int U = 2;  // blocks of K in flight
     for (int k0 = w; k0 < KB; k0 += GW * U) {
         Fp8Raw G[U], V[U];
-        uint32_t xv[U];
         float fg[U], fv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = min(k0 + u * GW, KB - 1);
-            xv[u] = *(const uint32_t *)(x + kb * FP8_BLOCK + lane * 2);
             G[u] = frag_at(p.w_gate + mat, kb, lg);
             V[u] = frag_at(p.w_up + mat, kb, lg);
             fg[u] = p.s_gate[sc + kb];
             fv[u] = p.s_up[sc + kb];
         }
+        // x into codes while the weights are on their way
+        Fp8Raw B[U];
+        float sx[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            B[u] = one_row_frag(__uint_as_float(xv[u] << 16), __uint_as_float(xv[u] & 0xFFFF0000u),
+                                s_code[w], lane, sx[u]);
+            xv[u] = *(const uint32_t *)(x + min(k0 + (U + u) * GW, KB - 1) * FP8_BLOCK + lane * 2);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = k0 + u * GW;
-            if (kb >= KB)  // uniform
-                break;
-            float sx;
-            const Fp8Frag<false> B(one_row_frag(__uint_as_float(xv[u] << 16),
-                                                __uint_as_float(xv[u] & 0xFFFF0000u), s_code[w], lane, sx));
-            const floatx4 g = mfma_fp8(Fp8Frag<false>(G[u]), B), v = mfma_fp8(Fp8Frag<false>(V[u]), B);
-            if (l16 == 0) {
+            const floatx4 g = mfma_fp8(Fp8Frag<false>(G[u]), Fp8Frag<false>(B[u]));
+            const floatx4 v = mfma_fp8(Fp8Frag<false>(V[u]), Fp8Frag<false>(B[u]));
+            if (kb < KB && l16 == 0) {
                 *(floatx4 *)(s_t + kb * 16 + lg * 4) = g;
                 *(floatx4 *)(s_t + (KB + kb) * 16 + lg * 4) = v;
-            }
-            if (lane == 0) {
-                s_f[kb] = sx * fg[u];
-                s_f[KB + kb] = sx * fv[u];
+                if (lane == 0) {
+                    s_f[kb] = sx[u] * fg[u];
+                    s_f[KB + kb] = sx[u] * fv[u];
+                }
             }
         }
     }
@@ -235,70 +243,73 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
         return;
     // lanes 0..15: gate, 16..31: up
     const int m = (lane >> 4) & 1;
-    const float acc = chain(s_t + m * KB * 16 + l16, s_f + m * KB, KB);
+    const float acc = chain<16>(s_t + m * KB * 16 + l16, s_f + m * KB, KB);
     const float up = __shfl(acc, l16 + 16);
     if (lane < 16)
         p.h[(int64_t)pair * p.I + n0 + lane] = silu(acc) * up;
 }
 
 constexpr int DW = 16;  // waves of fp8_token_down, and most slots of a token
+constexpr int DN = 8;   // its columns of y: an MFMA's rows 8..15 repeat 0..7
 
 __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
 {
-    extern __shared__ float s_t[];  // [k][KB][16] sums of blocks, then [k][KB] their scales
+    extern __shared__ float s_t[];  // [k][KB][DN] sums of blocks, then [k][KB] their scales
     __shared__ __attribute__((aligned(16))) uint8_t s_code[DW][FP8_BLOCK];
-    __shared__ float s_o[DW][16], s_w[DW];
+    __shared__ float s_o[DW][DN], s_w[DW];
     __shared__ int s_live[DW];
-    const int t = blockIdx.x / (p.H / 16), n0 = (blockIdx.x - t * (p.H / 16)) * 16;
+    const int t = blockIdx.x / (p.H / DN), n0 = (blockIdx.x - t * (p.H / DN)) * DN;
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KB = p.I / FP8_BLOCK, units = p.k * KB;
-    float *s_f = s_t + units * 16;
+    float *s_f = s_t + units * DN;
     // this wave's slot of the combine, loaded early
     const int my_e = w < p.k ? p.idx[t * p.k + w] : -1;
     const float my_w = w < p.k ? p.topk_w[t * p.k + w] : 0.0f;
+    const float *h = p.h + (int64_t)t * p.k * p.I + lane * 2;
     constexpr int U = 4;  // units in flight
     for (int u0 = w; u0 < units; u0 += DW * U) {
         Fp8Raw W[U];
         float2 hv[U];
-        bool live[U];
+        int e[U];
         float fw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int q = min(u0 + u * DW, units - 1), j = q / KB, kb = q - j * KB;
-            const int e = p.idx[t * p.k + j];
-            live[u] = u0 + u * DW < units && (unsigned)e < (unsigned)p.E;
-            if (live[u]) {  // uniform
-                hv[u] = *(const float2 *)(p.h + (int64_t)(t * p.k + j) * p.I + kb * FP8_BLOCK + lane * 2);
-                W[u] = frag_at(p.w_down + ((int64_t)e * p.H + n0 + l16) * p.I, kb, lg);
-                fw[u] = p.s_down[((int64_t)e * (p.H >> 7) + (n0 >> 7)) * KB + kb];
-            }
+            const int q = min(u0 + u * DW, units - 1), j = q / KB;
+            e[u] = p.idx[t * p.k + j];
+            hv[u] = *(const float2 *)(h + (int64_t)j * p.I + (q - j * KB) * FP8_BLOCK);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!live[u])
-                continue;
+            const int q = min(u0 + u * DW, units - 1), kb = q - q / KB * KB;
+            // an empty slot reads expert 0, and nobody its results
+            const int64_t ev = (unsigned)e[u] < (unsigned)p.E ? e[u] : 0;
+            W[u] = frag_at(p.w_down + (ev * p.H + n0 + (l16 & (DN - 1))) * p.I, kb, lg);
+            fw[u] = p.s_down[(ev * (p.H >> 7) + (n0 >> 7)) * KB + kb];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             const int q = u0 + u * DW;
             float sh;
             const Fp8Frag<false> B(one_row_frag(hv[u].x, hv[u].y, s_code[w], lane, sh));
             const floatx4 o = mfma_fp8(Fp8Frag<false>(W[u]), B);
-            if (l16 == 0)
-                *(floatx4 *)(s_t + q * 16 + lg * 4) = o;
-            if (lane == 0)
+            if (q < units && l16 == 0 && lg < DN / 4)
+                *(floatx4 *)(s_t + q * DN + lg * 4) = o;
+            if (q < units && lane == 0)
                 s_f[q] = sh * fw[u];
         }
     }
     __syncthreads();
-    // wave j: slot j's 16 outputs, rounded as a staging row is
+    // wave j: slot j's outputs, rounded as a staging row is
     const bool mine = (unsigned)my_e < (unsigned)p.E;
     if (mine) {
-        const float acc = chain(s_t + w * KB * 16 + l16, s_f + w * KB, KB);
+        const float acc = chain<DN>(s_t + w * KB * DN + (l16 & (DN - 1)), s_f + w * KB, KB);
         uint32_t ex = stage_exponent(acc);
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1)
+        for (int d = 1; d < DN; d <<= 1)
             ex = max(ex, (uint32_t)__shfl_xor((int)ex, d));
         ex = max(ex, STAGE_MIN_EXP);
-        if (lane < 16)
+        if (lane < DN)
             s_o[w][lane] = (float)(_Float16)(acc * stage_pack(ex)) * stage_unpack(ex);
     }
     if (lane == 0) {
@@ -306,7 +317,7 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
         s_w[w] = my_w;
     }
     __syncthreads();
-    if (threadIdx.x < 16) {
+    if (threadIdx.x < DN) {
         float y = 0.0f;
         for (int j = 0; j < p.k; ++j)
             if (s_live[j])
@@ -343,7 +354,7 @@ void launch_fp8_decode(const Fp8Decode &p, hipStream_t st)
 {
     const int kb = p.H / FP8_BLOCK, units = p.k * (p.I / FP8_BLOCK);
     fp8_pair_gate_up<<<(unsigned)(p.T * p.k * (p.I / 16)), 64 * GW, (size_t)kb * 34 * 4, st>>>(p);
-    fp8_token_down<<<(unsigned)(p.T * (p.H / 16)), 64 * DW, (size_t)units * 17 * 4, st>>>(p);
+    fp8_token_down<<<(unsigned)(p.T * (p.H / DN)), 64 * DW, (size_t)units * (DN + 1) * 4, st>>>(p);
 }
 
 }  // namespace moe

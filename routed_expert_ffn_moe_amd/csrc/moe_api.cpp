@@ -245,7 +245,7 @@ Layout layout(const moe_shape_t *s, int Tc)
         L.f8_x = take((size_t)Tc * s->H);
         L.f8_sx = take((size_t)Tc * (s->H / moe::FP8_K) * 4);
         L.f8_sh = take((size_t)rows * (s->I / moe::FP8_K) * 4);
-        L.f8_exp = take((size_t)rows * (s->H / 16));  // exponents of the staging rows
+        L.f8_exp = take((size_t)rows * (s->H / 8));   // exponents of the staging rows
     }
     // decode, verify and other short passes with MXFP4 experts
     const int act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;

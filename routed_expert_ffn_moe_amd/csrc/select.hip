@@ -12,9 +12,11 @@
 // between neighbouring keys that fp32 rounding (6e-8 near 1) closes for about
 // one token in ten thousand, and another expert would run.  So a token is
 // routed in fp32 and the gaps that its selection rests on are checked against
-// the bound of the fp32 keys' errors; the few tokens with a gap too small (1%
-// with a bias, none without one unless the scores saturate) are routed again
-// in 64 bits.
+// the bound of the fp32 keys' errors; where one is too small (1 token in 1000
+// with sigmoid and a bias, 1 in 100 with softmax and a bias, none without a
+// bias unless the scores saturate) the experts in question are ordered in 64
+// bits, or, where those are many or the doubt is between groups, the token is
+// routed again in 64 bits.
 //
 // An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is
 // masked: it ranks behind every other one (among masked ones by index) and
@@ -24,6 +26,8 @@
 //
 // One wave per token.  Bound by its instructions: the k selection rounds are a
 // wave maximum each.  T=8192, E=384, bias: all in 64 bits 25 us.
+#include <algorithm>
+
 #include "common.h"
 #include "kernels.h"
 #include "topk.h"
@@ -193,12 +197,15 @@ __device__ __forceinline__ void select_exact(const SelectArgs &a, int t, double 
 
 // Twice the bound of a fp32 key's error, in units of 2^-24.  Sigmoid: the
 // exponential's argument is off by |l| (s (1 - s) |l| <= 0.23 in the score), the
-// exponential and the reciprocal by 2 each.  Softmax: difference and argument
-// 2 |l - m| (p |l - m| <= 0.37), the exponential 2, the products 2, and the sum
-// over the experts: their own errors weighted by p (2 |l - m| averages to
-// 2 ln 1024 = 14 at most, and 2) and at most 23 additions.  Below 64 together,
-// with the key's own sum.
-__device__ __forceinline__ float key_slack(float k) { return 0x1p-17f * fmaxf(1.0f, fabsf(k)); }
+// exponential by 2 (s (1 - s) <= 0.25), the reciprocal by 2, the key's own sum by
+// 1: below 4.  Softmax: difference and argument 2 |l - m| (p |l - m| <= 0.37),
+// the exponential 2, the products 2, and the sum over the experts: their own
+// errors weighted by p (2 |l - m| averages to 2 ln 1024 = 14 at most, and 2) and
+// at most 23 additions: below 64 with the key's sum.
+__device__ __forceinline__ float key_slack(float k, int softmax)
+{
+    return (softmax ? 0x1p-17f : 0x1p-21f) * fmaxf(1.0f, fabsf(k));
+}
 
 // Whether the keys in 64 bits of two logits l > m (no bias) are sure to differ:
 // their ratio is 1 + (l - m) (1 - s) at least, s = 0 for softmax, against 2^-52
@@ -209,16 +216,48 @@ __device__ __forceinline__ bool logits_apart(float l, float m, float top, bool s
     return softmax ? d > 1e-13f && m - top > -600.0f : d * __expf(-fmaxf(l, 0.0f)) > 1e-13f && m > -600.0f;
 }
 
-// Token t in fp32; false if a gap is too small to be sure of the order.
+// The order of the few experts (c <= 64) that may be among the k best, in 64
+// bits: lane j < c takes one of them (cand[j]) and its rank by counting.
+template <int PER, bool BF16>
+__device__ __forceinline__ void select_refine(const SelectArgs &a, int t, const float (&l)[PER], float top,
+                                              int *cand, int c, int &my_e)
+{
+    const int lane = threadIdx.x & 63;
+    double z = 1.0;
+    if (a.softmax) {
+        z = 0.0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            z += l[i] > -INFINITY ? exp((double)l[i] - (double)top) : 0.0;
+        z = wave_sum_f64(z);
+    }
+    const int e = cand[min(lane, c - 1)];
+    const double v = (double)fminf(logit_at<BF16>(a.logits, (int64_t)t * a.ld + e), LARGEST);
+    double key = a.softmax ? exp(v - (double)top) / z : 1.0 / (1.0 + exp(-v));
+    if (a.bias)
+        key += (double)fminf(a.bias[e], LARGEST);
+    int rank = 0;
+    for (int j = 0; j < c; ++j) {
+        const double o = __shfl(key, j);
+        const int oe = __shfl(e, j);
+        rank += o > key || (o == key && oe < e) ? 1 : 0;
+    }
+    wave_lds_sync();
+    if (lane < c && rank < a.k)
+        cand[rank] = e;
+    wave_lds_sync();
+    my_e = cand[min(lane, a.k - 1)];
+}
+
+// Token t in fp32, and where a gap is too small to be sure of the order, in 64
+// bits among the experts in question; false if they are too many, or if the
+// doubt is between groups.
 template <int PER, bool BF16>
 __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *row, int &my_e, float &my_w)
 {
     const int lane = threadIdx.x & 63;
     const bool bias = a.bias != nullptr;
     const bool grouped = a.n_group > 1;
-    // scores of all experts: for keys with a bias, sums of two keys, and the
-    // softmax's own weights
-    const bool all_scores = bias || (grouped && a.group_top2);
     float l[PER], key[PER];
     float top = -INFINITY;
 #pragma unroll
@@ -229,18 +268,21 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
         top = fmaxf(top, l[i]);
     }
     float inv_z = 0.0f;
+    auto sum_scores = [&]() {
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            z += l[i] > -INFINITY ? __expf(l[i] - top) : 0.0f;
+#pragma unroll
+        for (int d = 32; d; d >>= 1)
+            z += __shfl_xor(z, d);
+        inv_z = z > 0.0f ? 1.0f / z : 0.0f;
+    };
     if (a.softmax) {
         top = key_value(wave_max_u32(order_key(top)));
-        if (all_scores || !a.renorm) {
-            float z = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                z += l[i] > -INFINITY ? __expf(l[i] - top) : 0.0f;
-#pragma unroll
-            for (int d = 32; d; d >>= 1)
-                z += __shfl_xor(z, d);
-            inv_z = z > 0.0f ? 1.0f / z : 0.0f;
-        }
+        // not needed for an order of logits with renormalised weights
+        if (bias || !a.renorm || (grouped && a.group_top2))
+            sum_scores();
     }
     auto score = [&](float v) {
         return a.softmax ? __expf(v - top) * inv_z : __builtin_amdgcn_rcpf(1.0f + __expf(-v));
@@ -302,16 +344,15 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
         const float lo = -key_value(wave_max_u32(order_key(in ? -mine : -INFINITY)));
         const float hi = key_value(wave_max_u32(order_key(lane < a.n_group && !in ? mine : -INFINITY)));
         if (hi > -INFINITY)  // (groups of masked experts only are in order)
-            sure = a.group_top2 ? lo - hi > 2.0f * key_slack(fmaxf(fabsf(lo), fabsf(hi)))
-                   : bias       ? lo - hi > key_slack(fmaxf(fabsf(lo), fabsf(hi)))
+            sure = a.group_top2 ? lo - hi > 2.0f * key_slack(fmaxf(fabsf(lo), fabsf(hi)), a.softmax)
+                   : bias       ? lo - hi > key_slack(fmaxf(fabsf(lo), fabsf(hi)), a.softmax)
                                 : logits_apart(lo, hi, top, a.softmax);
     }
+    auto may = [&](int e) { return e < a.E && (!grouped || (open >> (e / gs & 63)) & 1); };
     uint32_t ok[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        ok[i] = e < a.E && (!grouped || (open >> (e / gs & 63)) & 1) ? order_key(key[i]) : 0u;
-    }
+    for (int i = 0; i < PER; ++i)
+        ok[i] = may(lane + 64 * i) ? order_key(key[i]) : 0u;
     // one more than k: the gap behind the last one
     uint32_t my_k;
     wave_topk_keys<PER>(ok, min(a.k + 1, a.E), my_e, my_k);
@@ -327,10 +368,39 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
     bool fine = true;
     if (lane < a.k && nk > -INFINITY)
         fine = (lv == nl && bv == nb) ||
-               (bias ? kv - nk > key_slack(kv) : logits_apart(kv, nk, top, a.softmax));
-    sure &= __all(fine);
+               (bias ? kv - nk > key_slack(kv, a.softmax) : logits_apart(kv, nk, top, a.softmax));
+    if (!sure)
+        return false;
+    if (!__all(fine)) {
+        // every expert whose key is not surely below the k-th one's; where no
+        // bias was added the keys are the scores now, not the logits
+        if (a.softmax && inv_z == 0.0f)
+            sum_scores();
+        const float last = __shfl(bias ? kv : score(kv), a.k - 1);
+        if (!(last > -INFINITY))
+            return false;
+        const float least = last - key_slack(last, a.softmax);
+        int *cand = (int *)row;
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool in = may(lane + 64 * i) && key[i] > -INFINITY &&
+                            (bias ? key[i] : score(key[i])) >= least;
+            const uint64_t m = __ballot(in);
+            if (in && c + __popcll(m & ((1ull << lane) - 1)) < 64)
+                cand[c + __popcll(m & ((1ull << lane) - 1))] = lane + 64 * i;
+            c += __popcll(m);
+        }
+        if (c > 64 || c < a.k)
+            return false;
+        wave_lds_sync();
+        select_refine<PER, BF16>(a, t, l, top, cand, c, my_e);
+        lv = -INFINITY;
+        if (lane < a.k)
+            lv = fminf(logit_at<BF16>(a.logits, (int64_t)t * a.ld + my_e), LARGEST);
+    }
     // weights; a masked expert (key -inf) has none
-    const bool live = lane < a.k && kv > -INFINITY;
+    const bool live = lane < a.k && lv > -INFINITY && kv > -INFINITY;
     float s;
     if (a.softmax) {
         const float base = a.renorm ? key_value(wave_max_u32(order_key(live ? lv : -INFINITY))) : top;
@@ -352,12 +422,12 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
 template <int PER, bool BF16>
 __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
 {
-    extern __shared__ double s_key[];  // [waves][E], grouped selection only
+    extern __shared__ double s_key[];  // [waves][max(E, 32)]
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int t = blockIdx.x * SEL_WAVES + wv;
     if (t >= a.T)  // uniform in the wave; no workgroup barrier below
         return;
-    double *row = s_key + (int64_t)wv * a.E;
+    double *row = s_key + wv * max(a.E, 32);
     int my_e;
     float my_w;
     if (!select_fast<PER, BF16>(a, t, (float *)row, my_e, my_w))  // uniform
@@ -373,7 +443,7 @@ template <int PER>
 void launch_per(const SelectArgs &a, hipStream_t st)
 {
     const unsigned nb = (unsigned)((a.T + SEL_WAVES - 1) / SEL_WAVES);
-    const size_t lds = a.n_group > 1 ? (size_t)SEL_WAVES * a.E * sizeof(double) : 0;
+    const size_t lds = (size_t)SEL_WAVES * std::max(a.E, 32) * sizeof(double);
     if (a.bf16)
         select_kernel<PER, true><<<nb, 64 * SEL_WAVES, lds, st>>>(a);
     else
