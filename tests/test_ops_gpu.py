@@ -124,6 +124,18 @@ def test_select_orders_keys_that_fp32_cannot_tell_apart(ng):
     check_select(l, bias[perm], 8, score="softmax", n_group=ng, topk_group=3 if ng > 1 else 1)
 
 
+@pytest.mark.parametrize("ng", [1, 8])
+def test_select_orders_softmax_keys_that_fp32_cannot_tell_apart(ng):
+    """As above with softmax scores: bias = 0.05 - p of the row without its noise."""
+    g = gen(6)
+    T, E = 24, 128
+    base = torch.linspace(-1, 1, E).float()[torch.randperm(E, generator=g)]
+    p = torch.softmax(base.double(), 0)
+    l = base.repeat(T, 1) + torch.randint(-2, 3, (T, E), generator=g) * 2.0 ** -24
+    check_select(l, (0.05 - p).float(), 8, score="softmax", n_group=ng, topk_group=3 if ng > 1 else 1,
+                 group_score="top2")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("ng", [1, 4])
 def test_select_masked_experts(score, ng):
@@ -357,6 +369,27 @@ def test_matmul_many_groups(M, G):
     check_matmul(M, 128, 128, "bf16", off=[0] + cuts + [M], G=G)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1000, 4200, 260), (2000, 4200, 1100), (4000, 4100, 130), (4000, 4100, 900)])
+def test_matmul_more_tiles_than_workgroups(M, N, K, out):
+    """One matrix of 272 tiles of 64, 128 and 256 rows: a workgroup takes several,
+    the copies of the next begin while the last steps of one still run (or, in
+    few steps of K, after them)."""
+    check_matmul(M, N, K, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [100, 384, 640, 1152])
+@pytest.mark.parametrize("per", [10, 20, 45, 70, 100, 150, 220])
+def test_matmul_groups_of_every_tile_height(per, K, out):
+    """Uneven groups of `per` rows on average, over 300 tiles in all: tiles of
+    16, 32, 64, 96, 144, 128 and 256 rows, one to nine steps of K."""
+    G, N = 9, 8008
+    g = gen(per + K)
+    cuts = (torch.arange(1, G) * per + torch.randint(-(per // 2), per // 2, (G - 1,), generator=g)).tolist()
+    check_matmul(G * per, N, K, out, off=[0] + cuts + [G * per], G=G, what="%d rows a group" % per)
+
+
 @pytest.mark.parametrize("M", [4, 40, 200])
 def test_matmul_nan_stays_in_its_row_and_column(M):
     g = gen(1)
@@ -428,6 +461,19 @@ def test_experts(T, E, k, H, I):
     want, tol = L.ref(x, idx, w)
     within(y, want, tol + 1e-30, "experts T%d E%d k%d" % (T, E, k))
     say("bound over y: %.3g" % float(tol.norm() / want.norm()))
+
+
+@pytest.mark.parametrize("per", [10, 20, 45, 70, 100, 150, 220])
+def test_experts_of_every_tile_height(per):
+    """Every tile height, in more tiles than there are CUs."""
+    E, H, I = 20, 768, 2048
+    g = gen(per)
+    L = Experts(E, H, I, per)
+    x = randn(g, E * per, H, dtype=torch.bfloat16)
+    idx, w = routing(g, E * per, E, 1, 0.2)
+    y = L.run(x.cuda(), idx.cuda(), w.cuda())
+    want, tol = L.ref(x, idx, w)
+    within(y, want, tol + 1e-30, "%d rows an expert" % per)
 
 
 @pytest.mark.parametrize("T", [1, 5, 40, 300])
