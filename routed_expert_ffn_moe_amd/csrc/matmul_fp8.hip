@@ -116,18 +116,28 @@ struct Cfg {
     static constexpr int OCC = 163840 / LDS;                      // workgroups of a CU
     // Stores of a wave and tile (EPI_PLAIN: bf16 in whole words; more otherwise)
     static constexpr int NS = EPI == EPI_SWIGLU ? 2 * MB : EPI == EPI_STAGE ? 3 * MB : MB * (NBW / 2);
+    // Stages the copies are ahead of the one that is multiplied.  A copy that the
+    // memory system is not ready for holds up the wave's MFMAs behind it, so with
+    // three stages a stage's copies are spread over the row blocks of a step
+    // (into the buffer that the step before has left); with two that would leave
+    // them too little time, and with four the tiles are small and wait for memory
+    // anyway: there all copies of a stage are made when its buffer falls free.
+    // (T=8192 over 384 experts: gate+up 1550 us spread, 1620 at once, down 825 and
+    // 860.)
+    static constexpr bool SPREAD = ST == 3 && NW == 8;
+    static constexpr int LEAD = SPREAD ? ST - 1 : ST;
     // Depth from which a tile's last stages are multiplied while the next
     // tile's first ones are copied (its rows are known by then).
-    static constexpr int DEEP = 2 * ST - 1;
+    static constexpr int DEEP = ST + LEAD - 1;
     static_assert(BR / 8 % NW == 0, "weight copies divide among the waves");
     static_assert(EPI != EPI_SWIGLU || (COLS == 128 && NBW % 2 == 0), "a tile of h is one scale block wide");
     static_assert(LDS <= 163840, "LDS of one workgroup");
     static_assert(ST >= 2 && ST <= 4, "chunks of scales in use or under way: three");
-    static_assert((ST - 1) * L + NS < 64 && NBW % 2 == 0, "the counter of outstanding operations holds 63");
+    static_assert((LEAD - 1) * L + NS < 64 && NBW % 2 == 0, "the counter of outstanding operations holds 63");
 };
 
 // Persistent workgroups.  The consumer multiplies stage after stage of its
-// tile; the producer (the same waves) is ST stages ahead and goes on to the
+// tile; the producer (the same waves) is LEAD stages ahead and goes on to the
 // next tile, so that a tile's epilogue and its first latency overlap with
 // copies.
 template <int NBW, int BM, int WN, int WM, int ST, int EPI, bool EXACT>
@@ -219,10 +229,12 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         ++pt;
         pk = 0;
     };
-    auto issue = [&]() {
+    // part J of N of the next stage's copies
+    auto issue = [&](auto part, auto parts) {
+        constexpr int J = decltype(part)::value, N = decltype(parts)::value;
         const uint32_t st = lds + (uint32_t)(pq % ST) * C::STAGE;
         const int64_t k = (int64_t)pk * FP8_BLOCK;
-        if (pk % C::CH == 0) {  // the scales of this stage and the CH - 1 behind it
+        if (J == 0 && pk % C::CH == 0) {  // the scales of this stage and the CH - 1 behind it
             const int kb = min(pk + lane % C::CH, KB - 1);
 #pragma unroll
             for (int i = 0; i < C::CI; ++i)
@@ -232,19 +244,26 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
             ++pc;
         }
 #pragma unroll
-        for (int i = 0; i < C::WI; ++i) {
-            const uint8_t *base = gw0;
-            if (EPI == EPI_SWIGLU && ((((w * C::WI + i) * 8) >> 4) % NBW) >= NBW / 2)
-                base = gw1;
-            dma16(base + k, woff[i], st + (uint32_t)(w * C::WI + i) * 1024u);
+        for (int i = 0; i < C::L; ++i) {
+            if (i * N / C::L != J)
+                continue;
+            if (i < C::WI) {
+                const uint8_t *base = gw0;
+                if (EPI == EPI_SWIGLU && ((((w * C::WI + i) * 8) >> 4) % NBW) >= NBW / 2)
+                    base = gw1;
+                dma16(base + k, woff[i], st + (uint32_t)(w * C::WI + i) * 1024u);
+            } else {
+                dma16(ga + k, toff[i - C::WI],
+                      st + C::BR * 128u + (uint32_t)((w * C::TI + i - C::WI) % (C::BM / 8)) * 1024u);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < C::TI; ++i)
-            dma16(ga + k, toff[i],
-                  st + C::BR * 128u + (uint32_t)((w * C::TI + i) % (C::BM / 8)) * 1024u);
-        ++pk;
-        ++pq;
+        if (J == N - 1) {
+            ++pk;
+            ++pq;
+        }
     };
+    constexpr std::integral_constant<int, 0> all{};
+    constexpr std::integral_constant<int, 1> once{};
 
     Where cur = find((int)blockIdx.x >> 3);
     if (cur.g < 0)
@@ -253,11 +272,11 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
     const int o0 = l16 * 128 + ((lg ^ (l16 >> 1)) << 4), o1 = o0 ^ 64;
     const int nsb = EPI == EPI_SWIGLU ? 0 : (wn * NBW * 16) >> 7;
     aim(cur, false);
-    for (int s = 0; s < ST && s < KB; ++s)
-        issue();
+    for (int s = 0; s < C::LEAD && s < KB; ++s)
+        issue(all, once);
 
     int cq = 0, cc = 0, ct = 0;  // consumer: stages, chunks and tiles done
-    bool stored = false;  // NS stores (at least) were issued behind this tile's first ST stages
+    bool stored = false;  // NS stores (at least) were issued behind this tile's first LEAD stages
     for (;;) {
     const Where next = find(cur.q + step_q);
     const bool go_on = next.g >= 0, ahead = go_on && deep;
@@ -309,10 +328,13 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
     // no rows of this tile).  A block's fragment is read while the one before
     // it is multiplied.  Behind the MFMAs of a stage's last block, while they
     // run, the workgroup turns to the next stage: everything of it has arrived
-    // for every wave, every wave is done reading this one (whose buffer takes
-    // the stage that is ST further), and the next weights and first block are
-    // read.  The sums of a block are scaled and added while the next block's
-    // MFMAs run (LAG), where there are registers for it.
+    // for every wave, every wave is done reading this one (whose buffer is free
+    // for the stage that is ST further), and the next weights and first block
+    // are read.  The sums of a block are scaled and added while the next block's
+    // MFMAs run (LAG), where there are registers for it.  The copies stand before
+    // a block's MFMAs: behind them, their branch stood between the MFMAs and the
+    // first use of the sums, and the wait states before that were missing on one
+    // of its paths (a wrong last sum).
     constexpr bool LAG = MB < 8;
     auto kloop = [&](auto nm) {
         constexpr int NM = decltype(nm)::value;
@@ -335,14 +357,27 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
                 asm volatile("" : "+v"(acc[c][m]));
             }
         };
-        // MORE: 2 = the tile's stage s + ST is copied, 1 = the next tile's
-        // stages are (if `ahead`), 0 = the tile's last stage
+        // MORE: 2 = the copies made in stage s are the tile's own, 1 = the next
+        // tile's (if `ahead`), 0 = as 1, in the tile's last stage
+        auto part = [&](int m) {  // (m is a constant in every call)
+            constexpr std::integral_constant<int, NM> n{};
+            if (m == 0) issue(std::integral_constant<int, 0>{}, n);
+            if (m == 1) issue(std::integral_constant<int, 1>{}, n);
+            if (m == 2) issue(std::integral_constant<int, 2>{}, n);
+            if (m == 3) issue(std::integral_constant<int, 3>{}, n);
+            if (m == 4) issue(std::integral_constant<int, 4>{}, n);
+            if (m == 5) issue(std::integral_constant<int, 5>{}, n);
+            if (m == 6) issue(std::integral_constant<int, 6>{}, n);
+            if (m == 7) issue(std::integral_constant<int, 7>{}, n);
+        };
         auto step = [&](int s, auto more) {
             constexpr int MORE = decltype(more)::value;
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
                 if (m + 1 < NM)
                     load_block(bf[(m + 1) & 1], s, m + 1);
+                if (C::SPREAD && (MORE == 2 || ahead))
+                    part(m);
                 const Fp8Frag<EXACT> B(bf[m & 1].v);
                 floatx4 n[NBW];
 #pragma unroll
@@ -353,7 +388,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
                     __builtin_amdgcn_sched_barrier(0);
                     if (MORE != 2 && !ahead)
                         dma_wait_barrier<0>();
-                    else if (s < ST - 1 && stored)  // the stores of the tile before are newer
+                    else if (s < C::LEAD - 1 && stored)  // the stores of the tile before are newer
                         dma_wait_barrier<(ST - 2) * C::L + C::NS>();
                     else if (ST == 3 && (s + 2 < KB ? s + 2 : s + 2 - KB) % C::CH == 0)
                         dma_wait_barrier<(ST - 2) * C::L + C::CI>();  // stage s + 2 holds scales
@@ -361,8 +396,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
                         dma_wait_barrier<(ST - 2) * C::L>();
                     load_weights(wf, s + 1);
                     load_block(bf[0], s + 1, 0);
-                    if (MORE == 2 || ahead)
-                        issue();
+                    if (!C::SPREAD && (MORE == 2 || ahead))
+                        issue(all, once);
                 }
                 if (LAG)
                     join(m ? m - 1 : NM - 1);
@@ -377,15 +412,15 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
             }
         };
         if (stored)
-            dma_wait_barrier<(ST - 1) * C::L + C::NS>();
-        else if (KB >= ST)
-            dma_wait_barrier<(ST - 1) * C::L>();
+            dma_wait_barrier<(C::LEAD - 1) * C::L + C::NS>();
+        else if (KB >= C::LEAD)
+            dma_wait_barrier<(C::LEAD - 1) * C::L>();
         else
             dma_wait_barrier<0>();
         load_weights(wf, 0);
         load_block(bf[0], 0, 0);
         int s = 0;
-        for (; s + ST < KB; ++s)
+        for (; s + C::LEAD < KB; ++s)
             step(s, std::integral_constant<int, 2>{});
         if (ahead)
             aim(next, true);
@@ -406,8 +441,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         kloop(std::integral_constant<int, HALF>{});
     }
     lds_barrier();  // every wave is done with this tile's last stage
-    if (ahead)
-        issue();
+    if (!C::SPREAD && ahead)
+        issue(all, once);
 
     __builtin_amdgcn_sched_barrier(0);
     int e16 = l16, eg = lg;  // hidden as in aim()
@@ -545,8 +580,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
     stored = deep && (EPI != EPI_PLAIN || p.vec);
     if (!deep) {  // few stages: no copies under way between tiles
         aim(cur, false);
-        for (int s = 0; s < ST && s < KB; ++s)
-            issue();
+        for (int s = 0; s < C::LEAD && s < KB; ++s)
+            issue(all, once);
     }
     }
 }
@@ -569,7 +604,7 @@ void launch_cfg(const Fp8Args &p, hipStream_t st)
 // stream from memory once per row tile, so one tile should take all of a
 // group's rows, 1.4 standard deviations of a balanced routing above the mean,
 // up to the 144 rows whose three stages fill LDS (T=8192 over 384 experts, 128
-// rows each: gate+up 1650 us with tiles of 144 rows, 1860 with 128, which a
+// rows each: gate+up 1550 us with tiles of 144 rows, 1860 with 128, which a
 // second tile follows for half of the experts).  Groups of more rows are bound
 // by the matrix cores and take the largest tiles.  One matrix: the largest
 // tiles that still give every CU one (8192 x 4096 x 4096: 144 us with 256 rows,
