@@ -210,9 +210,13 @@ struct Fp8Args {
     int64_t lda, ldb, ldy, bstride, sstride;
     int M, N, KB, G, mtiles, out_f32, vec;  // vec: rows of y allow 16-byte stores
 };
-int fp8_bm(int64_t rows, int groups, int64_t cols);              // rows of a tile
+struct Fp8Tile {
+    int rows, cols;
+};
+// narrow: tiles of 64 columns are allowed
+Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool f32, bool narrow);
 int64_t fp8_row_tiles(int64_t rows, int groups, int bm);         // upper bound of the row tiles
-void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st);
+void launch_fp8_matmul(const Fp8Args &p, Fp8Tile t, hipStream_t st);
 void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st);
 // Few rows (matmul_fp8_small.hip): one matrix of few tiles, and the whole of
 // the FP8 experts for decode rows with given routing.

@@ -54,6 +54,7 @@ __device__ __forceinline__ T uniform_load(const T *p)
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // Buffer of the bytes from p on; an offset of DROP is out of its range, where
 // stores do nothing.
@@ -477,6 +478,22 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
                         __builtin_amdgcn_raw_buffer_store_b128(
                             u32x4{v[2 * c], v[2 * c + 1], v[2 * c + 2], v[2 * c + 3]}, rsrc, at, 8 * c, 0);
                 }
+            } else if (rr < nrows && n + 4 * NBW <= p.N) {
+                // 16-byte stores at any element's address: the hardware takes
+                // them, if not at full speed
+                char *at = (char *)p.y + ((int64_t)(row0 + rr) * p.ldy + n) * esz;
+                if (p.out_f32) {
+#pragma unroll
+                    for (int c = 0; c < NBW; ++c)
+                        *(u32x4_any *)(at + 16 * c) = __builtin_bit_cast(u32x4, acc[c][m]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NBW; c += 2)
+                        *(u32x4_any *)(at + 8 * c) =
+                            u32x4{cvt_bf2(acc[c][m][0], acc[c][m][1]), cvt_bf2(acc[c][m][2], acc[c][m][3]),
+                                  cvt_bf2(acc[c + 1][m][0], acc[c + 1][m][1]),
+                                  cvt_bf2(acc[c + 1][m][2], acc[c + 1][m][3])};
+                }
             } else if (rr < nrows) {
                 const int64_t at = (int64_t)(row0 + rr) * p.ldy + n;
 #pragma unroll
@@ -592,36 +609,55 @@ void launch_cfg(const Fp8Args &p, hipStream_t st)
     using C = Cfg<NBW, BM, WN, WM, ST, EPI>;
     const int64_t tiles = (int64_t)p.mtiles * ((p.N + C::COLS - 1) / C::COLS);
     const unsigned grid = (unsigned)(std::min<int64_t>(tiles, 256 * C::OCC) + 7) / 8 * 8;
-    if (EPI == EPI_PLAIN && p.out_f32)
-        fp8_tile<NBW, BM, WN, WM, ST, EPI, EPI == EPI_PLAIN><<<grid, 64 * C::NW, 0, st>>>(p);
-    else
-        fp8_tile<NBW, BM, WN, WM, ST, EPI, false><<<grid, 64 * C::NW, 0, st>>>(p);
+    if constexpr (EPI == EPI_PLAIN && BM < 256) {  // fp8_size
+        if (p.out_f32)
+            return fp8_tile<NBW, BM, WN, WM, ST, EPI, true><<<grid, 64 * C::NW, 0, st>>>(p);
+    }
+    fp8_tile<NBW, BM, WN, WM, ST, EPI, false><<<grid, 64 * C::NW, 0, st>>>(p);
 }
 
 }  // namespace
 
-// Rows of a tile.  Grouped rows (the rows of an expert): the weights of a group
-// stream from memory once per row tile, so one tile should take all of a
-// group's rows, 1.4 standard deviations of a balanced routing above the mean,
-// up to the 144 rows whose three stages fill LDS (T=8192 over 384 experts, 128
-// rows each: gate+up 1550 us with tiles of 144 rows, 1860 with 128, which a
-// second tile follows for half of the experts).  Groups of more rows are bound
-// by the matrix cores and take the largest tiles.  One matrix: the largest
-// tiles that still give every CU one (8192 x 4096 x 4096: 144 us with 256 rows,
-// 163 with 128).
-int fp8_bm(int64_t rows, int groups, int64_t cols)
+// Size of a tile.  The time is that of the rounds in which the CUs take their
+// tiles, times a round's.  A step of 128 of K costs a CU about 0.33 us plus 6 ns
+// for each row of the tile (measured with one tile a CU and K = 2048, in units of
+// 5.5 ns: 32 rows 95, 64 rows 130, 96 rows 160, 128 rows 195, 144 rows 210, 256
+// rows 345), 64 x 64 tiles 90 up to two of them a CU, then 72 for each 256.
+// Groups whose balanced rows (1.4 standard deviations above the mean) fit into a
+// tile have one; larger ones leave half a tile empty.  So groups are covered by
+// one tile where that is possible, which then streams their weights once (T=8192
+// over 384 experts, 128 rows each: gate+up 1550 us with tiles of 144 rows, 1860
+// with 128), long matrices take the largest tiles (8192 x 4096 x 4096: 144 us with
+// 256 rows, 163 with 128) and short ones tiles that give every CU one (8 groups of
+// 347 rows, N=1664, K=2048: 18 us with 96 rows, 33 with 256; 4 groups of 217 rows,
+// N=1024, K=640: 7.3 us with 64 x 64, 14.7 with 256 rows).  The largest tiles' fp32
+// output would need more registers than there are (71 us against 33 in the first
+// of these), so it goes without them.
+Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool f32, bool narrow)
 {
-    if (groups > 1) {
-        const double per = (double)rows / groups, want = per + 1.4 * std::sqrt(per);
-        for (int bm : {16, 32, 64, 96, 144})
-            if (want <= bm)
-                return bm;
-        return per < 192 ? 128 : 256;
+    const double per = (double)rows / groups;
+    Fp8Tile best{16, 256};
+    double least = 1e300;
+    const auto take = [&](int bm, int cols, double first, double round, double cus) {
+        double tiles = groups == 1                       ? (double)((rows + bm - 1) / bm)
+                       : per + 1.4 * std::sqrt(per) <= bm ? (double)std::min<int64_t>(rows, groups)
+                                                          : (double)rows / bm + 0.5 * groups;
+        tiles *= (double)((N + cols - 1) / cols);
+        const double t = tiles <= cus ? first : groups == 1 ? std::ceil(tiles / 256) * round
+                                                            : (tiles / 256 + 0.5) * round;
+        if (t < least) {
+            least = t;
+            best = Fp8Tile{bm, cols};
+        }
+    };
+    for (int bm : {16, 32, 64, 96, 128, 144, 256}) {
+        const double t = std::max(92.0, 60 + 1.1 * bm);
+        if (bm != 256 || !f32)
+            take(bm, swiglu ? 128 : 256, t, t, 256);
     }
-    for (int bm : {256, 128, 64})
-        if (rows > bm / 2 && (rows + bm - 1) / bm * ((cols + 255) / 256) >= 256)
-            return bm;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    if (narrow)
+        take(64, 64, 90, 72, 512);
+    return best;
 }
 
 int64_t fp8_row_tiles(int64_t rows, int groups, int bm)
@@ -632,7 +668,7 @@ int64_t fp8_row_tiles(int64_t rows, int groups, int bm)
 namespace {
 
 template <int EPI>
-void launch_bm(const Fp8Args &p, int bm, hipStream_t st)
+void launch_rows(const Fp8Args &p, int bm, hipStream_t st)
 {
     switch (bm) {
     case 16: launch_cfg<4, 16, 4, 1, 4, EPI>(p, st); break;
@@ -647,17 +683,17 @@ void launch_bm(const Fp8Args &p, int bm, hipStream_t st)
 
 }  // namespace
 
-void launch_fp8_matmul(const Fp8Args &p, int bm, hipStream_t st)
+void launch_fp8_matmul(const Fp8Args &p, Fp8Tile t, hipStream_t st)
 {
     if (p.exps)
-        launch_bm<EPI_STAGE>(p, bm, st);
+        launch_rows<EPI_STAGE>(p, t.rows, st);
     else if (fp8_split_ok(p))
         launch_fp8_split(p, st);
-    else if (!p.offsets && bm == 64 && (int64_t)p.mtiles * ((p.N + 255) / 256) < 256)
-        launch_cfg<2, 64, 2, 2, 3, EPI_PLAIN>(p, st);  // tiles of 64 columns, to fill the chip
+    else if (t.cols == 64)
+        launch_cfg<2, 64, 2, 2, 3, EPI_PLAIN>(p, st);
     else
-        launch_bm<EPI_PLAIN>(p, bm, st);
+        launch_rows<EPI_PLAIN>(p, t.rows, st);
 }
-void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st) { launch_bm<EPI_SWIGLU>(p, bm, st); }
+void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st) { launch_rows<EPI_SWIGLU>(p, bm, st); }
 
 }  // namespace moe

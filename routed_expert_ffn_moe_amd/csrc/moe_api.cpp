@@ -200,8 +200,10 @@ Layout layout(const moe_shape_t *s, int Tc)
     Layout L{};
     const moe::ExpertArgs a = expert_shape(s, Tc);
     const bool f8 = s->w_dtype == MOE_FP8;
-    L.bm_gu = f8 ? moe::fp8_bm((int64_t)Tc * s->top_k, s->E, s->H) : moe::gemm_bm_gu(a);
-    L.bm_dc = f8 ? L.bm_gu : moe::gemm_bm_dc(a);
+    L.bm_gu = f8 ? moe::fp8_size((int64_t)Tc * s->top_k, s->E, s->I, true, false, false).rows
+                  : moe::gemm_bm_gu(a);
+    L.bm_dc = f8 ? moe::fp8_size((int64_t)Tc * s->top_k, s->E, s->H, false, false, false).rows
+                  : moe::gemm_bm_dc(a);
     L.max_tiles_gu = max_tiles(Tc, s, L.bm_gu);
     L.max_tiles_dc = max_tiles(Tc, s, L.bm_dc);
     L.ntn_gu = moe::stream_ntn(a, true);
@@ -480,7 +482,7 @@ int fp8_products(const moe_shape_t *s, const moe_weights_t *w, const void *x, in
     d.G = s->E;
     d.mtiles = L.max_tiles_dc;
     d.vec = 1;
-    moe::launch_fp8_matmul(d, L.bm_dc, st);
+    moe::launch_fp8_matmul(d, moe::Fp8Tile{L.bm_dc, 256}, st);
     return launched("down");
 }
 

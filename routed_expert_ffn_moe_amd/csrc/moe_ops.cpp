@@ -145,8 +145,8 @@ int moe_matmul_fp8(const moe_matmul_t *s, const void *a, const float *sa, const 
         return bad("moe_matmul_fp8: a matrix b or 256 rows of a reach 2^32 bytes");
     if (s->G > 1 && !offsets)
         return bad("moe_matmul_fp8: G > 1 needs offsets");
-    const int bm = moe::fp8_bm(s->M, s->G, s->N);
-    const int64_t mtiles = moe::fp8_row_tiles(s->M, s->G, bm);
+    const moe::Fp8Tile t = moe::fp8_size(s->M, s->G, s->N, false, s->out_dtype == MOE_F32, true);
+    const int64_t mtiles = moe::fp8_row_tiles(s->M, s->G, t.rows);
     if (mtiles * cdiv(s->N, 32) >= (int64_t)1 << 31 || s->G > 65535)
         return bad("moe_matmul_fp8: too many tiles or groups");
     if (s->M == 0)
@@ -182,7 +182,7 @@ int moe_matmul_fp8(const moe_matmul_t *s, const void *a, const float *sa, const 
     p.out_f32 = s->out_dtype == MOE_F32;
     // whole words, with 32-bit offsets inside a tile of up to 256 rows
     p.vec = aligned(y, 16) && ldy * esz % 16 == 0 && s->N % 16 == 0 && 256 * ldy * esz < (int64_t)1 << 31;
-    moe::launch_fp8_matmul(p, bm, (hipStream_t)stream);
+    moe::launch_fp8_matmul(p, t, (hipStream_t)stream);
     return moe::api_launched("moe_matmul_fp8");
 }
 

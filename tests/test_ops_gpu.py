@@ -372,9 +372,9 @@ def test_matmul_many_groups(M, G):
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1000, 4200, 260), (2000, 4200, 1100), (4000, 4100, 130), (4000, 4100, 900)])
 def test_matmul_more_tiles_than_workgroups(M, N, K, out):
-    """One matrix of 272 tiles of 64, 128 and 256 rows: a workgroup takes several,
-    the copies of the next begin while the last steps of one still run (or, in
-    few steps of K, after them)."""
+    """One matrix of more tiles than CUs: a workgroup takes several, the copies of
+    the next begin while the last steps of one still run (or, in few steps of K,
+    after them)."""
     check_matmul(M, N, K, out)
 
 
