@@ -81,14 +81,14 @@ __global__ __launch_bounds__(512) void fp8_split(Fp8Args p)
             }
             // a block behind the last one is the last one again, with a scale
             // of 0 (no branch, behind which its loads would be moved)
-            fw[u] = k0 + u * KS < p.KB ? sw[kb] : 0.0f;
+            fw[u] = sw[kb];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
                 const Fp8Frag<EXACT> b(B[u][m]);
-                const float f = fr[u][m] * fw[u];
+                const float f = k0 + u * KS < p.KB ? fr[u][m] * fw[u] : 0.0f;
 #pragma unroll
                 for (int c = 0; c < NB; ++c) {
                     const floatx4 t = mfma_fp8(Fp8Frag<EXACT>(A[u][c]), b);
@@ -249,9 +249,9 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
         p.h[(int64_t)pair * p.I + n0 + lane] = silu(acc) * up;
 }
 
-constexpr int DW = 16;  // waves of fp8_token_down, and most slots of a token
-constexpr int DN = 8;   // its columns of y: an MFMA's rows 8..15 repeat 0..7
-
+// DN columns of y of a token (of 8, an MFMA's rows 8..15 repeat 0..7) by DW
+// waves, no fewer than a token's slots.
+template <int DN, int DW>
 __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
 {
     extern __shared__ float s_t[];  // [k][KB][DN] sums of blocks, then [k][KB] their scales
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
         const float acc = chain<DN>(s_t + w * KB * DN + (l16 & (DN - 1)), s_f + w * KB, KB);
         uint32_t ex = stage_exponent(acc);
 #pragma unroll
-        for (int d = 1; d < DN; d <<= 1)
+        for (int d = 1; d < 8; d <<= 1)
             ex = max(ex, (uint32_t)__shfl_xor((int)ex, d));
         ex = max(ex, STAGE_MIN_EXP);
         if (lane < DN)
@@ -350,11 +350,29 @@ bool fp8_decode_ok(int T, int H, int k, int I)
     return T <= 8 && H / FP8_BLOCK <= 256 && (int64_t)k * (I / FP8_BLOCK) <= 512;
 }
 
+namespace {
+
+template <int DN, int DW>
+void launch_token_down(const Fp8Decode &p, hipStream_t st)
+{
+    const size_t units = (size_t)p.k * (p.I / FP8_BLOCK);
+    fp8_token_down<DN, DW><<<(unsigned)(p.T * (p.H / DN)), 64 * DW, units * (DN + 1) * 4, st>>>(p);
+}
+
+}  // namespace
+
 void launch_fp8_decode(const Fp8Decode &p, hipStream_t st)
 {
-    const int kb = p.H / FP8_BLOCK, units = p.k * (p.I / FP8_BLOCK);
+    const int kb = p.H / FP8_BLOCK;
     fp8_pair_gate_up<<<(unsigned)(p.T * p.k * (p.I / 16)), 64 * GW, (size_t)kb * 34 * 4, st>>>(p);
-    fp8_token_down<<<(unsigned)(p.T * (p.H / DN)), 64 * DW, (size_t)units * (DN + 1) * 4, st>>>(p);
+    // Few columns: the smallest groups of them, to use every CU; else larger
+    // ones, of fewer waves where the slots allow it, so that several share a CU.
+    if (p.T * (p.H / 8) <= 256)
+        launch_token_down<8, 16>(p, st);
+    else if (p.k <= 8)
+        launch_token_down<16, 8>(p, st);
+    else
+        launch_token_down<16, 16>(p, st);
 }
 
 }  // namespace moe
