@@ -192,6 +192,11 @@ struct QuantArgs {
 };
 void launch_quant_fp8(const QuantArgs &a, hipStream_t st);
 
+// The permutation of given routing and the codes of x (bf16, K a multiple of 8)
+// in one launch, for passes of few pairs (permute.hip).
+bool permute_quant_ok(int T, int k, int E);
+void launch_permute_quant(const PermuteArgs &a, const QuantArgs &q, hipStream_t st);
+
 // Products of E4M3 codes with block scales (matmul_fp8.hip).
 constexpr int FP8_MAX_K = 32768;  // K whose weight scales fit the kernels' LDS
 struct Fp8Args {

@@ -415,27 +415,43 @@ int route_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, int 
     return launched("permute");
 }
 
+// Given routing of n tokens with FP8 experts is permuted in the launch that
+// makes the codes of x.
+bool fp8_unpermuted(const moe_shape_t *s, int n)
+{
+    return s->w_dtype == MOE_FP8 && moe::permute_quant_ok(n, s->top_k, s->E);
+}
+
 // The FP8 experts' two products of one permuted pass: x as codes, gate and up
-// with h as codes, and down into the staging rows.
-int fp8_products(const moe_shape_t *s, const moe_weights_t *w, const void *x, int n, char *ws,
-                 const Layout &L, hipStream_t st)
+// with h as codes, and down into the staging rows.  idx: given routing that is
+// yet to be permuted, or null.
+int fp8_products(const moe_shape_t *s, const moe_weights_t *w, const void *x, int n, const int32_t *idx,
+                 char *ws, const Layout &L, hipStream_t st)
 {
     const int KB = s->H / moe::FP8_K, IB = s->I / moe::FP8_K;
     int rc;
+    moe::QuantArgs q{};
+    q.x = x;
+    q.codes = (uint8_t *)(ws + L.f8_x);
+    q.scales = (float *)(ws + L.f8_sx);
+    q.ld = q.K = s->H;
+    q.R = n;
+    q.KB = KB;
+    q.block_rows = 1;
+    q.bf16 = 1;
+    if (idx) {
+        StageScope sc(1, st);
+        moe::launch_permute_quant(permute_args(s, n, idx, ws, L), q, st);
+        if ((rc = launched("permute_quant")))
+            return rc;
+    }
     {
         StageScope sc(2, st);
-        moe::QuantArgs q{};
-        q.x = x;
-        q.codes = (uint8_t *)(ws + L.f8_x);
-        q.scales = (float *)(ws + L.f8_sx);
-        q.ld = q.K = s->H;
-        q.R = n;
-        q.KB = KB;
-        q.block_rows = 1;
-        q.bf16 = 1;
-        moe::launch_quant_fp8(q, st);
-        if ((rc = launched("quant_fp8")))
-            return rc;
+        if (!idx) {
+            moe::launch_quant_fp8(q, st);
+            if ((rc = launched("quant_fp8")))
+                return rc;
+        }
         moe::Fp8Args g{};
         g.a = q.codes;
         g.sa = q.scales;
@@ -521,7 +537,7 @@ int expert_pass(const moe_shape_t *s, const moe_weights_t *w, const void *x, voi
     if (fp8_decode(s, Tc))
         return fp8_decode_pass(s, w, x, y, n, idx, wts, ws, L, st);
     if (s->w_dtype == MOE_FP8) {
-        if ((rc = fp8_products(s, w, x, n, ws, L, st)))
+        if ((rc = fp8_products(s, w, x, n, given && fp8_unpermuted(s, n) ? idx : nullptr, ws, L, st)))
             return rc;
     } else {
         moe::ExpertArgs a = expert_shape(s, n);
@@ -858,7 +874,7 @@ int moe_experts(const moe_shape_t *s, const moe_weights_t *w, const void *x,
         Layout Lw = L;
         Lw.max_tiles_gu = max_tiles(n, s, L.bm_gu);
         Lw.max_tiles_dc = max_tiles(n, s, L.bm_dc);
-        {
+        if (!fp8_unpermuted(s, n)) {
             StageScope sc(1, st);
             moe::launch_permute(permute_args(s, n, idx, wsb, Lw), st);
         }

@@ -14,8 +14,11 @@
 // histogram; positions come from ballot-based ranks inside waves that walk
 // their pairs in order, so the grouped order is t ascending, then j, within
 // every expert, the same as a stable counting sort.
+#include <algorithm>
+
 #include "common.h"
 #include "kernels.h"
+#include "quant_fp8.h"
 
 namespace moe {
 
@@ -25,6 +28,9 @@ constexpr int PAIRS_PER_BLOCK = PERMUTE_PAIRS_PER_BLOCK;
 constexpr int FUSED_HIST = 8192;
 // Most permutation blocks placed by permute_place (see launch_permute).
 constexpr int PLACE_MAX_BLOCKS = 256;
+
+// Most blocks whose pairs each placing workgroup counts by itself.
+constexpr int COUNT_MAX_BLOCKS = 16;
 
 // Orders one wave's LDS accesses across its lanes (no other wave shares
 // the data).
@@ -92,7 +98,15 @@ __device__ __forceinline__ void scan_groups(
     const int tid = threadIdx.x;
     const int G = E + (shared ? 1 : 0);  // groups
     constexpr int SCH = 16;
-    if constexpr (!POS) {
+    if (!POS && idx) {
+        for (int e = tid; e < E; e += 1024)
+            s_cnt[e] = 0;
+        __syncthreads();
+        for (int p = tid; p < n_pairs; p += 1024)
+            if (const int e = pair_expert(idx, p, n_pairs, E); e >= 0)
+                atomicAdd(&s_cnt[e], 1);
+        __syncthreads();
+    } else if constexpr (!POS) {
         // column sums over blocks only
         for (int e = tid; e < E; e += 1024) {
             int run = 0;
@@ -285,7 +299,9 @@ __global__ __launch_bounds__(1024) void permute_scan(
 // earlier blocks, both formed here from the histograms; inside the block the
 // waves follow in order and a wave's lanes with equal experts are ranked by
 // a ballot-built match mask.  The same grouped order as permute_scatter (t,
-// then j, within every expert).
+// then j, within every expert).  COUNT: the sums of the histograms are counted
+// from the pairs (all of them; COUNT_MAX_BLOCKS bounds that work) instead.
+template <bool COUNT>
 __device__ __forceinline__ void place_block(const int32_t *__restrict__ idx,
                                             const int32_t *__restrict__ blk, int nblk, int b,
                                             int32_t *__restrict__ row_src,
@@ -303,7 +319,25 @@ __device__ __forceinline__ void place_block(const int32_t *__restrict__ idx,
     constexpr int SCH = 16;
     // column sums over all blocks (the expert's rows) and over those before b
     int tot = 0, pre = 0;
-    if (tid < E) {
+    if constexpr (COUNT) {
+        __shared__ int32_t s_tot[1024], s_pre[1024];
+        s_tot[tid] = s_pre[tid] = 0;
+        __syncthreads();
+        int ev[COUNT_MAX_BLOCKS];  // all reads in flight together
+#pragma unroll
+        for (int i = 0; i < COUNT_MAX_BLOCKS; ++i)
+            ev[i] = pair_expert(idx, i * PAIRS_PER_BLOCK + tid, n_pairs, E);
+#pragma unroll
+        for (int i = 0; i < COUNT_MAX_BLOCKS; ++i)
+            if (ev[i] >= 0) {
+                atomicAdd(&s_tot[ev[i]], 1);  // integer counts: order-free
+                if (i < b)
+                    atomicAdd(&s_pre[ev[i]], 1);
+            }
+        __syncthreads();
+        tot = s_tot[tid];
+        pre = s_pre[tid];
+    } else if (tid < E) {
         for (int b0 = 0; b0 < nblk; b0 += SCH) {
             int c[SCH];
 #pragma unroll
@@ -389,7 +423,38 @@ __global__ __launch_bounds__(1024) void permute_place(
                            items_b, ntn_b, wrows_b);
         return;
     }
-    place_block(idx, blk, nblk, blockIdx.x, row_src, row_tok, row_of, n_pairs, E, T, k, shared);
+    place_block<false>(idx, blk, nblk, blockIdx.x, row_src, row_tok, row_of, n_pairs, E, T, k, shared);
+}
+
+// The permutation of a short pass and the codes of its rows of x, in one launch:
+// workgroup 0 forms the counts, offsets and tile lists, the next nblk place their
+// blocks' pairs, each counting what it needs from the pairs themselves, and the
+// others quantise.  (In launches of their own these are three, each waiting for
+// the one before.)
+__global__ __launch_bounds__(1024) void permute_quant(PermuteArgs a, QuantArgs q, int nblk, int n_pairs)
+{
+    const int b = (int)blockIdx.x - 1;
+    if (b < 0)  // uniform
+        scan_groups<false>(a.idx, nullptr, a.counts, a.offsets, a.tiles_a, a.ntiles_a, a.tiles_b,
+                           a.ntiles_b, a.bm_a, a.bm_b, nblk, a.E, n_pairs, a.T, 0, nullptr, 0, 0, nullptr,
+                           0, 0);
+    else if (b < nblk)
+        place_block<true>(a.idx, nullptr, nblk, b, a.row_src, a.row_tok, a.row_of, n_pairs, a.E, a.T, a.k, 0);
+    else
+        quant_row_blocks<true, true>(q, (int64_t)(b - nblk) * 64 + (threadIdx.x >> 4),
+                                     (int64_t)(gridDim.x - 1 - nblk) * 64);
+}
+
+bool permute_quant_ok(int T, int k, int E)
+{
+    return permute_blocks(T * k) <= COUNT_MAX_BLOCKS && E <= 1024;
+}
+
+void launch_permute_quant(const PermuteArgs &a, const QuantArgs &q, hipStream_t st)
+{
+    const int n_pairs = a.T * a.k, nblk = permute_blocks(n_pairs);
+    const int64_t wgs = std::min<int64_t>(((int64_t)q.R * q.KB + 63) / 64, 1024);
+    permute_quant<<<(unsigned)(1 + nblk + wgs), 1024, 0, st>>>(a, q, nblk, n_pairs);
 }
 
 // Stable scatter.  Each of a block's 4 waves walks a quarter of its pairs 64

@@ -9,74 +9,16 @@
 // NaN element gets the NaN code, and all of a block with an infinity does.
 #include <type_traits>
 
-#include "common.h"
-#include "fp8.h"
-#include "kernels.h"
+#include "quant_fp8.h"
 
 namespace moe {
 
 namespace {
 
-// The 8 elements at column c of a row, 0 behind K.  VEC: K and the row
-// stride are multiples of 8 elements (4 for fp32) and the rows 16-byte
-// aligned, so the 8 are all inside or all behind.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const void *x, int64_t row, int c, int K)
-{
-    if constexpr (VEC) {
-        if (c >= K) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = 0.0f;
-        } else if constexpr (BF16) {
-            const uint4 r = *(const uint4 *)((const uint16_t *)x + row + c);
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        } else {
-            const float4 p = *(const float4 *)((const float *)x + row + c);
-            const float4 q = *(const float4 *)((const float *)x + row + c + 4);
-            v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
-            v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t at = row + c + i;
-            v[i] = c + i >= K ? 0.0f : BF16 ? bf2f(((const uint16_t *)x)[at]) : ((const float *)x)[at];
-        }
-    }
-}
-
-__device__ __forceinline__ float amax8(const float (&v)[8])
-{
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, fabsf(v[i]));
-    return m;
-}
-
-// One 1 x 128 block per 16 lanes, 8 elements a lane.
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(256) void quant_rows(QuantArgs a)
 {
-    const int64_t n = (int64_t)a.R * a.KB;
-    const int sub = threadIdx.x & 15;
-    for (int64_t b = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); b < n; b += (int64_t)gridDim.x * 16) {
-        const int64_t r = b / a.KB;
-        const int c = (int)(b - r * a.KB) * FP8_BLOCK + sub * 8;
-        float v[8];
-        load8<BF16, VEC>(v, a.x, r * a.ld, c, a.K);
-        const Fp8Block q = fp8_block(row16_max(amax8(v)));
-        *(uint2 *)(a.codes + b * FP8_BLOCK + sub * 8) =
-            uint2{fp8x4(v[0], v[1], v[2], v[3], q), fp8x4(v[4], v[5], v[6], v[7], q)};
-        if (sub == 0)
-            a.scales[b] = q.scale;
-    }
+    quant_row_blocks<BF16, VEC>(a, (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), (int64_t)gridDim.x * 16);
 }
 
 // One 128 x 128 block per workgroup: 16 rows a pass, the values kept in
@@ -136,7 +78,7 @@ void launch_quant_fp8(const QuantArgs &a, hipStream_t st)
 {
     if (a.R == 0)
         return;
-    const bool vec = a.K % 8 == 0 && a.ld % (a.bf16 ? 8 : 4) == 0 && (uintptr_t)a.x % 16 == 0;
+    const bool vec = a.K % 8 == 0;
     if (a.bf16)
         vec ? launch_typed<true, true>(a, st) : launch_typed<true, false>(a, st);
     else
