@@ -400,8 +400,14 @@ def moe_quant_fp8(quant, x, codes, scales, stream=None) -> None:
 
 def quant_fp8(x, block_rows=1, stream=None):
     """(codes, scales) of a device tensor [R, K] or [E, N, K] (N a multiple of
-    block_rows), bf16 or float32; unit stride along K."""
+    block_rows), bf16 or float32.  With `stream`, the outputs (and a copy of
+    x, if its rows are not of unit stride) are allocated and written on it."""
     import torch
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return quant_fp8(x, block_rows)
     if x.dim() not in (2, 3) or (x.dim() == 3 and x.shape[1] % block_rows):
         raise ValueError("quant_fp8 takes [R, K], or [E, N, K] with N a multiple of block_rows")
     if x.dim() == 3 or x.stride(1) != 1 or x.stride(0) < x.shape[1]:
@@ -413,7 +419,7 @@ def quant_fp8(x, block_rows=1, stream=None):
     scales = torch.empty(*lead[:-1], -(-lead[-1] // block_rows), kb, dtype=torch.float32, device=x.device)
     src = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(x.dtype, -1)
     moe_quant_fp8(moe_quant_t(R, K, block_rows, src, x.stride(0) if x.dim() == 2 and R > 1 else 0), x,
-                  codes, scales, stream)
+                  codes, scales)
     return codes, scales
 
 

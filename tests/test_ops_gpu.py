@@ -274,6 +274,27 @@ def test_quant_strided_rows_and_helper():
         assert torch.equal(codes[e].cpu().double(), rq)
 
 
+def test_quant_helper_copies_on_the_stream_it_runs_on():
+    """x transposed, so that the helper copies it first, on a stream that has
+    work before it."""
+    g = gen(10)
+    x = randn(g, 4096, 2048, dtype=torch.bfloat16).cuda()
+    want = moe.quant_fp8(x.t().contiguous())
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for s in (st, st.cuda_stream):
+        junk = torch.empty(2048, 4096, dtype=torch.bfloat16, device="cuda").fill_(math.nan)
+        del junk  # its block would be taken for a copy made on the current stream
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                x.add_(0)
+        got = moe.quant_fp8(x.t(), stream=s)
+        st.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 # ---- matmul -----------------------------------------------------------------
 
 def codes_of(g, *shape):
