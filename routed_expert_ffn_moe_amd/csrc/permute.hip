@@ -29,7 +29,8 @@ constexpr int FUSED_HIST = 8192;
 // Most permutation blocks placed by permute_place (see launch_permute).
 constexpr int PLACE_MAX_BLOCKS = 256;
 
-// Most blocks whose pairs each placing workgroup counts by itself.
+// Most blocks whose pairs each placing workgroup counts by itself: that work
+// grows with the square of their number, and a thread holds a pair of each.
 constexpr int COUNT_MAX_BLOCKS = 16;
 
 // Orders one wave's LDS accesses across its lanes (no other wave shares
@@ -429,8 +430,9 @@ __global__ __launch_bounds__(1024) void permute_place(
 // The permutation of a short pass and the codes of its rows of x, in one launch:
 // workgroup 0 forms the counts, offsets and tile lists, the next nblk place their
 // blocks' pairs, each counting what it needs from the pairs themselves, and the
-// others quantise.  (In launches of their own these are three, each waiting for
-// the one before.)
+// others quantise.  In launches of their own these are three, each waiting for
+// the one before: a call with T=16, E=8 took 37.6 us with them and 31.0 with this
+// one, T=2048, k=8, E=256 331 and 323 (this launch 10).
 __global__ __launch_bounds__(1024) void permute_quant(PermuteArgs a, QuantArgs q, int nblk, int n_pairs)
 {
     const int b = (int)blockIdx.x - 1;
