@@ -10,8 +10,8 @@
 //                   (token, slot) pair and 16 columns of h, no permutation;
 //                   the pair's x is quantised on the way.
 //  fp8_token_down   their down projections and the combine: one workgroup per
-//                   token and 8 or 16 columns of y, h quantised on the way.
-// T=1, H=2048, k=8, I=768: 8.7 + 11.3 us (38 MB take 6.2): each is a chain of
+//                   token and 16 columns of y, h quantised on the way.
+// T=1, H=2048, k=8, I=768: 8.7 + 11.0 us (38 MB take 6.2): each is a chain of
 // indices, weights, MFMA, LDS and the sums of the blocks in their order.
 //
 // The decode kernels pass the sums of single blocks of K through LDS and join
@@ -252,9 +252,10 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
         p.h[(int64_t)pair * p.I + n0 + lane] = silu(acc) * up;
 }
 
-// DN columns of y of a token (of 8, an MFMA's rows 8..15 repeat 0..7) by DW
-// waves, no fewer than a token's slots.
-template <int DN, int DW>
+constexpr int DN = 16;  // columns of y of a workgroup
+
+// DW waves, no fewer than a token's slots
+template <int DW>
 __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
 {
     extern __shared__ float s_t[];  // [k][KB][DN] sums of blocks, then [k][KB] their scales
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
             const int q = min(u0 + u * DW, units - 1), kb = q - q / KB * KB;
             // an empty slot reads expert 0, and nobody its results
             const int64_t ev = (unsigned)e[u] < (unsigned)p.E ? e[u] : 0;
-            W[u] = frag_at(p.w_down + (ev * p.H + n0 + (l16 & (DN - 1))) * p.I, kb, lg);
+            W[u] = frag_at(p.w_down + (ev * p.H + n0 + l16) * p.I, kb, lg);
             fw[u] = p.s_down[(ev * (p.H >> 7) + (n0 >> 7)) * KB + kb];
         }
 #pragma unroll
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
             float sh;
             const Fp8Frag<false> B(one_row_frag(hv[u].x, hv[u].y, s_code[w], lane, sh));
             const floatx4 o = mfma_fp8(Fp8Frag<false>(W[u]), B);
-            if (q < units && l16 == 0 && lg < DN / 4)
+            if (q < units && l16 == 0)
                 *(floatx4 *)(s_t + q * DN + lg * 4) = o;
             if (q < units && lane == 0)
                 s_f[q] = sh * fw[u];
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(64 * DW) void fp8_token_down(Fp8Decode p)
     // wave j: slot j's outputs, rounded as a staging row is
     const bool mine = (unsigned)my_e < (unsigned)p.E;
     if (mine) {
-        const float acc = chain<DN>(s_t + w * KB * DN + (l16 & (DN - 1)), s_f + w * KB, KB);
+        const float acc = chain<DN>(s_t + w * KB * DN + l16, s_f + w * KB, KB);
         uint32_t ex = stage_exponent(acc);
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1)
@@ -356,31 +357,21 @@ bool fp8_decode_ok(int T, int H, int k, int I)
     return T <= 8 && H / FP8_BLOCK <= 256 && (int64_t)k * (I / FP8_BLOCK) <= 512;
 }
 
-namespace {
-
-template <int DN, int DW>
-void launch_token_down(const Fp8Decode &p, hipStream_t st)
-{
-    const size_t units = (size_t)p.k * (p.I / FP8_BLOCK);
-    fp8_token_down<DN, DW><<<(unsigned)(p.T * (p.H / DN)), 64 * DW, units * (DN + 1) * 4, st>>>(p);
-}
-
-}  // namespace
-
 void launch_fp8_decode(const Fp8Decode &p, hipStream_t st)
 {
-    const int kb = p.H / FP8_BLOCK;
+    const int kb = p.H / FP8_BLOCK, units = p.k * (p.I / FP8_BLOCK);
     fp8_pair_gate_up<<<(unsigned)(p.T * p.k * (p.I / 16)), 64 * GW, (size_t)kb * 34 * 4, st>>>(p);
-    // Few columns: the smallest groups of them, to use every CU; else larger
-    // ones, of fewer waves where the slots allow it, so that several share a CU
-    // (both products: T=1, H=3840, I=1536, k=1 20.1 us with 8 columns, 13.8 with
-    // 16; T=8, H=2048, I=768, k=8 88 and 55).
-    if (p.T * (p.H / 8) <= 256)
-        launch_token_down<8, 16>(p, st);
-    else if (p.k <= 8)
-        launch_token_down<16, 8>(p, st);
+    // Eight waves where the slots allow it, which start sooner and share a CU with
+    // another group's: where their 32 units in flight are all there are (T=1,
+    // H=1536, I=512, k=8 11.7 us for both products, 13.7 with sixteen waves) or the
+    // groups are more than the CUs take at once (T=8, H=2048, I=768, k=8 55 and
+    // 88).  Else sixteen (T=1, H=2048, I=768, k=8 16.5 us, 17.5 with eight).
+    const unsigned grid = (unsigned)(p.T * (p.H / DN));
+    const size_t lds = (size_t)units * (DN + 1) * 4;
+    if (p.k <= 8 && (units <= 32 || grid > 128))
+        fp8_token_down<8><<<grid, 64 * 8, lds, st>>>(p);
     else
-        launch_token_down<16, 16>(p, st);
+        fp8_token_down<16><<<grid, 64 * 16, lds, st>>>(p);
 }
 
 }  // namespace moe
