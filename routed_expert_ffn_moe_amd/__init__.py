@@ -297,7 +297,11 @@ def _begin(stream):
     if _device is None:
         import torch
         _types()
-        _device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -1
+        if torch.cuda.is_available():
+            torch.cuda.current_device()  # initialised from here on
+            _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        else:
+            _device = lambda: -1  # noqa: E731
         # the current stream's handle without building a Stream object
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     dev = _device()

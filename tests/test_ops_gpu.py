@@ -484,6 +484,21 @@ def test_experts(T, E, k, H, I):
     say("bound over y: %.3g" % float(tol.norm() / want.norm()))
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 64, 8, 512, 1024), (1, 16, 2, 128, 128), (3, 20, 16, 384, 256),
+                                       (8, 32, 12, 2176, 128), (8, 8, 8, 640, 640), (2, 16, 3, 4096, 256),
+                                       (1, 4, 4, 256, 16384)])
+def test_experts_decode_rows_have_the_bits_of_long_passes(T, E, k, H, I):
+    """Few rows in the kernels of their own, and as the first rows of a longer pass."""
+    g = gen(T + k)
+    L = Experts(E, H, I, T)
+    x = randn(g, 20, H, dtype=torch.bfloat16)
+    idx, w = routing(g, 20, E, k)
+    y = L.run(x[:T].contiguous().cuda(), idx[:T].contiguous().cuda(), w[:T].contiguous().cuda())
+    want, tol = L.ref(x[:T], idx[:T], w[:T])
+    within(y, want, tol + 1e-30, "decode rows T%d k%d H%d I%d" % (T, k, H, I))
+    assert torch.equal(y, L.run(x.cuda(), idx.cuda(), w.cuda())[:T])
+
+
 @pytest.mark.parametrize("per", [10, 20, 45, 70, 100, 150, 220])
 def test_experts_of_every_tile_height(per):
     """Every tile height, in more tiles than there are CUs."""
