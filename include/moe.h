@@ -290,7 +290,7 @@ typedef struct {
  * K must hold zero codes, as moe_quant_fp8 writes them), sa [M, Kp / 128],
  * b [G, N, Kp] codes, sb [G, N / 128 rounded up, Kp / 128], offsets [G + 1]
  * (G = 1: NULL takes all rows), y [M, N].  a and b 16-byte aligned, the others
- * element aligned; y overlaps neither a nor sa. */
+ * element aligned; y overlaps none of the operands. */
 int moe_matmul_fp8(const moe_matmul_t *matmul, const void *a, const float *sa, const void *b,
                    const float *sb, const int32_t *offsets, void *y, void *stream);
 

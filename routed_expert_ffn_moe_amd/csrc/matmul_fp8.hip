@@ -112,10 +112,8 @@ struct Cfg {
     // Scales of the weights, of two tiles
     static constexpr int NSB = EPI == EPI_SWIGLU ? 2 : (BR + 127) / 128;  // rows of them
     static constexpr int SIDE = EPI == EPI_SWIGLU ? WN * BM * 4 : 0;      // block maxima / next rows
-    static constexpr int KBC = ST * STAGE + 3 * CHUNK + 2 * NSB * MAX_KB * 4 + SIDE <= 163840
-                                   ? MAX_KB : MAX_KB / 2;
     static constexpr int O_CHUNK = ST * STAGE, O_W = O_CHUNK + 3 * CHUNK,
-                         O_SIDE = O_W + 2 * NSB * KBC * 4, LDS = O_SIDE + SIDE;
+                         O_SIDE = O_W + 2 * NSB * MAX_KB * 4, LDS = O_SIDE + SIDE;
     static constexpr int OCC = 163840 / LDS;                      // workgroups of a CU
     // Stores of a wave and tile (EPI_PLAIN: bf16 in whole words; more otherwise)
     static constexpr int NS = EPI == EPI_SWIGLU ? 2 * MB : EPI == EPI_STAGE ? 3 * MB : MB * (NBW / 2);
@@ -227,7 +225,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
             const float *src = EPI == EPI_SWIGLU && q ? p.s1 : p.s0;
             const int nb = EPI == EPI_SWIGLU ? t.n0 >> 7 : min((t.n0 >> 7) + q, ((p.N + 127) >> 7) - 1);
             dma4(src + gs + (int64_t)nb * KB, (uint32_t)min(at + ln, KB - 1) * 4,
-                 lds + C::O_W + (uint32_t)(((pt & 1) * C::NSB + q) * C::KBC + at) * 4);
+                 lds + C::O_W + (uint32_t)(((pt & 1) * C::NSB + q) * MAX_KB + at) * 4);
         }
         ++pt;
         pk = 0;
@@ -310,14 +308,14 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         Fp8Raw v;
         float s;
     };
-    const float *s_w = (const float *)(smem + C::O_W) + ((ct & 1) * C::NSB + nsb) * C::KBC;
+    const float *s_w = (const float *)(smem + C::O_W) + ((ct & 1) * C::NSB + nsb) * MAX_KB;
     auto load_weights = [&](Weights &a, int s) {
         const uint8_t *wt = smem + ((cq + s) % ST) * C::STAGE + wn * (NBW * 2048);
 #pragma unroll
         for (int c = 0; c < NBW; ++c)
             a.v[c] = fp8_raw(*(const uint4 *)(wt + c * 2048 + o0), *(const uint4 *)(wt + c * 2048 + o1));
         a.s0 = s_w[s];
-        a.s1 = EPI == EPI_SWIGLU ? s_w[C::KBC + s] : 0.0f;
+        a.s1 = EPI == EPI_SWIGLU ? s_w[MAX_KB + s] : 0.0f;
     };
     auto load_block = [&](Block &b, int s, int m) {
         const uint8_t *st = smem + ((cq + s) % ST) * C::STAGE + C::BR * 128;

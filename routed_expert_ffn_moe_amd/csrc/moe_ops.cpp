@@ -158,8 +158,10 @@ int moe_matmul_fp8(const moe_matmul_t *s, const void *a, const float *sa, const 
         !aligned(offsets, 4) || !aligned(y, esz))
         return bad("moe_matmul_fp8: a or b not 16-byte, or another pointer not element aligned");
     const int64_t yb = ((s->M - 1) * ldy + s->N) * esz;
-    if (overlap(y, yb, a, (s->M - 1) * lda + Kp) || overlap(y, yb, sa, s->M * KB * 4))
-        return bad("moe_matmul_fp8: y overlaps a or sa");
+    const int64_t bb = (s->G * (int64_t)s->N - 1) * ldb + Kp, sbb = s->G * cdiv(s->N, moe::FP8_K) * KB * 4;
+    if (overlap(y, yb, a, (s->M - 1) * lda + Kp) || overlap(y, yb, sa, s->M * KB * 4) ||
+        overlap(y, yb, b, bb) || overlap(y, yb, sb, sbb))
+        return bad("moe_matmul_fp8: y overlaps an operand");
     if (const int rc = moe::api_check_device())
         return rc;
     moe::Fp8Args p{};

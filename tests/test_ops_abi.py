@@ -85,7 +85,7 @@ def call_matmul(a=ptr(1), sa=ptr(2), b=ptr(3), sb=ptr(4), off=None, y=ptr(5), **
     dict(N=1 << 30), dict(lda=1 << 25), dict(a=0), dict(sa=0), dict(b=0), dict(sb=0), dict(y=0),
     dict(a=ptr(1) + 8), dict(b=ptr(3) + 4), dict(sa=ptr(2) + 2), dict(sb=ptr(4) + 1),
     dict(off=ptr(6) + 2), dict(y=ptr(5) + 1), dict(y=ptr(5) + 2, out_dtype=0), dict(y=ptr(1)),
-    dict(y=ptr(2)),
+    dict(y=ptr(2)), dict(y=ptr(3)), dict(y=ptr(4)),
 ])
 def test_matmul_refusals(bad):
     fails(call_matmul(**bad), moe.MOE_EINVAL, "moe_matmul_fp8")
