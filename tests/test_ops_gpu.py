@@ -426,6 +426,24 @@ def test_matmul_nan_stays_in_its_row_and_column(M):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [3, 20, 40])
+def test_matmul_infinite_scale_of_a_row(M, out):
+    """The last block's scale of a row infinite: y there is infinite with the
+    sign of that block's sum, in whatever way K is divided."""
+    g = gen(M)
+    a, sa, b, sb = operands(g, M, 96, 384)
+    sa[1, 2] = math.inf
+    y = torch.empty(M, 96, dtype=DT[out], device="cuda")
+    moe.moe_matmul_fp8(moe.make_matmul(M, 96, 384, out=out), a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), y)
+    t = a[1, 256:].double() @ b[0, :, 256:].double().t()
+    # sums far from what the FP8 instruction may lose of them (2^-10 of the products)
+    sure = t.abs() > 2.0 ** -9 * (a[1, 256:].double().abs() @ b[0, :, 256:].double().abs().t())
+    got = y[1].cpu().double()
+    assert int(sure.sum()) > 60 and torch.equal(got[sure], torch.sign(t[sure]) * math.inf)
+    assert torch.isfinite(y[0]).all() and torch.isfinite(y[2:]).all()
+
+
 # ---- experts ----------------------------------------------------------------
 
 class Experts:
