@@ -218,8 +218,8 @@ struct Fp8Args {
 struct Fp8Tile {
     int rows, cols;
 };
-// narrow: tiles of 64 columns are allowed
-Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool f32, bool narrow);
+// exact: the codes are multiplied as bf16; narrow: tiles of 64 columns are allowed
+Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool exact, bool narrow);
 int64_t fp8_row_tiles(int64_t rows, int groups, int bm);         // upper bound of the row tiles
 void launch_fp8_matmul(const Fp8Args &p, Fp8Tile t, hipStream_t st);
 void launch_fp8_gate_up(const Fp8Args &p, int bm, hipStream_t st);

@@ -8,7 +8,8 @@
 // One scaled-format MFMA of 16 x 16 x 128 covers exactly one scale block, so
 // the sum inside a block stays in the matrix core and the blocks are joined
 // by one fp32 FMA per output and block, with the product of the two scales
-// (fp32 results multiply the codes as bf16, four MFMAs per block: fp8.h).
+// (fp32 results and the sums of gate and up multiply the codes as bf16, four
+// MFMAs per block: fp8.h).
 // The weights are the MFMA's A operand and the rows of `a` its B operand: a
 // lane then holds one row of y, whose scale is one register, and adjacent
 // columns, which it stores as whole words.
@@ -609,11 +610,15 @@ void launch_cfg(const Fp8Args &p, hipStream_t st)
     using C = Cfg<NBW, BM, WN, WM, ST, EPI>;
     const int64_t tiles = (int64_t)p.mtiles * ((p.N + C::COLS - 1) / C::COLS);
     const unsigned grid = (unsigned)(std::min<int64_t>(tiles, 256 * C::OCC) + 7) / 8 * 8;
-    if constexpr (EPI == EPI_PLAIN && BM < 256) {  // fp8_size
-        if (p.out_f32)
-            return fp8_tile<NBW, BM, WN, WM, ST, EPI, true><<<grid, 64 * C::NW, 0, st>>>(p);
+    if constexpr (EPI == EPI_SWIGLU) {
+        fp8_tile<NBW, BM, WN, WM, ST, EPI, true><<<grid, 64 * C::NW, 0, st>>>(p);
+    } else {
+        if constexpr (EPI == EPI_PLAIN && BM < 256) {  // fp8_size
+            if (p.out_f32)
+                return fp8_tile<NBW, BM, WN, WM, ST, EPI, true><<<grid, 64 * C::NW, 0, st>>>(p);
+        }
+        fp8_tile<NBW, BM, WN, WM, ST, EPI, false><<<grid, 64 * C::NW, 0, st>>>(p);
     }
-    fp8_tile<NBW, BM, WN, WM, ST, EPI, false><<<grid, 64 * C::NW, 0, st>>>(p);
 }
 
 }  // namespace
@@ -633,7 +638,7 @@ void launch_cfg(const Fp8Args &p, hipStream_t st)
 // N=1024, K=640: 7.3 us with 64 x 64, 14.7 with 256 rows).  The largest tiles' fp32
 // output would need more registers than there are (71 us against 33 in the first
 // of these), so it goes without them.
-Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool f32, bool narrow)
+Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool exact, bool narrow)
 {
     const double per = (double)rows / groups;
     Fp8Tile best{16, 256};
@@ -652,7 +657,7 @@ Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool f32, boo
     };
     for (int bm : {16, 32, 64, 96, 128, 144, 256}) {
         const double t = std::max(92.0, 60 + 1.1 * bm);
-        if (bm != 256 || !f32)
+        if (bm != 256 || !exact)
             take(bm, swiglu ? 128 : 256, t, t, 256);
     }
     if (narrow)
@@ -676,8 +681,13 @@ void launch_rows(const Fp8Args &p, int bm, hipStream_t st)
     case 64: launch_cfg<4, 64, 4, 2, 3, EPI>(p, st); break;
     case 96: launch_cfg<4, 96, 4, 2, 3, EPI>(p, st); break;
     case 128: launch_cfg<4, 128, 4, 2, 3, EPI>(p, st); break;
-    case 144: launch_cfg<4, 144, 4, 2, 3, EPI>(p, st); break;
-    default: launch_cfg<4, 256, 4, 2, 2, EPI>(p, st); break;
+    case 256:
+        if constexpr (EPI != EPI_SWIGLU) {  // fp8_size
+            launch_cfg<4, 256, 4, 2, 2, EPI>(p, st);
+            break;
+        }
+        [[fallthrough]];
+    default: launch_cfg<4, 144, 4, 2, 3, EPI>(p, st); break;
     }
 }
 

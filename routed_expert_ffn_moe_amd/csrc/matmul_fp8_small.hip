@@ -229,8 +229,9 @@ __global__ __launch_bounds__(64 * GW) void fp8_pair_gate_up(Fp8Decode p)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = k0 + u * GW;
-            const floatx4 g = mfma_fp8(Fp8Frag<false>(G[u]), Fp8Frag<false>(B[u]));
-            const floatx4 v = mfma_fp8(Fp8Frag<false>(V[u]), Fp8Frag<false>(B[u]));
+            const Fp8Frag<true> b(B[u]);  // the exact sums that codes of h need (fp8.h)
+            const floatx4 g = mfma_fp8(Fp8Frag<true>(G[u]), b);
+            const floatx4 v = mfma_fp8(Fp8Frag<true>(V[u]), b);
             if (kb < KB && l16 == 0) {
                 *(floatx4 *)(s_t + kb * 16 + lg * 4) = g;
                 *(floatx4 *)(s_t + (KB + kb) * 16 + lg * 4) = v;

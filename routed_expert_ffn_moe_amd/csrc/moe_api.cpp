@@ -200,7 +200,7 @@ Layout layout(const moe_shape_t *s, int Tc)
     Layout L{};
     const moe::ExpertArgs a = expert_shape(s, Tc);
     const bool f8 = s->w_dtype == MOE_FP8;
-    L.bm_gu = f8 ? moe::fp8_size((int64_t)Tc * s->top_k, s->E, s->I, true, false, false).rows
+    L.bm_gu = f8 ? moe::fp8_size((int64_t)Tc * s->top_k, s->E, s->I, true, true, false).rows
                   : moe::gemm_bm_gu(a);
     L.bm_dc = f8 ? moe::fp8_size((int64_t)Tc * s->top_k, s->E, s->H, false, false, false).rows
                   : moe::gemm_bm_dc(a);

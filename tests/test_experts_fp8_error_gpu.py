@@ -1,0 +1,111 @@
+"""How far y of the FP8 experts is from its definition, per token in the
+2-norm and per element.
+
+The bounds hold the kernels to sums in fp32.  Every rounding of h to a code
+that such sums leave open is allowed, no other: a sum in fewer bits than
+fp32's moves codes that are further from a midpoint, each by a step of 6 to
+12% of its value, and shows."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU visible", allow_module_level=True)
+
+import ops_ref as ref  # noqa: E402
+from test_ops_gpu import Experts, gen, randn, routing, say  # noqa: E402
+
+# An fp32 sum of K products p_i of random signs.  128 additions a block of K,
+# the partial sums below 4 sqrt(i) s (s: rms of the products), each addition off by
+# 2^-24 of its result at most and by 1/sqrt(3) of that in the mean square:
+# 4 * 128 / sqrt(2) / sqrt(3) * 2^-24 s = 209 * 2^-24 s, which is 18.5 * 2^-24 of the
+# 2-norm of the products of one block, and of all of them (blocks in quadrature).
+# Joining up to 32 blocks: sqrt(32 / 2) * 4 / sqrt(3) = 9.2 of the same unit.
+# Together 20.7 * 2^-24 < 2^-19.
+SUM = 2.0 ** -19
+# A rounding to bf16 is uniform in +- 2^-8 of the value's power of two: in the mean
+# square 2^-8 / sqrt(3) = 0.00226 of the value at most (0.0016 for values spread over
+# a power of two, the room for the scatter of a sum of squares).
+BF16 = 0.0023
+# Likewise 2^-11 / sqrt(3) for the half staging rows, for each slot.
+HALF = 2.0 ** -11 / math.sqrt(3) * 1.1
+# The down products' sums in the FP8 instruction: 7 of 8 products each cut by up to 2^-13 of
+# the largest, in the mean square 2^-13 / sqrt(3), of random signs: sqrt(7 / 3) * 2^-13.
+CUT = math.sqrt(7 / 3) * 2.0 ** -13
+
+
+def expected(L, x, idx, w):
+    """(y, 2-norm bound of each token's error, bound of each element's error), float64."""
+    m = L.mats
+    T, k = idx.shape
+    H = x.shape[1]
+    qx, sx, _ = ref.quant(x)
+    xv = ref.rows_value(qx, sx)
+    y = torch.zeros(T, H, dtype=torch.float64)
+    sq = torch.zeros(T, dtype=torch.float64)  # squares of the independent parts
+    el = torch.zeros(T, H, dtype=torch.float64)
+    for e in range(L.E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        if not t.numel():
+            continue
+        wg, wu = ref.matrix_value(m["w_gate"][e], m["s_gate"][e]), ref.matrix_value(m["w_up"][e], m["s_up"][e])
+        g, u = xv[t] @ wg.t(), xv[t] @ wu.t()
+        dg = SUM * ((xv[t] ** 2) @ (wg ** 2).t()).sqrt()
+        du = SUM * ((xv[t] ** 2) @ (wu ** 2).t()).sqrt()
+        sig = torch.sigmoid(g)
+        h = g * sig * u
+        # silu' <= 1.1; eight roundings, and the exponential's argument off by 2^-24 of itself
+        dh = 1.1 * dg * u.abs() + (g * sig).abs() * du + (8 + g.abs()) * ref.U32 * h.abs()
+        qh, sh, v = ref.quant(h)
+        step, off = ref.e4m3_grid(v)[1:]
+        wide = sh.repeat_interleave(ref.BLOCK, 1)
+        # the largest value's error moves the scale and, against it, the quotients
+        at = (h.abs().view(len(t), -1, ref.BLOCK)).argmax(2, keepdim=True)
+        dtop = dh.view(len(t), -1, ref.BLOCK).gather(2, at)[:, :, 0].repeat_interleave(ref.BLOCK, 1)
+        top = wide * ref.E4M3_MAX
+        dv = (dh * ref.E4M3_MAX + v.abs() * dtop) / top + 4 * ref.U32 * v.abs()
+        flip = torch.where(off <= dv, step, torch.zeros_like(step)) * wide
+        wd = ref.matrix_value(m["w_down"][e], m["s_down"][e])
+        hv = ref.rows_value(qh, sh)
+        o = hv @ wd.t()
+        cut = CUT * ((hv ** 2) @ (wd ** 2).t()).sqrt()
+        c = w[t, j].double()[:, None]
+        y.index_add_(0, t, c * o)
+        part = (HALF * o) ** 2 + cut ** 2
+        sq.index_add_(0, t, (c ** 2 * part).sum(1) + (c ** 2 * flip ** 2 * (wd ** 2).sum(0)).sum(1))
+        # single elements: half a step, six times the mean square of the cuts, every open code moved
+        el.index_add_(0, t, c * (2.0 ** -11 * o.abs() + 6 * cut + flip @ wd.abs().t()))
+    norm = y.norm(dim=1)
+    return y, ((BF16 * norm) ** 2 + sq).sqrt(), el + 2.0 ** -8 * (y.abs() + el)
+
+
+def check(L, x, idx, w, y, what):
+    want, bound, el = expected(L, x, idx, w)
+    size = want.norm(dim=1)
+    assert bool((bound < 0.02 * size).all()) and bool((el.norm(dim=1) < 0.05 * size).all()), "the bounds bind"
+    d = y.cpu().double() - want
+    err = d.norm(dim=1)
+    r = err / size
+    say("[%s] error of a token: median %.5f, largest %.5f; of its bound %.3f; elements %.3f" %
+        (what, float(r.median()), float(r.max()), float((err / bound).max()), float((d.abs() / el).max())))
+    far, out = int((~(err <= bound)).sum()), int((~(d.abs() <= el)).sum())
+    assert far == 0 and out == 0, (what, far, out, float(r.max()))
+
+
+@pytest.mark.parametrize("H,I,k", [(2048, 768, 8), (1024, 256, 2), (4096, 512, 4)])
+def test_error_of_single_tokens(H, I, k):
+    """256 tokens one by one, by eights, and in one pass (the same bits)."""
+    T, E = 256, 16
+    g = gen(H + I)
+    L = Experts(E, H, I, k)
+    x = randn(g, T, H, dtype=torch.bfloat16)
+    idx, w = routing(g, T, E, k)
+    xd, id_, wd = x.cuda(), idx.cuda(), w.cuda()
+    one = torch.cat([L.run(xd[t:t + 1], id_[t:t + 1], wd[t:t + 1]) for t in range(T)])
+    eight = torch.cat([L.run(xd[t:t + 8], id_[t:t + 8], wd[t:t + 8]) for t in range(0, T, 8)])
+    check(L, x, idx, w, one, "single tokens H%d I%d k%d" % (H, I, k))
+    assert torch.equal(one, eight) and torch.equal(one, L.run(xd, id_, wd))
