@@ -128,9 +128,33 @@ struct Cfg {
     // 860.)
     static constexpr bool SPREAD = ST == 3 && NW == 8;
     static constexpr int LEAD = SPREAD ? ST - 1 : ST;
+    // The next tile's row numbers (EPI_SWIGLU) are copied behind the first LEAD
+    // stages and the stores of the tile before, and read when the next tile's
+    // copies begin, before step kb - LEAD.  Whether a wait has covered that copy by
+    // then: the wave's operations since it (`newer`), counted as the loop issues
+    // them, are no fewer than the wait leaves outstanding.  A wait that leaves NS
+    // stores out does not cover it, since the stores are older than the copy.
+    static constexpr bool rows_arrive(int kb)
+    {
+        int newer = 0;
+        for (int s = 0; s < kb - LEAD; ++s) {
+            const int copies = L + ((s + LEAD) % CH == 0 ? CI : 0);
+            if (SPREAD)
+                newer += copies;
+            const int left = (ST - 2) * L + (s < LEAD - 1 ? NS : ST == 3 && (s + 2) % CH == 0 ? CI : 0);
+            if (newer >= left)
+                return true;
+            if (!SPREAD)
+                newer += copies;
+        }
+        return false;
+    }
     // Depth from which a tile's last stages are multiplied while the next
-    // tile's first ones are copied (its rows are known by then).
-    static constexpr int DEEP = ST + LEAD - 1;
+    // tile's first ones are copied.  With row numbers to wait for, the step before
+    // has to be behind the first LEAD - 1, whose waits leave stores out.
+    static constexpr int DEEP = std::max(ST + LEAD - 1, EPI == EPI_SWIGLU ? 2 * LEAD : 0);
+    static_assert(EPI != EPI_SWIGLU || (rows_arrive(DEEP) && rows_arrive(DEEP + 1) && rows_arrive(DEEP + 2) &&
+                                        rows_arrive(DEEP + 3)), "the next rows are there when they are read");
     static_assert(BR / 8 % NW == 0, "weight copies divide among the waves");
     static_assert(EPI != EPI_SWIGLU || (COLS == 128 && NBW % 2 == 0), "a tile of h is one scale block wide");
     static_assert(LDS <= 163840, "LDS of one workgroup");

@@ -17,6 +17,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
 import ops_ref as ref  # noqa: E402
+import routed_expert_ffn_moe_amd as moe  # noqa: E402
 from test_ops_gpu import Experts, gen, randn, routing, say  # noqa: E402
 
 # An fp32 sum of K products p_i of random signs.  128 additions a block of K,
@@ -38,21 +39,34 @@ HALF = 2.0 ** -11 / math.sqrt(3) * 1.1
 CUT = math.sqrt(7 / 3) * 2.0 ** -13
 
 
-def expected(L, x, idx, w):
-    """(y, 2-norm bound of each token's error, bound of each element's error), float64."""
-    m = L.mats
-    T, k = idx.shape
-    H = x.shape[1]
-    qx, sx, _ = ref.quant(x)
-    xv = ref.rows_value(qx, sx)
-    y = torch.zeros(T, H, dtype=torch.float64)
-    sq = torch.zeros(T, dtype=torch.float64)  # squares of the independent parts
-    el = torch.zeros(T, H, dtype=torch.float64)
-    for e in range(L.E):
+def quant(x):
+    """ref.quant's 1 x 128 form where x is: (code values, scales, quotients), float64."""
+    R, K = x.shape
+    p = x.double().view(R, K // ref.BLOCK, ref.BLOCK)
+    top = p.abs().amax(2).clamp(min=ref.TINY)
+    v = p * ref.E4M3_MAX / top[:, :, None]
+    return ref.e4m3_grid(v)[0].view(R, K), top / ref.E4M3_MAX, v.view(R, K)
+
+
+def matrix(m, name, e):
+    c, s = m["w_" + name][e].double(), m["s_" + name][e].double()
+    return c * s.repeat_interleave(ref.BLOCK, 0).repeat_interleave(ref.BLOCK, 1)
+
+
+def expected(m, E, x, idx, w):
+    """(y, 2-norm bound of each token's error, bound of each element's error), float64, of the
+    matrices m on x's device."""
+    T, H = x.shape
+    qx, sx, _ = quant(x)
+    xv = qx * sx.repeat_interleave(ref.BLOCK, 1)
+    y = torch.zeros(T, H, dtype=torch.float64, device=x.device)
+    sq = torch.zeros(T, dtype=torch.float64, device=x.device)  # squares of the independent parts
+    el = torch.zeros_like(y)
+    for e in range(E):
         t, j = (idx == e).nonzero(as_tuple=True)
         if not t.numel():
             continue
-        wg, wu = ref.matrix_value(m["w_gate"][e], m["s_gate"][e]), ref.matrix_value(m["w_up"][e], m["s_up"][e])
+        wg, wu = matrix(m, "gate", e), matrix(m, "up", e)
         g, u = xv[t] @ wg.t(), xv[t] @ wu.t()
         dg = SUM * ((xv[t] ** 2) @ (wg ** 2).t()).sqrt()
         du = SUM * ((xv[t] ** 2) @ (wu ** 2).t()).sqrt()
@@ -60,7 +74,7 @@ def expected(L, x, idx, w):
         h = g * sig * u
         # silu' <= 1.1; eight roundings, and the exponential's argument off by 2^-24 of itself
         dh = 1.1 * dg * u.abs() + (g * sig).abs() * du + (8 + g.abs()) * ref.U32 * h.abs()
-        qh, sh, v = ref.quant(h)
+        qh, sh, v = quant(h)
         step, off = ref.e4m3_grid(v)[1:]
         wide = sh.repeat_interleave(ref.BLOCK, 1)
         # the largest value's error moves the scale and, against it, the quotients
@@ -69,8 +83,8 @@ def expected(L, x, idx, w):
         top = wide * ref.E4M3_MAX
         dv = (dh * ref.E4M3_MAX + v.abs() * dtop) / top + 4 * ref.U32 * v.abs()
         flip = torch.where(off <= dv, step, torch.zeros_like(step)) * wide
-        wd = ref.matrix_value(m["w_down"][e], m["s_down"][e])
-        hv = ref.rows_value(qh, sh)
+        wd = matrix(m, "down", e)
+        hv = qh * wide
         o = hv @ wd.t()
         cut = CUT * ((hv ** 2) @ (wd ** 2).t()).sqrt()
         c = w[t, j].double()[:, None]
@@ -83,11 +97,11 @@ def expected(L, x, idx, w):
     return y, ((BF16 * norm) ** 2 + sq).sqrt(), el + 2.0 ** -8 * (y.abs() + el)
 
 
-def check(L, x, idx, w, y, what):
-    want, bound, el = expected(L, x, idx, w)
+def check(m, E, x, idx, w, y, what):
+    want, bound, el = expected(m, E, x, idx, w)
     size = want.norm(dim=1)
     assert bool((bound < 0.02 * size).all()) and bool((el.norm(dim=1) < 0.05 * size).all()), "the bounds bind"
-    d = y.cpu().double() - want
+    d = y.double() - want
     err = d.norm(dim=1)
     r = err / size
     say("[%s] error of a token: median %.5f, largest %.5f; of its bound %.3f; elements %.3f" %
@@ -107,5 +121,37 @@ def test_error_of_single_tokens(H, I, k):
     xd, id_, wd = x.cuda(), idx.cuda(), w.cuda()
     one = torch.cat([L.run(xd[t:t + 1], id_[t:t + 1], wd[t:t + 1]) for t in range(T)])
     eight = torch.cat([L.run(xd[t:t + 8], id_[t:t + 8], wd[t:t + 8]) for t in range(0, T, 8)])
-    check(L, x, idx, w, one, "single tokens H%d I%d k%d" % (H, I, k))
+    check(L.dev, E, xd, id_, wd, one, "single tokens H%d I%d k%d" % (H, I, k))
     assert torch.equal(one, eight) and torch.equal(one, L.run(xd, id_, wd))
+
+
+class Wide(Experts):
+    """Many large experts, made on the GPU."""
+
+    def __init__(self, E, H, I, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.E, self.H, self.I, self.dev = E, H, I, {}
+        for n, r, c in (("gate", I, H), ("up", I, H), ("down", H, I)):
+            v = torch.randn(E, r, c, generator=g, device="cuda")
+            self.dev["w_" + n] = v.mul_(120).clamp_(-448, 448).to(torch.float8_e4m3fn)
+            self.dev["s_" + n] = (torch.rand(E, r // 128, c // 128, generator=g, device="cuda") + 0.5) / \
+                (120 * math.sqrt(c))
+        self.weights = moe.make_weights(None, **self.dev)
+
+
+# Rows an expert that take gate+up tiles of 16, 32, 64, 96, 128 and 144 rows, and the sizes
+# around the depth (blocks of 128 of H) from which a workgroup's next tile is copied
+# while the last one is multiplied: 8 for tiles of 16 and 32 rows, 4 for the others.
+@pytest.mark.parametrize("per,H", [(per, H) for per in (8, 20) for H in (768, 896, 1024, 1152)] +
+                         [(per, H) for per in (45, 75, 100, 118) for H in (384, 512, 640)])
+def test_many_gate_up_tiles_of_a_workgroup(per, H):
+    """32 column tiles of each of 28 experts: three tiles a workgroup and more, so
+    that tiles follow a tile that has stored, with uneven groups of rows."""
+    E, I = 28, 4096
+    L = Wide(E, H, I, per + H)
+    g = gen(per * H)
+    x = randn(g, E * per, H, dtype=torch.bfloat16).cuda()
+    idx, w = (t.cuda() for t in routing(g, E * per, E, 1, 0.1))
+    y = L.run(x, idx, w)
+    check(L.dev, E, x, idx, w, y, "%d rows an expert, H%d" % (per, H))
+    assert torch.equal(y, L.run(x, idx, w))
