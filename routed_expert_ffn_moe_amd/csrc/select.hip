@@ -372,6 +372,21 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
     if (lane < a.k && nk > -INFINITY)
         fine = (lv == nl && bv == nb) ||
                (bias ? kv - nk > key_slack(kv, a.softmax) : logits_apart(kv, nk, top, a.softmax));
+    // The last one selected and the one behind it may be equal, logit and bias:
+    // then it is the next different key that must be apart (it may be larger in 64
+    // bits, or equal there, with a lower index).
+    if (__any(lane == a.k - 1 && nk > -INFINITY && lv == nl && bv == nb)) {
+        const float kl = __shfl(kv, a.k - 1), ll = __shfl(lv, a.k - 1), bl = __shfl(bv, a.k - 1);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = lane + 64 * i;
+            if (!may(e) || !(key[i] > -INFINITY) || key[i] > kl)
+                continue;
+            const bool same = l[i] == ll && (!bias || a.bias[e] == bl);
+            fine &= same || (bias ? kl - key[i] > key_slack(kl, a.softmax)
+                                  : logits_apart(kl, key[i], top, a.softmax));
+        }
+    }
     if (!sure)
         return false;
     if (!__all(fine)) {

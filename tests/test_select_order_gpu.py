@@ -1,0 +1,49 @@
+"""moe_select where the order rests on what fp32 does not show, against the
+64-bit definition (ops_ref.select)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU visible", allow_module_level=True)
+
+from test_ops_gpu import check_select, gen  # noqa: E402
+
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("logits,bias,k,score", [
+    ([17.0, 17.0, 17.125], 0.0, 1, "sigmoid"),            # one fp32 key, 64-bit ones apart
+    ([40.0, 50.0, 50.0], None, 1, "sigmoid"),             # equal 64-bit scores: the lowest index
+    ([0.0, -20.0, -20.0, -19.875], 0.5, 2, "softmax"),    # scores far below the bias's rounding
+    ([17.0, 3.0, 17.0, 17.125, 17.125], 0.0, 2, "sigmoid"),
+    ([0.0, -690.0, -680.0, -680.0], None, 2, "softmax"),  # scores near the smallest 64-bit ones
+    ([5.0, 5.0, 5.0, 5.0], None, 4, "sigmoid"),           # nothing behind the last place
+])
+def test_equal_scores_on_the_last_place(logits, bias, k, score):
+    l = torch.tensor([logits], dtype=BF)
+    check_select(l, None if bias is None else torch.full((len(logits),), bias), k, score=score)
+    check_select(l.float(), None if bias is None else torch.full((len(logits),), bias), k, score=score)
+    # the same among others that are far below
+    wide = torch.full((1, 150), -3.0 if score == "sigmoid" else -700.0)
+    wide[0, 20:20 + len(logits)] = l[0].float()
+    check_select(wide, None if bias is None else torch.full((150,), bias), k, score=score)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bias", [None, "zero", "equal", "few"])
+@pytest.mark.parametrize("ng,tg", [(1, 1), (8, 3)])
+def test_few_distinct_scores(score, bias, ng, tg):
+    """Rows of a few values whose fp32 keys are equal or next to equal."""
+    g = gen(ng + len(bias or ""))
+    v = torch.tensor([16.5, 17.0, 17.125, 17.25, 40.0, 50.0] if score == "sigmoid" else
+                     [-20.0, -19.875, -19.75, -18.0, -17.5, 2.0])
+    b = {None: None, "zero": torch.zeros(64), "equal": torch.full((64,), 0.25),
+         "few": torch.tensor([0.0, 0.125, 0.25])[torch.randint(0, 3, (64,), generator=g)]}[bias]
+    for n in (2, 3, 6):
+        l = v[torch.randint(0, n, (40, 64), generator=g)]
+        for k in (1, 3, 8):
+            check_select(l.to(BF), b, k, "%d values, k=%d" % (n, k), score=score, n_group=ng, topk_group=tg,
+                         group_score="top2")
