@@ -330,9 +330,20 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
             if (m2 > -INFINITY)
                 val += bias ? m2 : score(m2);
         }
+        // Bound of the value's error: 7/8 of a slack a key (half, and 3 units of 2^-24
+        // for the roundings of the sum and of the bound added to it), all of the larger
+        // key's size, which the sum need not have (keys of opposite signs).
+        float err = 0.0f;
+        if (bias || a.group_top2) {
+            const float size = !bias ? 1.0f : fmaxf(m1 > -INFINITY ? fabsf(m1) : 0.0f,
+                                                    a.group_top2 && m2 > -INFINITY ? fabsf(m2) : 0.0f);
+            err = (a.group_top2 ? 1.75f : 0.875f) * key_slack(size, a.softmax);
+        }
         wave_lds_sync();
-        if (g < a.n_group && (lane & (per - 1)) == 0)
+        if (g < a.n_group && (lane & (per - 1)) == 0) {
             row[g] = val;
+            row[a.n_group + g] = err;
+        }
         wave_lds_sync();
         // rank by counting; lane g < n_group for group g
         const float mine = lane < a.n_group ? row[lane] : -INFINITY;
@@ -343,13 +354,13 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
         }
         const bool in = lane < a.n_group && rank < a.topk_group;
         open = __ballot(in);
-        // the gap between the last open and the first closed group
-        const float lo = -key_value(wave_max_u32(order_key(in ? -mine : -INFINITY)));
-        const float hi = key_value(wave_max_u32(order_key(lane < a.n_group && !in ? mine : -INFINITY)));
+        // the gap between the open and the closed groups: the least that an open
+        // one's value may be, against the most that a closed one's may
+        const float off = lane < a.n_group ? row[a.n_group + lane] : 0.0f;
+        const float lo = -key_value(wave_max_u32(order_key(in ? off - mine : -INFINITY)));
+        const float hi = key_value(wave_max_u32(order_key(lane < a.n_group && !in ? mine + off : -INFINITY)));
         if (hi > -INFINITY)  // (groups of masked experts only are in order)
-            sure = a.group_top2 ? lo - hi > 2.0f * key_slack(fmaxf(fabsf(lo), fabsf(hi)), a.softmax)
-                   : bias       ? lo - hi > key_slack(fmaxf(fabsf(lo), fabsf(hi)), a.softmax)
-                                : logits_apart(lo, hi, top, a.softmax);
+            sure = bias || a.group_top2 ? lo > hi : logits_apart(lo, hi, top, a.softmax);
     }
     auto may = [&](int e) { return e < a.E && (!grouped || (open >> (e / gs & 63)) & 1); };
     uint32_t ok[PER];

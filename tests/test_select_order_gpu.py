@@ -47,3 +47,22 @@ def test_few_distinct_scores(score, bias, ng, tg):
         for k in (1, 3, 8):
             check_select(l.to(BF), b, k, "%d values, k=%d" % (n, k), score=score, n_group=ng, topk_group=tg,
                          group_score="top2")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6])
+def test_group_keys_that_cancel(score, size):
+    """Groups valued by the sum of two keys near +size and -size: the sum is of the
+    scores' size, the rounding of the fp32 keys of theirs.  Biases are powers of two
+    apart from the scores, so that 64-bit sums are exact to 1e-9."""
+    g = gen(int(size))
+    T, ng, per = 64, 8, 8
+    l = torch.randn(T, ng * per, generator=g)
+    b = torch.full((ng, per), -4 * size)
+    b[:, 2], b[:, 5] = size, -size
+    check_select(l, b.reshape(-1), 4, "size %g" % size, score=score, n_group=ng, topk_group=3, group_score="top2")
+    # one group of such keys among ordinary ones
+    c = torch.randn(ng, per, generator=g) * 0.1
+    c[3] = b[3]
+    check_select(l, c.reshape(-1), 4, "one of size %g" % size, score=score, n_group=ng, topk_group=3,
+                 group_score="top2")
