@@ -253,8 +253,8 @@ __device__ __forceinline__ void select_refine(const SelectArgs &a, int t, const 
 }
 
 // Token t in fp32, and where a gap is too small to be sure of the order, in 64
-// bits among the experts in question; false if they are too many, or if the
-// doubt is between groups.
+// bits among the experts in question; false if they are too many, if the doubt is
+// between groups, or if the selected scores are too small for fp32.
 template <int PER, bool BF16>
 __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *row, int &my_e, float &my_w)
 {
@@ -430,6 +430,9 @@ __device__ __forceinline__ bool select_fast(const SelectArgs &a, int t, float *r
     }
     // weights; a masked expert (key -inf) has none
     const bool live = lane < a.k && lv > -INFINITY && kv > -INFINITY;
+    // sigmoid scores that fp32 does not hold (from e^-88 on): their ratios are weights all the same
+    if (!a.softmax && __any(live && lv < -80.0f))
+        return false;
     float s;
     if (a.softmax) {
         const float base = a.renorm ? key_value(wave_max_u32(order_key(live ? lv : -INFINITY))) : top;

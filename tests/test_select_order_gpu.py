@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
-from test_ops_gpu import check_select, gen  # noqa: E402
+from test_ops_gpu import check_select, gen, run_select  # noqa: E402
 
 BF = torch.bfloat16
 
@@ -66,3 +66,25 @@ def test_group_keys_that_cancel(score, size):
     c[3] = b[3]
     check_select(l, c.reshape(-1), 4, "one of size %g" % size, score=score, n_group=ng, topk_group=3,
                  group_score="top2")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_scores_below_the_smallest_fp32_value(score, renorm):
+    """The selected scores are near e^-100 (softmax: all but one of them)."""
+    g = gen(9)
+    l = -100 + torch.randn(20, 48, generator=g)
+    if score == "softmax":
+        l[:, 5] = 0
+    for b in (None, torch.randn(48, generator=g) * 0.1):
+        check_select(l, b, 6, score=score, renorm=renorm)
+        check_select(l, b, 6, score=score, renorm=renorm, n_group=6, topk_group=3, group_score="top2")
+    # sums of scores from e^-80 to e^-700, and weights scaled up again
+    for low in (-80.0, -87.0, -89.0, -104.0, -300.0, -690.0):
+        check_select(low + torch.randn(8, 48, generator=g), None, 6, score=score, renorm=renorm)
+
+
+def test_renormalised_weights_of_small_scores_sum_to_the_scale():
+    idx, w = run_select((-95 - torch.arange(32.0)).view(1, 32).cuda(), None, 4, score="sigmoid", scale=2.5)
+    assert idx.tolist() == [[0, 1, 2, 3]]
+    assert abs(float(w.double().sum()) - 2.5) < 4 * 2.5 * 2.0 ** -24
