@@ -160,7 +160,8 @@ int moe_matmul_fp8(const moe_matmul_t *s, const void *a, const float *sa, const 
     const int64_t yb = ((s->M - 1) * ldy + s->N) * esz;
     const int64_t bb = (s->G * (int64_t)s->N - 1) * ldb + Kp, sbb = s->G * cdiv(s->N, moe::FP8_K) * KB * 4;
     if (overlap(y, yb, a, (s->M - 1) * lda + Kp) || overlap(y, yb, sa, s->M * KB * 4) ||
-        overlap(y, yb, b, bb) || overlap(y, yb, sb, sbb))
+        overlap(y, yb, b, bb) || overlap(y, yb, sb, sbb) ||
+        (offsets && overlap(y, yb, offsets, (s->G + (int64_t)1) * 4)))
         return bad("moe_matmul_fp8: y overlaps an operand");
     if (const int rc = moe::api_check_device())
         return rc;

@@ -197,3 +197,10 @@ def test_binding_refuses_tensors_it_cannot_pass():
         moe.quant_fp8(torch.zeros(4))
     with pytest.raises(ValueError, match="block_rows"):
         moe.quant_fp8(torch.zeros(2, 100, 128), block_rows=128)
+
+
+@pytest.mark.parametrize("y", [ptr(6), ptr(6) + 4, ptr(6) - 8 * 96 * 2 + 2])
+def test_matmul_refuses_a_y_that_overlaps_the_offsets(y):
+    """Workgroups read the offsets while others store y."""
+    fails(call_matmul(G=3, off=ptr(6), y=y), moe.MOE_EINVAL, "overlaps")
+    assert call_matmul(G=3, off=ptr(6), y=ptr(6) + 16, M=0) == moe.MOE_OK
