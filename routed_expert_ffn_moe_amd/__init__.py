@@ -168,6 +168,10 @@ class _Weights:
     def __init__(self, layout, **tensors):
         self._keep = tensors
         self.c = moe_weights_t(**{k: _ptr(v) for k, v in tensors.items()}, layout=layout)
+        # what lies behind those pointers, and the FP8 sizes (E, H, I, device) found to fit it
+        self._held = {k: (v.dtype, v.numel(), v.get_device()) for k, v in tensors.items()
+                      if v is not None and not isinstance(v, int)}
+        self._fits = set()
 
 
 def _is_packed(t) -> bool:
@@ -192,6 +196,31 @@ def _check(rc: int):
         raise MoeError(rc, moe_last_error())
 
 
+def _fp8_fit(s, weights, dev) -> None:
+    """Refuse expert matrices and scales that an FP8 shape would read out of
+    range: of another type, on another device, or of fewer elements."""
+    key = (s.E, s.H, s.I, dev)
+    if s.w_dtype != MOE_FP8 or key in weights._fits:
+        return
+    if _SRC is None:
+        _types()
+    for name in ("w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down"):
+        if name not in weights._held:  # NULL, which the library refuses, or the caller's own pointer
+            continue
+        dtype, held, on = weights._held[name]
+        types, block = (_CODES, 1) if name[0] == "w" else (_F32, 128)
+        if dtype not in types:
+            raise ValueError("%s: dtype %s, expected %s" % (name, dtype, " or ".join(map(str, types))))
+        if on < 0:
+            raise ValueError("%s is not on a GPU" % name)
+        if on != dev:
+            raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, on, dev))
+        need = s.E * (s.H // block) * (s.I // block)
+        if held < need:
+            raise ValueError("%s holds %d elements, E=%d, H=%d, I=%d take %d" % (name, held, s.E, s.H, s.I, need))
+    weights._fits.add(key)
+
+
 def moe_workspace_bytes(shape: moe_shape_t) -> int:
     return int(load().moe_workspace_bytes(ctypes.byref(shape)))
 
@@ -200,6 +229,8 @@ def moe_forward(shape, weights, x, y, topk_idx, topk_w, ws, ws_bytes=None, strea
     """y[T,H] and the routing of x[T,H]; asynchronous on `stream`."""
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    if shape.w_dtype == MOE_FP8:
+        _fp8_fit(shape, weights, _begin(stream)[1])
     _check(load().moe_forward(ctypes.byref(shape), ctypes.byref(weights.c), _ptr(x), _ptr(y),
                               _ptr(topk_idx), _ptr(topk_w), _ptr(ws), ws_bytes,
                               _stream(stream)))
@@ -210,6 +241,8 @@ MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 def moe_forward_noalloc(shape, weights, x, y, topk_idx, topk_w, stream=None) -> None:
     """moe_forward on the library's static device scratch (allocates nothing)."""
+    if shape.w_dtype == MOE_FP8:
+        _fp8_fit(shape, weights, _begin(stream)[1])
     _check(load().moe_forward_noalloc(ctypes.byref(shape), ctypes.byref(weights.c), _ptr(x),
                                       _ptr(y), _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
 
@@ -380,6 +413,8 @@ def moe_experts(shape, weights, x, topk_idx, topk_w, y, ws, ws_bytes=None, strea
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     src = _SRC.get(s.act_dtype, _CODES)
+    if s.w_dtype == MOE_FP8:
+        _fp8_fit(s, weights, dev)
     rc = lib.moe_experts(ctypes.byref(s), ctypes.byref(weights.c), _mat(x, "x", T, H, H, src, dev),
                          _mat(topk_idx, "topk_idx", T, k, k, _I32, dev),
                          _mat(topk_w, "topk_w", T, k, k, _F32, dev), _mat(y, "y", T, H, H, src, dev),

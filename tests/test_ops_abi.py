@@ -204,3 +204,62 @@ def test_matmul_refuses_a_y_that_overlaps_the_offsets(y):
     """Workgroups read the offsets while others store y."""
     fails(call_matmul(G=3, off=ptr(6), y=y), moe.MOE_EINVAL, "overlaps")
     assert call_matmul(G=3, off=ptr(6), y=ptr(6) + 16, M=0) == moe.MOE_OK
+
+
+class OnGpu:
+    """A CPU tensor that says it is on device 0, for the checks before a call."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda = t, True
+
+    def get_device(self):
+        return 0
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def fp8_parts(E=4, H=256, I=128, **kw):
+    import torch
+    f8 = torch.float8_e4m3fn
+    d = dict(w_gate=torch.zeros(E, I, H, dtype=f8), w_up=torch.zeros(E, I, H, dtype=torch.uint8),
+             w_down=torch.zeros(E, H, I, dtype=f8))
+    for n, r, c in (("s_gate", I, H), ("s_up", I, H), ("s_down", H, I)):
+        d[n] = torch.zeros(E, r // 128, c // 128)
+    d.update(kw)
+    return {n: t if t is None or isinstance(t, int) else OnGpu(t) for n, t in d.items()}
+
+
+def test_binding_refuses_fp8_weights_that_the_shape_does_not_fit():
+    """A matrix of fewer codes (packed 4-bit ones, say) or scales of one byte would be read out of range."""
+    import torch
+    u8, bf = torch.uint8, torch.bfloat16
+    sh = moe.make_shape(2, 256, 4, 2, 128, w="fp8")
+    fit = lambda **kw: moe._fp8_fit(sh, moe.make_weights(None, **fp8_parts(**kw)), 0)  # noqa: E731
+    fit()
+    fit(w_gate=torch.zeros(5, 128, 256, dtype=u8))   # a bank of more experts
+    fit(s_up=None), fit(w_up=ptr(3))                 # NULL is the library's to refuse, a pointer the caller's to know
+    for bad, word in [(dict(w_gate=torch.zeros(4, 128, 128, dtype=u8)), "w_gate"),
+                      (dict(w_down=torch.zeros(3, 256, 128, dtype=u8)), "w_down"),
+                      (dict(w_up=torch.zeros(4, 128, 256, dtype=bf)), "w_up"),
+                      (dict(s_gate=torch.zeros(4, 1, 2, dtype=u8)), "s_gate"),
+                      (dict(s_up=torch.zeros(4, 128, 8, dtype=u8)), "s_up"),
+                      (dict(s_down=torch.zeros(4, 1, 1)), "s_down")]:
+        with pytest.raises(ValueError, match=word):
+            fit(**bad)
+    with pytest.raises(ValueError, match="GPU"):
+        moe._fp8_fit(sh, moe.make_weights(None, **{n: getattr(t, "t", t) for n, t in fp8_parts().items()}), 0)
+    with pytest.raises(ValueError, match="cuda:0"):
+        moe._fp8_fit(sh, moe.make_weights(None, **fp8_parts()), 1)
+
+
+@pytest.mark.parametrize("call", ["moe_experts", "moe_forward", "moe_forward_noalloc"])
+def test_calls_check_their_fp8_weights(call):
+    import torch
+    parts = {n: getattr(t, "t", t) for n, t in fp8_parts().items()}
+    w = moe.make_weights(ptr(1), **parts)
+    sh = moe.make_shape(2, 256, 4, 2, 128, w="fp8")
+    args = {"moe_experts": (None, None, None, None, None), "moe_forward": (None, None, None, None, None),
+            "moe_forward_noalloc": (None, None, None, None)}[call]
+    with pytest.raises(ValueError, match="GPU"):
+        getattr(moe, call)(sh, w, *args, stream=0)
