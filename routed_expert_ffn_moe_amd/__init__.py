@@ -373,7 +373,7 @@ def _mat_checked(t, what, rows, cols, ld, types, dev):
         held = t.stride(0) * (t.shape[0] - 1) + t.shape[1]
     else:
         ok = t.is_contiguous() or (t.dim() == 2 and t.stride(1) == 1)
-        held = t.numel()
+        held = t.numel() if t.is_contiguous() else t.shape[1] if t.dim() == 2 else 0
     if not ok:
         raise ValueError("%s: strides %s, the call takes rows of %d elements, %d apart"
                          % (what, tuple(t.stride()), cols, ld))

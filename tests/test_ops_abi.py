@@ -263,3 +263,23 @@ def test_calls_check_their_fp8_weights(call):
             "moe_forward_noalloc": (None, None, None, None)}[call]
     with pytest.raises(ValueError, match="GPU"):
         getattr(moe, call)(sh, w, *args, stream=0)
+
+
+def test_binding_refuses_single_rows_that_are_not_whole():
+    """A row of `cols` elements lies in one row of a 2-D tensor that is not dense:
+    the elements of its other rows (which may be the same ones) do not count."""
+    import torch
+    f32 = (torch.float32,)
+
+    def mat(t, cols, rows=1):
+        return moe._mat(OnGpu(t), "t", rows, cols, cols, f32, 0)
+
+    buf = torch.zeros(4, 128)
+    for good in (buf[:, :64], buf[1:2], buf, torch.zeros(64), torch.zeros(1, 64).expand(3, 64)):
+        assert mat(good, 64) == good.data_ptr()
+    for bad in (torch.zeros(1, 64).expand(2, 64), torch.zeros(80).as_strided((4, 40), (8, 1)), buf[:2, :64]):
+        with pytest.raises(ValueError, match="holds"):
+            mat(bad, 128)
+    assert mat(buf, 128, rows=4) == buf.data_ptr()
+    with pytest.raises(ValueError, match="holds|strides"):
+        mat(buf[:, :64], 128, rows=2)
