@@ -405,20 +405,37 @@ def moe_select(select, logits, bias, topk_idx, topk_w, stream=None) -> None:
         _check(rc)
 
 
+def _workspace(ws, ws_bytes, dev):
+    """(device pointer, bytes) of a workspace tensor; a caller's own pointer comes with its ws_bytes."""
+    if ws is None or isinstance(ws, int):
+        if ws and ws_bytes is None:
+            raise ValueError("ws is a pointer: ws_bytes says how much lies behind it")
+        return ws, ws_bytes or 0
+    if not ws.is_cuda:
+        raise ValueError("ws is not on a GPU")
+    if ws.get_device() != dev:
+        raise ValueError("ws is on cuda:%d, the current device is cuda:%d" % (ws.get_device(), dev))
+    held = ws.numel() * ws.element_size()
+    if ws_bytes is None:
+        ws_bytes = held
+    elif ws_bytes > held:
+        raise ValueError("ws holds %d bytes, ws_bytes is %d" % (held, ws_bytes))
+    return _ptr(ws), ws_bytes
+
+
 def moe_experts(shape, weights, x, topk_idx, topk_w, y, ws, ws_bytes=None, stream=None) -> None:
     """y[T, H] of the routed experts with given routing (see include/moe.h)."""
     lib, dev, st = _begin(stream)
     s = shape
     T, H, k = s.T, s.H, s.top_k
-    if ws_bytes is None:
-        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    ws, ws_bytes = _workspace(ws, ws_bytes, dev)
     src = _SRC.get(s.act_dtype, _CODES)
     if s.w_dtype == MOE_FP8:
         _fp8_fit(s, weights, dev)
     rc = lib.moe_experts(ctypes.byref(s), ctypes.byref(weights.c), _mat(x, "x", T, H, H, src, dev),
                          _mat(topk_idx, "topk_idx", T, k, k, _I32, dev),
                          _mat(topk_w, "topk_w", T, k, k, _F32, dev), _mat(y, "y", T, H, H, src, dev),
-                         _ptr(ws), ws_bytes, st)
+                         ws, ws_bytes, st)
     if rc:
         _check(rc)
 

@@ -283,3 +283,25 @@ def test_binding_refuses_single_rows_that_are_not_whole():
     assert mat(buf, 128, rows=4) == buf.data_ptr()
     with pytest.raises(ValueError, match="holds|strides"):
         mat(buf[:, :64], 128, rows=2)
+
+
+def test_experts_check_their_workspace_tensor():
+    import torch
+    sh = moe.make_shape(2, 256, 4, 2, 128, w="fp8")
+    n = moe.moe_workspace_bytes(sh)
+    ws = torch.zeros(n, dtype=torch.uint8)
+    assert moe._workspace(OnGpu(ws), None, 0) == (ws.data_ptr(), n)
+    assert moe._workspace(OnGpu(ws.view(torch.int16)), n - 256, 0) == (ws.data_ptr(), n - 256)
+    assert moe._workspace(None, None, 0) == (None, 0)
+    assert moe._workspace(ptr(1), n, 0) == (ptr(1), n)  # the caller's own pointer
+    with pytest.raises(ValueError, match="GPU"):
+        moe._workspace(ws, None, 0)
+    with pytest.raises(ValueError, match="cuda:0"):
+        moe._workspace(OnGpu(ws), None, 1)
+    with pytest.raises(ValueError, match="holds"):
+        moe._workspace(OnGpu(ws), n + 1, 0)
+    with pytest.raises(ValueError, match="ws_bytes"):
+        moe._workspace(ptr(1), None, 0)
+    with pytest.raises(ValueError, match="GPU"):  # the call itself
+        moe.moe_experts(sh, moe.make_weights(None, *(ptr(i) for i in (1, 2, 3)), s_gate=ptr(4), s_up=ptr(5),
+                                             s_down=ptr(6)), None, None, None, None, ws, stream=0)
