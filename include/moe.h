@@ -194,7 +194,8 @@ int moe_route(const moe_shape_t *shape, const moe_weights_t *w,
 /* The router's logits alone: logits[T, E] (fp32) = x . router_w^T
  * (+ router_bias).  Only the shape's T, H, E, top_k and act_dtype and the
  * weights' router_w and router_bias are used (the shape must be valid as a
- * whole).  x and logits 16-byte aligned. */
+ * whole).  Any T: the limits of a pass do not hold here.  x and logits 16-byte
+ * aligned. */
 int moe_logits(const moe_shape_t *shape, const moe_weights_t *w, const void *x, float *logits,
                void *stream);
 

@@ -802,27 +802,35 @@ int moe_logits(const moe_shape_t *s, const moe_weights_t *w, const void *x, floa
         return fail(MOE_EINVAL, "x or logits is NULL");
     if (!aligned16(x) || !aligned16(logits))
         return fail(MOE_EINVAL, "x or logits not 16-byte aligned");
-    if ((rc = check_pass_size(s, s->T)))
-        return rc;
+    // the router kernels' 32-bit offsets: check_pass_size's limits on x and the logits
+    const int64_t fit = (((int64_t)1 << 31) - 1) / std::max<int64_t>(s->H, (int64_t)s->E * 8);
+    if (fit < 1)
+        return fail(MOE_EINVAL, "a token's row reaches 2^31 elements");
+    const int64_t Tc = fit < 256 ? fit : fit / 256 * 256;
     if ((rc = check_device()))
         return rc;
     moe::RouterArgs r{};
-    r.x = x;
     r.wr = w->router_w;
     r.bias = w->router_bias;
-    r.logits = logits;
-    r.T = s->T;
     r.H = s->H;
     r.E = s->E;
     r.k = s->top_k;
     r.act = s->act_dtype == MOE_BF16 ? moe::ACT_BF16 : moe::ACT_F32;
     r.nparts = 1;
     hipStream_t st = (hipStream_t)stream;
-    if (moe::route_small_ok(s->T, s->top_k, s->E, s->H, r.act))
-        moe::launch_router_small(r, st);
-    else
-        moe::launch_router_logits(r, st);
-    return launched("logits");
+    const int64_t esz = s->act_dtype == MOE_F32 ? 4 : 2;
+    for (int64_t c0 = 0; c0 < s->T; c0 += Tc) {
+        r.T = (int)std::min(Tc, s->T - c0);
+        r.x = (const char *)x + c0 * s->H * esz;
+        r.logits = logits + c0 * s->E;
+        if (moe::route_small_ok(r.T, s->top_k, s->E, s->H, r.act))
+            moe::launch_router_small(r, st);
+        else
+            moe::launch_router_logits(r, st);
+        if ((rc = launched("logits")))
+            return rc;
+    }
+    return MOE_OK;
 }
 
 int moe_experts(const moe_shape_t *s, const moe_weights_t *w, const void *x,

@@ -1,0 +1,59 @@
+"""moe_logits of any number of tokens."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU visible", allow_module_level=True)
+
+import ops_ref as ref  # noqa: E402
+import routed_expert_ffn_moe_amd as moe  # noqa: E402
+from test_ops_gpu import gen, randn, within  # noqa: E402
+
+
+def logits(x, r, b, chunk=0, act="bf16"):
+    T, H = x.shape
+    E = r.shape[0]
+    out = torch.full((T + 1, E), -7.0, device="cuda")
+    moe.moe_logits(moe.make_shape(T, H, E, 1, 64, chunk_T=chunk, act=act, w=act),
+                   moe.make_weights(r, None, None, None, router_bias=b), x, out)
+    torch.cuda.synchronize()
+    assert (out[T] == -7).all()
+    return out[:T]
+
+
+def close(got, x, r, b):
+    xd, rd = x.cpu().double(), r.cpu().double()
+    # H products and additions and the bias's, each within 2^-24 (2^-23 where it may truncate)
+    mag = xd.abs() @ rd.abs().t() + b.cpu().double().abs()
+    within(got, xd @ rd.t() + b.cpu().double(), 2 * (x.shape[1] + 2) * ref.U32 * mag, "logits")
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E", [(1, 512, 8), (37, 512, 64), (200, 512, 64), (300, 2048, 128), (130, 320, 7)])
+def test_logits(T, H, E, act):
+    g = gen(T + H)
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    x, r = randn(g, T, H, dtype=dt).cuda(), randn(g, E, H, dtype=dt).cuda()
+    b = randn(g, E).cuda()
+    out = logits(x, r, b, act=act)
+    close(out, x, r, b)
+    assert torch.equal(out, logits(x, r, b, chunk=17, act=act))  # chunk_T plays no part
+
+
+@pytest.mark.parametrize("E", [1008, 1021])
+def test_logits_past_32_bit_offsets(E):
+    """More than 2^31 / 8 logits, which take two passes."""
+    T, H = (1 << 31) // (8 * E) + 700, 64
+    g = gen(E)
+    x, r = randn(g, T, H, dtype=torch.bfloat16).cuda(), randn(g, E, H, dtype=torch.bfloat16).cuda()
+    b = randn(g, E).cuda()
+    out = logits(x, r, b)
+    cut = (((1 << 31) - 1) // (8 * E)) // 256 * 256
+    for lo in (0, cut - 40, cut, T - 40):
+        close(out[lo:lo + 40], x[lo:lo + 40], r, b)
+    want = x.float() @ r.float().t() + b  # every row, in fp32: twice the bound of close()
+    mag = x.float().abs() @ r.float().abs().t() + b.abs()
+    assert bool(((out - want).abs() <= 4 * (H + 2) * ref.U32 * mag).all())

@@ -305,3 +305,17 @@ def test_experts_check_their_workspace_tensor():
     with pytest.raises(ValueError, match="GPU"):  # the call itself
         moe.moe_experts(sh, moe.make_weights(None, *(ptr(i) for i in (1, 2, 3)), s_gate=ptr(4), s_up=ptr(5),
                                              s_down=ptr(6)), None, None, None, None, ws, stream=0)
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"),
+                    reason="a GPU driver is present: a valid call would launch on made-up addresses")
+@pytest.mark.parametrize("kw", [
+    dict(T=1 << 20, H=4096, E=256, chunk_T=8192),           # as long as moe_forward's, in its passes
+    dict(T=1 << 20, H=4096, E=256),
+    dict(T=200000, H=4096, E=128, top_k=8, I=2048),         # rows of the experts do not count
+    dict(T=1000, H=512, E=8, top_k=8, I=512 * 1024, w="bf16"),
+])
+def test_logits_take_any_number_of_tokens(kw):
+    sh = shape(**kw)
+    rc = moe.load().moe_logits(ctypes.byref(sh), ctypes.byref(weights(router_w=ptr(12))), ptr(7), ptr(8), None)
+    fails(rc, moe.MOE_EHIP, "hipGetDevice")  # past every check
