@@ -365,11 +365,12 @@ void launch_fp8_decode(const Fp8Decode &p, hipStream_t st)
     // Eight waves where the slots allow it, which start sooner and share a CU with
     // another group's: where their 32 units in flight are all there are (T=1,
     // H=1536, I=512, k=8 11.7 us for both products, 13.7 with sixteen waves) or the
-    // groups are more than the CUs take at once (T=8, H=2048, I=768, k=8 55 and
-    // 88).  Else sixteen (T=1, H=2048, I=768, k=8 16.5 us, 17.5 with eight).
+    // groups are more than the 256 CUs take at once (H=2048, I=768, k=8: T=3 28.8 us
+    // and 30.7, T=4 33.0 and 35.2).  Else sixteen (the same, T=1 16.2 us, 17.0 with
+    // eight, T=2, 256 groups, 19.6 and 20.9; T=1, H=4096 22.5 and 23.7).
     const unsigned grid = (unsigned)(p.T * (p.H / DN));
     const size_t lds = (size_t)units * (DN + 1) * 4;
-    if (p.k <= 8 && (units <= 32 || grid > 128))
+    if (p.k <= 8 && (units <= 32 || grid > 256))
         fp8_token_down<8><<<grid, 64 * 8, lds, st>>>(p);
     else
         fp8_token_down<16><<<grid, 64 * 16, lds, st>>>(p);

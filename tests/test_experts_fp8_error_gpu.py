@@ -125,6 +125,20 @@ def test_error_of_single_tokens(H, I, k):
     assert torch.equal(one, eight) and torch.equal(one, L.run(xd, id_, wd))
 
 
+@pytest.mark.parametrize("T,H,I,k", [(1, 2048, 512, 8), (1, 4096, 768, 8), (2, 2048, 768, 8), (3, 2048, 768, 8),
+                                     (2, 2048, 2048, 4), (1, 2304, 640, 9)])
+def test_error_of_decode_rows_by_either_number_of_waves(T, H, I, k):
+    """Down projections of up to 32 units of work, of as many workgroups as CUs, and of more of both."""
+    E = 12
+    g = gen(T + H + I)
+    L = Experts(E, H, I, T)
+    x = randn(g, 20, H, dtype=torch.bfloat16).cuda()
+    idx, w = (t.cuda() for t in routing(g, 20, E, k))
+    y = L.run(x[:T], idx[:T], w[:T])
+    check(L.dev, E, x[:T], idx[:T], w[:T], y, "T%d H%d I%d k%d" % (T, H, I, k))
+    assert torch.equal(y, L.run(x, idx, w)[:T])
+
+
 class Wide(Experts):
     """Many large experts, made on the GPU."""
 
