@@ -471,15 +471,26 @@ __global__ __launch_bounds__(64 * SEL_WAVES) void select_kernel(SelectArgs a)
     }
 }
 
+// Tokens of a launch: 2^30 threads.  A grid of 2^32 threads and more is launched
+// short, without an error.
+constexpr int LAUNCH_TOKENS = 1 << 24;
+
 template <int PER>
-void launch_per(const SelectArgs &a, hipStream_t st)
+void launch_per(const SelectArgs &all, hipStream_t st)
 {
-    const unsigned nb = (unsigned)((a.T + SEL_WAVES - 1) / SEL_WAVES);
-    const size_t lds = (size_t)SEL_WAVES * std::max(a.E, 32) * sizeof(double);
-    if (a.bf16)
-        select_kernel<PER, true><<<nb, 64 * SEL_WAVES, lds, st>>>(a);
-    else
-        select_kernel<PER, false><<<nb, 64 * SEL_WAVES, lds, st>>>(a);
+    const size_t lds = (size_t)SEL_WAVES * std::max(all.E, 32) * sizeof(double);
+    for (int64_t t0 = 0; t0 < all.T; t0 += LAUNCH_TOKENS) {
+        SelectArgs a = all;
+        a.T = (int)std::min<int64_t>(all.T - t0, LAUNCH_TOKENS);
+        a.logits = (const char *)all.logits + t0 * all.ld * (all.bf16 ? 2 : 4);
+        a.idx = all.idx + t0 * all.k;
+        a.w = all.w ? all.w + t0 * all.k : nullptr;
+        const unsigned nb = (unsigned)((a.T + SEL_WAVES - 1) / SEL_WAVES);
+        if (a.bf16)
+            select_kernel<PER, true><<<nb, 64 * SEL_WAVES, lds, st>>>(a);
+        else
+            select_kernel<PER, false><<<nb, 64 * SEL_WAVES, lds, st>>>(a);
+    }
 }
 
 }  // namespace

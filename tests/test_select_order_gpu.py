@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
+import routed_expert_ffn_moe_amd as moe  # noqa: E402
 from test_ops_gpu import check_select, gen, run_select  # noqa: E402
 
 BF = torch.bfloat16
@@ -88,3 +89,17 @@ def test_renormalised_weights_of_small_scores_sum_to_the_scale():
     idx, w = run_select((-95 - torch.arange(32.0)).view(1, 32).cuda(), None, 4, score="sigmoid", scale=2.5)
     assert idx.tolist() == [[0, 1, 2, 3]]
     assert abs(float(w.double().sum()) - 2.5) < 4 * 2.5 * 2.0 ** -24
+
+
+def test_more_tokens_than_one_launch_takes():
+    """70 million tokens: a wave each are more threads than a launch may have."""
+    T = 70 * 10 ** 6
+    l = torch.randint(-5, 6, (T, 2), dtype=torch.int8, device="cuda").to(BF)
+    idx = torch.full((T + 1, 1), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, 1), -7.0, device="cuda")
+    moe.moe_select(moe.make_select(T, 2, 1, logits="bf16", renorm=False, score="sigmoid"), l, None, idx, w)
+    torch.cuda.synchronize()
+    assert int(idx[T]) == -7 and float(w[T]) == -7
+    assert torch.equal(idx[:T, 0], (l[:, 1] > l[:, 0]).to(torch.int32))
+    want = torch.sigmoid(l.amax(1).float())  # 11 different values
+    assert float((w[:T, 0] - want).abs().max()) <= 2.0 ** -19
