@@ -268,7 +268,8 @@ typedef struct {
 /* codes [R, Kp] bytes, Kp = K rounded up to a multiple of 128, the columns
  * behind K zero; scales [R, Kp / 128] (block_rows 1) or [R / 128 rounded up,
  * Kp / 128] (128).  x and scales element aligned, codes 16-byte aligned; the
- * outputs overlap neither x nor each other.  A stack of matrices [E, N, K]
+ * outputs overlap neither x nor each other.  Fewer than 2^31 blocks, 2^24 of
+ * 128 rows.  A stack of matrices [E, N, K]
  * with N a multiple of 128 is one call with R = E * N. */
 int moe_quant_fp8(const moe_quant_t *quant, const void *x, void *codes, float *scales,
                   void *stream);

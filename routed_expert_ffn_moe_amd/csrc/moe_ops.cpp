@@ -93,8 +93,10 @@ int moe_quant_fp8(const moe_quant_t *s, const void *x, void *codes, float *scale
     if (s->ld != 0 && s->ld < s->K)
         return bad("moe_quant_fp8: ld must be 0 or at least K");
     const int64_t KB = cdiv(s->K, moe::FP8_K);
-    if (cdiv(s->R, s->block_rows) * KB >= (int64_t)1 << 31)
-        return bad("moe_quant_fp8: more than 2^31 blocks");
+    // blocks of 128 x 128: a workgroup of 256 threads each, below 2^32 threads
+    const int64_t blocks = cdiv(s->R, s->block_rows) * KB;
+    if (blocks >= (int64_t)1 << (s->block_rows == 1 ? 31 : 24))
+        return bad("moe_quant_fp8: 2^31 blocks of 1 x 128, or 2^24 of 128 x 128, or more");
     if (s->R == 0)
         return MOE_OK;
     if (!x || !codes || !scales)

@@ -319,3 +319,9 @@ def test_logits_take_any_number_of_tokens(kw):
     sh = shape(**kw)
     rc = moe.load().moe_logits(ctypes.byref(sh), ctypes.byref(weights(router_w=ptr(12))), ptr(7), ptr(8), None)
     fails(rc, moe.MOE_EHIP, "hipGetDevice")  # past every check
+
+
+@pytest.mark.parametrize("bad", [dict(R=(1 << 31) - 1, K=1), dict(R=1 << 24, K=1 << 14), dict(R=(1 << 31) - 100, K=128)])
+def test_quant_refuses_more_blocks_than_a_launch_has_threads_for(bad):
+    """256 threads a block of 128 x 128; a grid of 2^32 threads would be launched short."""
+    fails(call_quant(x=ptr(1), codes=ptr(200), scales=ptr(400), block_rows=128, **bad), moe.MOE_EINVAL, "blocks")
