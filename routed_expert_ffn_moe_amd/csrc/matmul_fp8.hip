@@ -19,15 +19,20 @@
 // bytes are whole cache lines, so the weights need no packing; the pattern
 // alone streams 6.1 TB/s), ST stages of 128 K deep.  In LDS the 16-byte pieces
 // of a row are rotated (XOR) by the row, so that the 16 rows a fragment read
-// touches fall on distinct banks (no conflicts counted), and the weight rows
-// lie in the order in which a lane's results come out adjacent.  The rows'
+// touches fall on distinct banks (tiles of 144 rows count no conflicts, those of 96
+// rows cycles that are 1% of the time of a CU), and the weight rows lie in the order
+// in which a lane's results come out adjacent.  The rows'
 // scales are copied a few blocks of K at a time: one 4-byte copy per row and
 // block fetched as many cache lines as the weights themselves.
 //
 // Bound by memory where groups have few rows: 16 rows a group read their weights
 // at 5.7 TB/s, 64 rows at K=2048 at 4.9, 128 rows (384 experts of H=4096, I=2048,
-// gate+up 1550 us) at 4.2, where the copies alone take 85% of the time and 31% of
-// the cycles have an MFMA running.  Bound by the MFMAs and the FMAs beside them
+// down 825 us) at 4.2, where the copies alone take 85% of the time.  Gate+up of those
+// experts, whose products are bf16's, takes 1.8 to 2.0 ms (2.2 in single calls) and
+// is bound by its instructions: MFMAs run in 47% of the cycles and other vector
+// instructions, half of them the codes' conversion (once a stage for the weights,
+// once a row block for the rows), in 44%, at a clock that this load brings down to
+// 1.7 GHz.  Bound by the MFMAs and the FMAs beside them
 // for one matrix of many rows: 8192 x 4096 x 4096 in 140 us, 2.0 PFLOP/s (the two
 // alone reach 2.5 in registers; 44% and 27% of the cycles).
 #include <algorithm>
@@ -124,8 +129,7 @@ struct Cfg {
     // (into the buffer that the step before has left); with two that would leave
     // them too little time, and with four the tiles are small and wait for memory
     // anyway: there all copies of a stage are made when its buffer falls free.
-    // (T=8192 over 384 experts: gate+up 1550 us spread, 1620 at once, down 825 and
-    // 860.)
+    // (T=8192 over 384 experts: down 825 us spread, 860 at once.)
     static constexpr bool SPREAD = ST == 3 && NW == 8;
     static constexpr int LEAD = SPREAD ? ST - 1 : ST;
     // The next tile's row numbers (EPI_SWIGLU) are copied behind the first LEAD
@@ -567,7 +571,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         }
     } else {
         // h = silu(gate) * up, its block maximum over the tile's 128 columns
-        // (4 lanes of a wave, then the waves), and its codes
+        // (4 lanes of a wave, then the waves), and its codes.  (silu's hardware
+        // reciprocal is 1 ulp off, less than the sums are, and moves a code as rarely.)
         constexpr int HB = NBW / 2;
         float *s_max = (float *)(smem + C::O_SIDE);  // [WN][BM] (the next rows have been read)
 #pragma unroll
@@ -655,13 +660,15 @@ void launch_cfg(const Fp8Args &p, hipStream_t st)
 // Groups whose balanced rows (1.4 standard deviations above the mean) fit into a
 // tile have one; larger ones leave half a tile empty.  So groups are covered by
 // one tile where that is possible, which then streams their weights once (T=8192
-// over 384 experts, 128 rows each: gate+up 1550 us with tiles of 144 rows, 1860
-// with 128), long matrices take the largest tiles (8192 x 4096 x 4096: 144 us with
+// over 384 experts, 128 rows each: a whole call 2850 us with gate+up tiles of 144
+// rows, 3280 with 128), long matrices take the largest tiles (8192 x 4096 x 4096: 144 us with
 // 256 rows, 163 with 128) and short ones tiles that give every CU one (8 groups of
 // 347 rows, N=1664, K=2048: 18 us with 96 rows, 33 with 256; 4 groups of 217 rows,
-// N=1024, K=640: 7.3 us with 64 x 64, 14.7 with 256 rows).  The largest tiles' fp32
-// output would need more registers than there are (71 us against 33 in the first
-// of these), so it goes without them.
+// N=1024, K=640: 7.3 us with 64 x 64, 14.7 with 256 rows).  Products by bf16
+// (`exact`) would need more registers than there are in the largest tiles (71 us
+// against 33 in the first of these), so they go without them.  Their steps cost more
+// than the ones these times are of, alike for all sizes: over eight expert passes of
+// 32 to 2048 rows an expert, gate+up by any one size was at best 4% faster.
 Fp8Tile fp8_size(int64_t rows, int groups, int64_t N, bool swiglu, bool exact, bool narrow)
 {
     const double per = (double)rows / groups;

@@ -8,11 +8,13 @@
 //                   16.8 MB take 2.8 and a launch with one wait for memory 3.
 //  fp8_pair_gate_up decode rows of the experts (T <= 8): one workgroup per
 //                   (token, slot) pair and 16 columns of h, no permutation;
-//                   the pair's x is quantised on the way.
+//                   the pair's x is quantised on the way.  The codes are
+//                   multiplied as bf16, as in the tiles (fp8.h).
 //  fp8_token_down   their down projections and the combine: one workgroup per
 //                   token and 16 columns of y, h quantised on the way.
-// T=1, H=2048, k=8, I=768: 8.7 + 11.0 us (38 MB take 6.2): each is a chain of
-// indices, weights, MFMA, LDS and the sums of the blocks in their order.
+// T=1, H=2048, k=8, I=768: 8.3 + 9.6 us, 16.2 a call in a run of them (38 MB take
+// 6.2): each is a chain of indices, weights, MFMA, LDS and the sums of the blocks in
+// their order.
 //
 // The decode kernels pass the sums of single blocks of K through LDS and join
 // them in K order with the same FMAs as the tile kernel, and round each

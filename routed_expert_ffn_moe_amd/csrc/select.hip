@@ -15,8 +15,10 @@
 // the bound of the fp32 keys' errors; where one is too small (1 token in 1000
 // with sigmoid and a bias, 1 in 100 with softmax and a bias, none without a
 // bias unless the scores saturate) the experts in question are ordered in 64
-// bits, or, where those are many or the doubt is between groups, the token is
-// routed again in 64 bits.
+// bits, or, where those are many, the doubt is between groups or the selected
+// scores are too small for fp32, the token is routed again in 64 bits.  The
+// weights of the others are computed in fp32: 6e-8 off, the size of their own
+// rounding to fp32 (3e-8).
 //
 // An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is
 // masked: it ranks behind every other one (among masked ones by index) and
@@ -26,9 +28,9 @@
 //
 // One wave per token.  Bound by its instructions, of which the k + 1 selection
 // rounds, a wave maximum each, are the most: T=8192, E=384, k=6, sigmoid and bias
-// 12.5 us for 686 vector instructions a token (9 us of issue on 1024 SIMDs; its
-// bytes take 2), all in 64 bits 25 us.  T=2048, E=256, k=8, softmax 6.0 us, T=1
-// with 4 of 8 groups 5.7.
+// 12.9 us for 694 vector instructions a token (9 us of issue on 1024 SIMDs; its
+// bytes take 2), all in 64 bits 25 us.  T=2048, E=256, k=8, softmax over bf16 logits,
+// which often tie on the last place, 6.8 us, T=1 with 4 of 8 groups 6.0.
 #include <algorithm>
 
 #include "common.h"
