@@ -112,8 +112,8 @@ __device__ __forceinline__ float row16_max(float v)
 // too much for an fp32 result and for gate and up: h is rounded to 3 bits of
 // mantissa, so that an error of its sums moves every code whose quotient is as
 // near to a midpoint by a step, 6 to 12% of the value (T=1, H=2048, k=8, I=768: 14
-// of 6144 codes, y off by 0.005 of its size in 3% of the tokens and by 0.0096 at most,
-// with exact sums 0.05 codes and 0.0018).  So results and staging rows that are
+// of 6144 codes, y off by more than 0.005 of its size in 4% of the tokens and by 0.010
+// at most of 256 tokens, with exact sums by 0.0018).  So results and staging rows that are
 // rounded to bf16 or half precision take the FP8 instruction, fp32 results and
 // the sums of gate and up the bf16 one on the same codes: every product is exact
 // there and the sum is fp32's, at half the instruction's rate.
