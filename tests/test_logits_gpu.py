@@ -57,3 +57,15 @@ def test_logits_past_32_bit_offsets(E):
     want = x.float() @ r.float().t() + b  # every row, in fp32: twice the bound of close()
     mag = x.float().abs() @ r.float().abs().t() + b.abs()
     assert bool(((out - want).abs() <= 4 * (H + 2) * ref.U32 * mag).all())
+
+
+def test_logits_of_more_token_blocks_than_a_grid_row_has():
+    """E=7, 32 tokens a block: more than 65536 blocks."""
+    T, H, E = 65536 * 32 + 900 * 32 + 5, 64, 7
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    r, b = randn(gen(3), E, H, dtype=torch.bfloat16).cuda(), randn(gen(4), E).cuda()
+    out = logits(x, r, b)
+    want = x.float() @ r.float().t() + b
+    mag = x.float().abs() @ r.float().abs().t() + b.abs()
+    assert bool(((out - want).abs() <= 4 * (H + 2) * ref.U32 * mag).all())
