@@ -296,6 +296,144 @@ typedef struct {
 int moe_matmul_fp8(const moe_matmul_t *matmul, const void *a, const float *sa, const void *b,
                    const float *sb, const int32_t *offsets, void *y, void *stream);
 
+/* ---- Rows by expert, and gradients ------------------------------------------
+ * For callers whose step through the experts is their own (training, adapters,
+ * other activations), and for the backward pass of the routed layer.  Forward:
+ *   moe_logits -> moe_select -> moe_dispatch -> moe_matmul_bf16 (gate, up) ->
+ *   moe_swiglu -> moe_matmul_bf16 (down) -> moe_combine
+ * and backward:
+ *   moe_combine_grad -> moe_matmul_bf16_dx / _dw (down) -> moe_swiglu_grad ->
+ *   moe_matmul_bf16_dx / _dw (gate, up) -> moe_combine without weights (the
+ *   gradient of moe_dispatch) and moe_select_grad
+ * The general rules above hold.  Element types: rows of moe_dispatch, moe_combine
+ * and moe_swiglu are MOE_F32 or MOE_BF16, operands of the products bf16.
+ * Pointers are aligned to their elements, codes to 16 bytes, unless said
+ * otherwise; strides are in elements, at most 2^31; an output overlaps neither an
+ * input nor another output (spans from the first to the last element count). */
+
+/* The pairs (t, j) sorted by expert, stably (t, then j within an expert), and
+ * the tokens' rows in that order:
+ *   offsets [E + 1]     first place of each expert's pairs; offsets[E] pairs in all
+ *   row_src [T * top_k] pair t * top_k + j at each place (nullable; the places from
+ *                       offsets[E] on stay as they were)
+ *   row_of [T, top_k]   place of each pair, -1 for an empty slot (an index outside
+ *                       0..E-1)
+ *   rows [T * top_k, H] rows[row_of[t, j]] = x[t]; the rows from offsets[E] on stay
+ *                       as they were
+ * x holds MOE_F32 or MOE_BF16 values, which are copied bit by bit, or MOE_FP8: codes
+ * and scales of moe_quant_fp8 in 1 x 128 blocks (an 8-bit checkpoint of x), which
+ * are multiplied in fp32 and rounded once to row_dtype. */
+typedef struct {
+    int32_t T, H;        /* tokens and columns                                  */
+    int32_t E, top_k;    /* experts, 1..1024; slots of a token, 1..16           */
+    int32_t x_dtype;     /* MOE_F32, MOE_BF16 or MOE_FP8                        */
+    int32_t row_dtype;   /* x_dtype; MOE_F32 or MOE_BF16 where x is MOE_FP8     */
+    int64_t ldx;         /* row stride of x, 0 = H (codes: H rounded up to 128; a multiple of 16) */
+    int64_t ldr;         /* row stride of rows, 0 = H                           */
+} moe_dispatch_t;
+
+/* Bytes of workspace of moe_dispatch, 0 if the sizes are invalid. */
+size_t moe_dispatch_workspace_bytes(const moe_dispatch_t *dispatch);
+
+/* At most 2^30 pairs.  x and rows NULL: the order alone.  sx: scales of MOE_FP8
+ * [T, H / 128 rounded up], else not used.  ws 256-byte aligned, one for each call
+ * that may run at the same time. */
+int moe_dispatch(const moe_dispatch_t *dispatch, const int32_t *topk_idx, const void *x, const float *sx,
+                 void *rows, int32_t *offsets, int32_t *row_src, int32_t *row_of, void *ws, size_t ws_bytes,
+                 void *stream);
+
+/* The rows alone, by a row_of [T, top_k] that moe_dispatch has made: places outside
+ * 0 .. T * top_k - 1 take no row.  (E is not used.) */
+int moe_gather(const moe_dispatch_t *dispatch, const int32_t *row_of, const void *x, const float *sx, void *rows,
+               void *stream);
+
+/* The way back: y[t] = sum over j of topk_w[t, j] * rows[row_of[t, j]] in j order
+ * (fp32, rounded once); a slot whose row_of is outside 0 .. R - 1 adds nothing,
+ * whatever its weight, and a token of empty slots gets zeros.  topk_w NULL: weights of 1,
+ * which is the gradient of moe_gather. */
+typedef struct {
+    int32_t T, H, top_k; /* tokens, columns, slots of a token (1..16)           */
+    int32_t R;           /* rows there are                                      */
+    int32_t dtype;       /* MOE_F32 or MOE_BF16, of rows and y                  */
+    int64_t ldr, ldy;    /* row strides of rows and y, 0 = H                    */
+} moe_combine_t;
+
+int moe_combine(const moe_combine_t *combine, const void *rows, const int32_t *row_of, const float *topk_w,
+                void *y, void *stream);
+
+/* Its gradient: drows[row_of[t, j]] = topk_w[t, j] * dy[t] and dtopk_w[t, j] = sum
+ * over the columns of dy[t] * rows[row_of[t, j]] (fp32), 0 for an empty slot.  Rows
+ * that no slot names stay as they were; a row may be named once.  drows or dtopk_w may
+ * be NULL (rows then too, without dtopk_w).  drows lies as rows do, dy as y. */
+int moe_combine_grad(const moe_combine_t *combine, const void *dy, const void *rows, const int32_t *row_of,
+                     const float *topk_w, void *drows, float *dtopk_w, void *stream);
+
+/* h = silu(gate) * up of rows [R, I], in fp32 and rounded once, and with codes an
+ * 8-bit checkpoint of gate and up: per row the codes of gate, then those of up, each
+ * Ip = I rounded up to a multiple of 128 wide (codes [R, 2 * Ip]), and their scales
+ * [R, 2 * Ip / 128], by the definition of moe_quant_fp8 in 1 x 128 blocks.  `used`:
+ * a device count of the rows in use (offsets + E of moe_dispatch, say), NULL: all; the
+ * rows behind stay as they were, in every output.  gate and up may be columns of one
+ * matrix (ld 2 * I or more). */
+typedef struct {
+    int32_t R, I;        /* rows and columns                                    */
+    int32_t dtype;       /* MOE_F32 or MOE_BF16                                 */
+    int64_t ld;          /* row stride of gate, up, dgate and dup, 0 = I        */
+    int64_t ldh;         /* row stride of h and dh, 0 = I                       */
+} moe_swiglu_t;
+
+int moe_swiglu(const moe_swiglu_t *swiglu, const void *gate, const void *up, const int32_t *used, void *h,
+               void *codes, float *scales, void *stream);
+
+/* Its gradient, with s = 1 / (1 + exp(-gate)):
+ *   dgate = dh * up * s * (1 + gate * (1 - s)),  dup = dh * gate * s
+ * and, if h is not NULL, h again.  gate and up are read from the checkpoint where
+ * codes and scales are given (gate and up are then not used), each output rounded
+ * once. */
+int moe_swiglu_grad(const moe_swiglu_t *swiglu, const void *gate, const void *up, const void *codes,
+                    const float *scales, const void *dh, const int32_t *used, void *dgate, void *dup, void *h,
+                    void *stream);
+
+/* Gradient of moe_select to the logits: dlogits [T, E] (dense, dlogit_dtype MOE_F32 or
+ * MOE_BF16) of a loss whose gradient to the weights is dtopk_w [T, top_k] and to every
+ * token's score s_e is dscore[e] (NULL: none; a balance loss c * sum_e f_e * mean_t
+ * s_te has dscore[e] = c * f_e / T).  The selection itself, the bias and the groups are
+ * constants: T, E, top_k, score, renorm, logit_dtype, scale and ld of `select` are
+ * used.  topk_idx as moe_select wrote it.  Masked experts (by logit or bias) have
+ * score 0 and pass no gradient from dtopk_w or dscore, nor do experts whose score is
+ * 0 in 64 bits.  An index outside 0..E-1 counts as no slot: it is left out of
+ * the renormalising sum as well (a slot dropped after the selection keeps its index here,
+ * with dtopk_w 0). */
+int moe_select_grad(const moe_select_t *select, const void *logits, const float *bias, const int32_t *topk_idx,
+                    const float *dtopk_w, const float *dscore, void *dlogits, int dlogit_dtype, void *stream);
+
+/* Grouped products of bf16 rows with bf16 matrices w [G, N, K] (row-major), sums in
+ * fp32, rounded once to out_dtype:
+ *   moe_matmul_bf16     y [M, N]     = x w[g]^T   for the rows of each group g
+ *   moe_matmul_bf16_dx  dx [M, K]    = dy w[g]
+ *   moe_matmul_bf16_dw  dw [G, N, K] = dy^T x     over the rows of each group
+ * (+ add, as the output lies and of its type, or NULL; it may be the output itself:
+ * a gradient summed over several calls).  Rows offsets[g] .. offsets[g + 1] - 1
+ * belong to group g; groups may be empty (their dw is 0, or add).  Rows of y and dx
+ * outside offsets[0] .. offsets[G] - 1 stay as they were, those of x and dy are not
+ * used.  offsets is a device array, not decreasing; parts of it outside 0..M are cut
+ * off; with G = 1 NULL takes all rows.  Any sizes, strides and element alignment are
+ * taken; strides that are multiples of 8 elements with pointers aligned to 16 bytes
+ * are fast. */
+typedef struct {
+    int32_t M, N, K;     /* rows; rows and columns of each w                    */
+    int32_t G;           /* matrices w, 1..65535                                */
+    int32_t out_dtype;   /* MOE_F32 or MOE_BF16                                 */
+    int64_t ldx, ldw, ldy; /* row strides of x and dx, w and dw, y and dy, 0: K, K, N */
+} moe_matmul_bf16_t;
+
+int moe_matmul_bf16(const moe_matmul_bf16_t *matmul, const void *x, const void *w, const int32_t *offsets,
+                    const void *add, void *y, void *stream);
+int moe_matmul_bf16_dx(const moe_matmul_bf16_t *matmul, const void *dy, const void *w, const int32_t *offsets,
+                       const void *add, void *dx, void *stream);
+int moe_matmul_bf16_dw(const moe_matmul_bf16_t *matmul, const void *dy, const void *x, const int32_t *offsets,
+                       const void *add, void *dw, void *stream);
+
 /* Repack E MXFP4 matrices of N rows and K columns (N a multiple of 16, K of
  * 128) from the OCP row-major form (codes [E, N, K/2], scales [E, N, K/32])
  * into the layout moe_forward reads (above); E * N * K / 2 code bytes and

@@ -25,6 +25,10 @@ __all__ = [
     "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_GROUP_MAX", "MOE_GROUP_TOP2", "moe_select_t",
     "moe_quant_t", "moe_matmul_t", "make_select", "make_quant", "make_matmul", "moe_logits",
     "moe_select", "moe_experts", "moe_quant_fp8", "quant_fp8", "moe_matmul_fp8",
+    "moe_dispatch_t", "moe_combine_t", "moe_swiglu_t", "moe_matmul_bf16_t", "make_dispatch", "make_combine",
+    "make_swiglu", "make_matmul_bf16", "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_gather",
+    "moe_combine", "moe_combine_grad", "moe_swiglu", "moe_swiglu_grad", "moe_select_grad", "moe_matmul_bf16",
+    "moe_matmul_bf16_dx", "moe_matmul_bf16_dw",
     "lib_path", "load",
 ]
 
@@ -73,6 +77,26 @@ class moe_quant_t(ctypes.Structure):
 class moe_matmul_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "G", "out_dtype")] + \
         [(n, ctypes.c_int64) for n in ("lda", "ldb", "ldy")]
+
+
+class moe_dispatch_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "E", "top_k", "x_dtype", "row_dtype")] + \
+        [(n, ctypes.c_int64) for n in ("ldx", "ldr")]
+
+
+class moe_combine_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "top_k", "R", "dtype")] + \
+        [(n, ctypes.c_int64) for n in ("ldr", "ldy")]
+
+
+class moe_swiglu_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "I", "dtype")] + \
+        [(n, ctypes.c_int64) for n in ("ld", "ldh")]
+
+
+class moe_matmul_bf16_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "G", "out_dtype")] + \
+        [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldy")]
 
 
 _lib = None
@@ -134,6 +158,17 @@ def load() -> ctypes.CDLL:
         lib.moe_quant_fp8.argtypes = [P, P, P, P, P]
         lib.moe_matmul_fp8.restype = ctypes.c_int
         lib.moe_matmul_fp8.argtypes = [P, P, P, P, P, P, P, P]
+        lib.moe_dispatch_workspace_bytes.restype = ctypes.c_size_t
+        lib.moe_dispatch_workspace_bytes.argtypes = [P]
+        lib.moe_dispatch.argtypes = [P] * 9 + [ctypes.c_size_t, P]
+        lib.moe_gather.argtypes = [P] * 6
+        lib.moe_combine.argtypes = [P] * 6
+        lib.moe_combine_grad.argtypes = [P] * 8
+        lib.moe_swiglu.argtypes = [P] * 8
+        lib.moe_swiglu_grad.argtypes = [P] * 11
+        lib.moe_select_grad.argtypes = [P] * 7 + [ctypes.c_int, P]
+        for name in ("moe_matmul_bf16", "moe_matmul_bf16_dx", "moe_matmul_bf16_dw"):
+            getattr(lib, name).argtypes = [P] * 7
         _lib = lib
     return _lib
 
@@ -493,6 +528,199 @@ def moe_matmul_fp8(matmul, a, sa, b, sb, y, offsets=None, stream=None) -> None:
                             _mat(sb, "sb", G * -(-N // 128), kb, kb, _F32, dev),
                             _mat(offsets, "offsets", 1, G + 1, G + 1, _I32, dev),
                             _mat(y, "y", M, N, m.ldy or N, _SRC.get(m.out_dtype, _CODES), dev), st)
+    if rc:
+        _check(rc)
+
+
+def make_dispatch(T, H, E, top_k, x="bf16", rows=None, ldx=0, ldr=0) -> moe_dispatch_t:
+    """rows: their type; by default x's, and bf16 where x is "fp8"."""
+    return moe_dispatch_t(T, H, E, top_k, _DT[x], _DT[rows or ("bf16" if x == "fp8" else x)], ldx, ldr)
+
+
+def make_combine(T, H, top_k, R, dtype="bf16", ldr=0, ldy=0) -> moe_combine_t:
+    return moe_combine_t(T, H, top_k, R, _DT[dtype], ldr, ldy)
+
+
+def make_swiglu(R, I, dtype="bf16", ld=0, ldh=0) -> moe_swiglu_t:
+    return moe_swiglu_t(R, I, _DT[dtype], ld, ldh)
+
+
+def make_matmul_bf16(M, N, K, G=1, out="bf16", ldx=0, ldw=0, ldy=0) -> moe_matmul_bf16_t:
+    return moe_matmul_bf16_t(M, N, K, G, _DT[out], ldx, ldw, ldy)
+
+
+def moe_dispatch_workspace_bytes(dispatch) -> int:
+    return int(load().moe_dispatch_workspace_bytes(ctypes.byref(dispatch)))
+
+
+def _tokens(d, x, sx, rows, dev):
+    """Pointers of x, its scales and the rows in expert order."""
+    T, H, kb = d.T, d.H, -(-d.H // 128)
+    fp8 = d.x_dtype == MOE_FP8
+    width = kb * 128 if fp8 else H
+    return (_mat(x, "x", T, width, d.ldx or width, _CODES if fp8 else _SRC.get(d.x_dtype, _CODES), dev),
+            _mat(sx, "sx", T, kb, kb, _F32, dev) if fp8 else None,
+            _mat(rows, "rows", T * d.top_k, H, d.ldr or H, _SRC.get(d.row_dtype, _CODES), dev))
+
+
+def moe_dispatch(dispatch, topk_idx, x, sx, rows, offsets, row_src, row_of, ws, ws_bytes=None, stream=None) -> None:
+    """The pairs sorted by expert, offsets [E + 1], row_src [T * top_k] and row_of
+    [T, top_k], and the rows [T * top_k, H] of x in that order (see include/moe.h);
+    x and rows None: the order alone."""
+    lib, dev, st = _begin(stream)
+    d = dispatch
+    T, E, k = d.T, d.E, d.top_k
+    ws, ws_bytes = _workspace(ws, ws_bytes, dev)
+    x, sx, rows = _tokens(d, x, sx, rows, dev)
+    rc = lib.moe_dispatch(ctypes.byref(d), _mat(topk_idx, "topk_idx", T, k, k, _I32, dev), x, sx, rows,
+                          _mat(offsets, "offsets", 1, E + 1, E + 1, _I32, dev),
+                          _mat(row_src, "row_src", 1, T * k, T * k, _I32, dev),
+                          _mat(row_of, "row_of", T, k, k, _I32, dev), ws, ws_bytes, st)
+    if rc:
+        _check(rc)
+
+
+def moe_gather(dispatch, row_of, x, sx, rows, stream=None) -> None:
+    """The rows of x by a row_of that moe_dispatch has made."""
+    lib, dev, st = _begin(stream)
+    d = dispatch
+    x, sx, rows = _tokens(d, x, sx, rows, dev)
+    rc = lib.moe_gather(ctypes.byref(d), _mat(row_of, "row_of", d.T, d.top_k, d.top_k, _I32, dev), x, sx, rows, st)
+    if rc:
+        _check(rc)
+
+
+def moe_combine(combine, rows, row_of, topk_w, y, stream=None) -> None:
+    """y[T, H], the weighted sum of each token's rows (topk_w None: weights of 1)."""
+    lib, dev, st = _begin(stream)
+    c = combine
+    T, H, k = c.T, c.H, c.top_k
+    src = _SRC.get(c.dtype, _CODES)
+    rc = lib.moe_combine(ctypes.byref(c), _mat(rows, "rows", c.R, H, c.ldr or H, src, dev),
+                         _mat(row_of, "row_of", T, k, k, _I32, dev), _mat(topk_w, "topk_w", T, k, k, _F32, dev),
+                         _mat(y, "y", T, H, c.ldy or H, src, dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_combine_grad(combine, dy, rows, row_of, topk_w, drows, dtopk_w, stream=None) -> None:
+    """drows [R, H] and dtopk_w [T, top_k] of dy[T, H]; either may be None."""
+    lib, dev, st = _begin(stream)
+    c = combine
+    T, H, k = c.T, c.H, c.top_k
+    src = _SRC.get(c.dtype, _CODES)
+    rc = lib.moe_combine_grad(ctypes.byref(c), _mat(dy, "dy", T, H, c.ldy or H, src, dev),
+                              _mat(rows, "rows", c.R, H, c.ldr or H, src, dev),
+                              _mat(row_of, "row_of", T, k, k, _I32, dev),
+                              _mat(topk_w, "topk_w", T, k, k, _F32, dev),
+                              _mat(drows, "drows", c.R, H, c.ldr or H, src, dev),
+                              _mat(dtopk_w, "dtopk_w", T, k, k, _F32, dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_swiglu(swiglu, gate, up, h, codes=None, scales=None, used=None, stream=None) -> None:
+    """h[R, I] = silu(gate) * up, and with codes [R, 2 * Ip] and scales [R, 2 * Ip / 128]
+    an 8-bit checkpoint of gate and up; used: an int32 tensor with the rows in use."""
+    lib, dev, st = _begin(stream)
+    s = swiglu
+    R, I, kb = s.R, s.I, -(-s.I // 128)
+    src = _SRC.get(s.dtype, _CODES)
+    rc = lib.moe_swiglu(ctypes.byref(s), _mat(gate, "gate", R, I, s.ld or I, src, dev),
+                        _mat(up, "up", R, I, s.ld or I, src, dev), _mat(used, "used", 1, 1, 1, _I32, dev),
+                        _mat(h, "h", R, I, s.ldh or I, src, dev),
+                        _mat(codes, "codes", R, 256 * kb, 256 * kb, _CODES, dev),
+                        _mat(scales, "scales", R, 2 * kb, 2 * kb, _F32, dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_swiglu_grad(swiglu, gate, up, codes, scales, dh, dgate, dup, h=None, used=None, stream=None) -> None:
+    """dgate, dup and (unless None) h again, from gate and up or from their checkpoint."""
+    lib, dev, st = _begin(stream)
+    s = swiglu
+    R, I, kb = s.R, s.I, -(-s.I // 128)
+    src = _SRC.get(s.dtype, _CODES)
+    ld, ldh = s.ld or I, s.ldh or I
+    rc = lib.moe_swiglu_grad(ctypes.byref(s), _mat(gate, "gate", R, I, ld, src, dev), _mat(up, "up", R, I, ld, src, dev),
+                             _mat(codes, "codes", R, 256 * kb, 256 * kb, _CODES, dev),
+                             _mat(scales, "scales", R, 2 * kb, 2 * kb, _F32, dev),
+                             _mat(dh, "dh", R, I, ldh, src, dev), _mat(used, "used", 1, 1, 1, _I32, dev),
+                             _mat(dgate, "dgate", R, I, ld, src, dev), _mat(dup, "dup", R, I, ld, src, dev),
+                             _mat(h, "h", R, I, ldh, src, dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_select_grad(select, logits, topk_idx, dtopk_w, dscore, dlogits, bias=None, stream=None) -> None:
+    """dlogits [T, E] (float32 or bfloat16) of the gradients dtopk_w [T, top_k] to
+    moe_select's weights and dscore [E] (or None) to every token's scores; bias as
+    moe_select had it."""
+    lib, dev, st = _begin(stream)
+    s = select
+    T, E, k = s.T, s.E, s.top_k
+    out = MOE_BF16 if dlogits is not None and dlogits.dtype in _SRC[MOE_BF16] else MOE_F32
+    rc = lib.moe_select_grad(ctypes.byref(s),
+                             _mat(logits, "logits", T, E, s.ld or E, _SRC.get(s.logit_dtype, _F32), dev),
+                             _mat(bias, "bias", 1, E, E, _F32, dev),
+                             _mat(topk_idx, "topk_idx", T, k, k, _I32, dev),
+                             _mat(dtopk_w, "dtopk_w", T, k, k, _F32, dev),
+                             _mat(dscore, "dscore", 1, E, E, _F32, dev),
+                             _mat(dlogits, "dlogits", T, E, E, _SRC[out], dev), out, st)
+    if rc:
+        _check(rc)
+
+
+def _bf16_mats(m, dev):
+    """How the operands of the bf16 products lie: rows of x, matrices w, rows of y."""
+    ldx, ldw, ldy = m.ldx or m.K, m.ldw or m.K, m.ldy or m.N
+
+    def x(t, what, types):
+        return _mat(t, what, m.M, m.K, ldx, types, dev)
+
+    def w(t, what, types):
+        if t is not None and t.dim() == 3 and not t.is_contiguous() and t.stride(0) == t.shape[1] * t.stride(1):
+            t = t.flatten(0, 1)
+        return _mat(t, what, m.G * m.N, m.K, ldw, types, dev)
+
+    def y(t, what, types):
+        return _mat(t, what, m.M, m.N, ldy, types, dev)
+
+    return x, w, y, _SRC[MOE_BF16], _SRC.get(m.out_dtype, _CODES)
+
+
+def moe_matmul_bf16(matmul, x, w, y, offsets=None, add=None, stream=None) -> None:
+    """y[M, N] = x w[g]^T (+ add) for the rows of each group g (see include/moe.h)."""
+    lib, dev, st = _begin(stream)
+    m = matmul
+    px, pw, py, src, out = _bf16_mats(m, dev)
+    rc = lib.moe_matmul_bf16(ctypes.byref(m), px(x, "x", src), pw(w, "w", src),
+                             _mat(offsets, "offsets", 1, m.G + 1, m.G + 1, _I32, dev), py(add, "add", out),
+                             py(y, "y", out), st)
+    if rc:
+        _check(rc)
+
+
+def moe_matmul_bf16_dx(matmul, dy, w, dx, offsets=None, add=None, stream=None) -> None:
+    """dx[M, K] = dy w[g] (+ add)."""
+    lib, dev, st = _begin(stream)
+    m = matmul
+    px, pw, py, src, out = _bf16_mats(m, dev)
+    rc = lib.moe_matmul_bf16_dx(ctypes.byref(m), py(dy, "dy", src), pw(w, "w", src),
+                                _mat(offsets, "offsets", 1, m.G + 1, m.G + 1, _I32, dev), px(add, "add", out),
+                                px(dx, "dx", out), st)
+    if rc:
+        _check(rc)
+
+
+def moe_matmul_bf16_dw(matmul, dy, x, dw, offsets=None, add=None, stream=None) -> None:
+    """dw[G, N, K] = dy^T x over the rows of each group (+ add)."""
+    lib, dev, st = _begin(stream)
+    m = matmul
+    px, pw, py, src, out = _bf16_mats(m, dev)
+    rc = lib.moe_matmul_bf16_dw(ctypes.byref(m), py(dy, "dy", src), px(x, "x", src),
+                                _mat(offsets, "offsets", 1, m.G + 1, m.G + 1, _I32, dev), pw(add, "add", out),
+                                pw(dw, "dw", out), st)
     if rc:
         _check(rc)
 

@@ -20,7 +20,8 @@ ARCH = "gfx950"
 SOURCES = ["probe.hip", "router.hip", "route_small.hip", "permute.hip", "expert_gemm.hip",
            "expert_stream.hip", "mxfp4.hip", "select.hip", "quant_fp8.hip", "matmul_fp8.hip",
            "matmul_fp8_small.hip",
-           "experts_given.hip", "moe_api.cpp", "moe_ops.cpp", "noalloc.hip"]
+           "experts_given.hip", "dispatch.hip", "swiglu.hip", "select_grad.hip", "matmul_bf16.hip",
+           "moe_api.cpp", "moe_ops.cpp", "moe_train.cpp", "noalloc.hip"]
 
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",

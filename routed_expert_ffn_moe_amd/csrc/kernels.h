@@ -240,6 +240,90 @@ struct Fp8Decode {
 bool fp8_decode_ok(int T, int H, int k, int I);
 void launch_fp8_decode(const Fp8Decode &p, hipStream_t st);
 
+// Tokens sorted by expert and back (dispatch.hip).
+struct SortArgs {
+    const int32_t *idx;  // [T, k]; outside 0..E-1: an empty slot
+    int32_t *offsets;    // [E + 1]
+    int32_t *row_src;    // [T * k] or null
+    int32_t *row_of;     // [T, k]
+    int32_t *blk;        // workspace of sort_blk_bytes
+    int T, E, k;
+};
+enum { GATHER_F32 = 0, GATHER_BF16 = 1, GATHER_FP8 = 2 };
+struct GatherArgs {
+    const void *x;    // [T, H] f32 / bf16, or codes with scales sx [T, H / 128 rounded up]
+    const float *sx;
+    void *rows;       // [R, H]: x's type; of codes fp32 (out_f32) or bf16
+    const int32_t *row_of;
+    int64_t ldx, ldr;
+    int T, H, k, R, src, out_f32;
+};
+size_t sort_blk_bytes(int T, int E, int k);
+void launch_dispatch(const SortArgs &s, const GatherArgs &a, hipStream_t st);  // a.x null: the order alone
+void launch_gather(const GatherArgs &a, hipStream_t st);
+struct CombineRowsArgs {
+    const void *rows;       // [R, H] f32 or bf16
+    const int32_t *row_of;  // [T, k]; outside 0..R-1: an empty slot
+    const float *w;         // [T, k] or null: 1
+    void *y;                // [T, H]
+    const void *dy;         // [T, H], row stride ldy as y
+    void *drows;            // [R, H] or null
+    float *dw;              // [T, k] or null
+    int64_t ldr, ldy;
+    int T, H, k, R, f32;
+};
+void launch_combine_rows(const CombineRowsArgs &a, hipStream_t st);
+void launch_combine_rows_grad(const CombineRowsArgs &a, hipStream_t st);
+
+// SwiGLU and its gradient, with gate and up as codes (swiglu.hip).
+struct SwigluArgs {
+    const void *gate, *up;  // [R, I], row stride ld
+    const void *dh;         // [R, I], row stride ldh
+    void *h;                // [R, I], row stride ldh
+    void *dgate, *dup;      // [R, I], row stride ld
+    uint8_t *codes;         // [R, 2 * 128 * KB]: gate's, then up's; or null
+    float *scales;          // [R, 2 * KB]
+    const int32_t *used;    // rows in use, or null: all
+    int64_t ld, ldh;
+    int R, I, KB, bf16;
+    uint32_t magic;         // quotient by KB (set by the launchers)
+    int magic_shift;
+};
+void launch_swiglu(SwigluArgs a, hipStream_t st);
+void launch_swiglu_grad(SwigluArgs a, hipStream_t st);
+
+// Gradient of the selection to the logits (select_grad.hip).
+struct SelectGradArgs {
+    const void *logits;   // [T, E], row stride ld elements, bf16 or fp32
+    const float *bias;    // [E] or null
+    const int32_t *idx;   // [T, k]
+    const float *dw;      // [T, k]
+    const float *dscore;  // [E] or null
+    void *dlogits;        // [T, E], fp32 or bf16
+    int64_t ld;
+    int T, E, k, softmax, renorm, bf16, out_f32;
+    float scale;
+};
+void launch_select_grad(const SelectGradArgs &a, hipStream_t st);
+
+// Grouped bf16 products and their gradients (matmul_bf16.hip): out = P Q^T over c,
+// P, Q and c by the way.
+enum { MM_Y = 0, MM_DX = 1, MM_DW = 2 };
+struct Mm16Args {
+    const uint16_t *p, *q;   // y: x, w; dx: dy, w; dw: dy, x
+    const int32_t *offsets;  // [G + 1] or null
+    const void *add;         // as out, or null
+    void *out;
+    int64_t ldp, ldq, ldo;
+    int64_t qstride;         // from one group's matrix q to the next (y, dx)
+    int64_t ostride;         // from one group's matrix of out to the next (dw)
+    int M, G;                // rows, groups
+    int P, Q, C;             // y: M, N, K; dx: M, K, N; dw: N, K, M
+    int way, out_f32;
+};
+int64_t mm16_most_tiles(const Mm16Args &a);  // bound of the tiles of any variant
+void launch_mm16(const Mm16Args &a, hipStream_t st);
+
 // Measurement aids (probe.hip): the device's HBM read (sequential and
 // scattered), MXFP4 dequantisation stream and bf16 MFMA ceilings.
 void launch_probe_read(const void *buf, size_t bytes, int *sink, hipStream_t st);

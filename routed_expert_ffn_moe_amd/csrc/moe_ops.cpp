@@ -5,23 +5,13 @@
 #include <cstdint>
 
 #include "../../include/moe.h"
+#include "args.h"
 #include "kernels.h"
 
-namespace {
-
-bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
-{
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
-int bad(const char *what) { return moe::api_fail(MOE_EINVAL, what); }
-
-}  // namespace
+using moe::aligned;
+using moe::bad;
+using moe::cdiv;
+using moe::overlap;
 
 extern "C" {
 

@@ -1,0 +1,208 @@
+// Gradient of moe_select's weights, and of a sum of scores, to the logits.
+//
+// With d_j the gradient of weight j, k slots with experts e_j, scale c:
+//   renormalised   p_j = s_j / sum of the selected s,
+//                  a_j = c p_j sum over i of p_i (d_j - d_i), and softmax
+//                  dl[e_j] += a_j, sigmoid dl[e_j] += a_j (1 - s_j)
+//   as they are    a gradient c d_j of score e_j, with the scores' below
+//   scores         g_e of score e (the caller's dscore and the line above):
+//                  softmax dl_e += s_e (g_e - sum over i of s_i g_i), sigmoid
+//                  dl_e += g_e s_e (1 - s_e)
+//
+// Differences are taken before they are weighted: sum_i p_i (d_j - d_i) in place
+// of d_j - sum_i p_i d_i, and g_e less the g of the largest score, so that a score
+// near 1, whose gradient is the small rest, keeps its digits.  The ratios p come
+// from the logarithms of the scores less the largest selected one, and neither
+// over- nor underflow.
+//
+// One wave per token, its row of logits in registers.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.h"
+#include "fp8.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float LARGEST = 3.4028234e38f;
+// Logits whose 64-bit score is 0: selected ones have weight 0 and no gradient.
+constexpr float SIGMOID_ZERO = -709.78f, SOFTMAX_ZERO = -745.14f;
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// Lane l's experts are l, l + 64, ...
+template <int PER, bool BF16, bool OUT_F32>
+__global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    for (int64_t t = blockIdx.x * 4ll + (threadIdx.x >> 6); t < a.T; t += gridDim.x * 4ll) {
+        float l[PER], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = lane + 64 * i;
+            float v = -INFINITY;
+            if (e < a.E)
+                v = BF16 ? bf2f(((const uint16_t *)a.logits)[t * a.ld + e]) : ((const float *)a.logits)[t * a.ld + e];
+            l[i] = v > -INFINITY ? fminf(v, LARGEST) : -INFINITY;  // NaN: masked
+            top = fmaxf(top, l[i]);
+        }
+        // lane j < k: slot j, its expert's logit, masked if it or the bias is
+        int e = -1;
+        float d = 0.0f, z = -INFINITY;
+        if (lane < a.k) {
+            e = a.idx[t * a.k + lane];
+            e = (unsigned)e < (unsigned)a.E ? e : -1;
+            if (e >= 0) {
+                d = a.dw[t * a.k + lane];
+                const float v = BF16 ? bf2f(((const uint16_t *)a.logits)[t * a.ld + e])
+                                     : ((const float *)a.logits)[t * a.ld + e];
+                const float b = a.bias ? a.bias[e] : 0.0f;
+                z = v > -INFINITY && b > -INFINITY ? fminf(v, LARGEST) : -INFINITY;
+            }
+        }
+        if (a.softmax) {
+            top = wave_max(top);
+            if (z - top < SOFTMAX_ZERO)
+                z = -INFINITY;
+        } else if (z < SIGMOID_ZERO) {
+            z = -INFINITY;
+        }
+        const bool live = z > -INFINITY;
+        float slot = d * a.scale;  // what a slot adds: to its logit if renormalised, else to its score's gradient
+        if (a.renorm) {
+            // logarithm of the score (of a softmax, up to the token's constant)
+            const float ls = !live || a.softmax ? z : fminf(z, 0.0f) - log1pf(expf(-fabsf(z)));
+            const float most = wave_max(ls);  // every lane takes part
+            const float q = live ? expf(ls - most) : 0.0f;
+            float total = 0.0f, sum = 0.0f;
+            for (int i = 0; i < a.k; ++i) {
+                const float qi = __shfl(q, i), di = __shfl(d, i);
+                total += qi;
+                sum += qi > 0.0f ? qi * (d - di) : 0.0f;
+            }
+            slot = live ? a.scale * (q / total) * (sum / total) : 0.0f;
+            if (!a.softmax && live)
+                slot *= z > 0.0f ? expf(-z) / (1.0f + expf(-z)) : 1.0f / (1.0f + expf(z));
+        }
+        if (!live)
+            e = -1;
+        float g[PER], out[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            g[i] = out[i] = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+            const int ej = __shfl(e, j);
+            const float v = __shfl(slot, j);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (ej == lane + 64 * i) {
+                    if (a.renorm)
+                        out[i] += v;
+                    else
+                        g[i] += v;
+                }
+        }
+        if (a.dscore || !a.renorm) {  // uniform
+            if (a.dscore)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int x = lane + 64 * i;
+                    if (x < a.E && l[i] > -INFINITY && !(a.bias && !(a.bias[x] > -INFINITY)))
+                        g[i] += a.dscore[x];
+                }
+            if (a.softmax) {
+                float s[PER], sum = 0.0f, mean = 0.0f, ref = 0.0f;
+                bool at_top = false;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    s[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+                    sum += s[i];
+                    if (l[i] == top && !at_top) {
+                        at_top = true;
+                        ref = g[i];
+                    }
+                }
+                const uint64_t who = __ballot(at_top);  // never empty unless all are NaN
+                ref = __shfl(ref, who ? __ffsll((unsigned long long)who) - 1 : 0);
+                sum = wave_sum(sum);
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    s[i] *= inv;
+                    g[i] -= ref;
+                    mean += s[i] > 0.0f ? s[i] * g[i] : 0.0f;
+                }
+                mean = wave_sum(mean);
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    out[i] += s[i] > 0.0f ? s[i] * (g[i] - mean) : 0.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const float x = expf(-fabsf(l[i])), y = 1.0f + x;  // masked: 0
+                    out[i] += x > 0.0f ? g[i] * (x / (y * y)) : 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = lane + 64 * i;
+            if (x < a.E) {
+                if constexpr (OUT_F32)
+                    ((float *)a.dlogits)[t * a.E + x] = out[i];
+                else
+                    ((uint16_t *)a.dlogits)[t * a.E + x] = (uint16_t)cvt_bf2(out[i], 0.0f);
+            }
+        }
+    }
+}
+
+template <int PER>
+void launch_per(const SelectGradArgs &a, hipStream_t st)
+{
+    const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)a.T + 3) / 4, 1 << 20);
+    if (a.bf16)
+        a.out_f32 ? select_grad_rows<PER, true, true><<<grid, 256, 0, st>>>(a)
+                  : select_grad_rows<PER, true, false><<<grid, 256, 0, st>>>(a);
+    else
+        a.out_f32 ? select_grad_rows<PER, false, true><<<grid, 256, 0, st>>>(a)
+                  : select_grad_rows<PER, false, false><<<grid, 256, 0, st>>>(a);
+}
+
+}  // namespace
+
+void launch_select_grad(const SelectGradArgs &a, hipStream_t st)
+{
+    const int per = (a.E + 63) / 64;
+    if (per <= 1)
+        launch_per<1>(a, st);
+    else if (per <= 2)
+        launch_per<2>(a, st);
+    else if (per <= 4)
+        launch_per<4>(a, st);
+    else if (per <= 6)
+        launch_per<6>(a, st);
+    else if (per <= 8)
+        launch_per<8>(a, st);
+    else
+        launch_per<16>(a, st);
+}
+
+}  // namespace moe
