@@ -323,6 +323,9 @@ struct Mm16Args {
 };
 int64_t mm16_most_tiles(const Mm16Args &a);  // bound of the tiles of any variant
 void launch_mm16(const Mm16Args &a, hipStream_t st);
+// Operands whose rows can be copied in pieces of 16 bytes (matmul_bf16_tile.hip).
+bool mm16_tiles_ok(const Mm16Args &a);
+void launch_mm16_tiles(const Mm16Args &a, hipStream_t st);
 
 // Measurement aids (probe.hip): the device's HBM read (sequential and
 // scattered), MXFP4 dequantisation stream and bf16 MFMA ceilings.

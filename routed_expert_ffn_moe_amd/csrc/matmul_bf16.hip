@@ -14,59 +14,12 @@
 #include "common.h"
 #include "fp8.h"
 #include "kernels.h"
+#include "mm16.h"
 #include "quant_fp8.h"
-#include "rows.h"
 
 namespace moe {
 
 namespace {
-
-enum { WAY_Y = MM_Y, WAY_DX = MM_DX, WAY_DW = MM_DW };
-
-// What a tile multiplies: P rows p0 .. p0 + np - 1 against Q rows from q0, over c.
-struct Job {
-    const uint16_t *p, *q;
-    int64_t out;      // element of the tile's first row
-    int np, nq, nc, p0, q0;
-    bool there;
-};
-
-// Tile `id`; the tiles of neighbouring numbers share their group.
-template <int WAY, int BP, int BQ>
-__device__ __forceinline__ Job find_job(const Mm16Args &a, int id)
-{
-    Job j{};
-    const int ntq = (a.Q + BQ - 1) / BQ, tp = id / ntq, q0 = (id - tp * ntq) * BQ;
-    j.q0 = q0;
-    j.nq = min(BQ, a.Q - q0);
-    if constexpr (WAY == WAY_DW) {
-        const int ntp = (a.P + BP - 1) / BP, g = tp / ntp;
-        int lo = 0, hi = a.M;
-        if (a.offsets) {
-            lo = min(max(uniform_load(a.offsets + g), 0), a.M);
-            hi = min(uniform_load(a.offsets + g + 1), a.M);
-        }
-        j.p0 = (tp - g * ntp) * BP;
-        j.np = min(BP, a.P - j.p0);
-        j.nc = max(hi - lo, 0);
-        j.p = a.p + (int64_t)lo * a.ldp + j.p0;
-        j.q = a.q + (int64_t)lo * a.ldq + q0;
-        j.out = (int64_t)g * a.ostride + (int64_t)j.p0 * a.ldo + q0;
-        j.there = true;
-    } else {
-        Where t{0, tp * BP, min(BP, a.M - tp * BP), 0, 0};
-        if (a.offsets)
-            t = find_rows<BP>(a.offsets, a.G, a.M, tp);
-        j.there = t.g >= 0;
-        j.p0 = t.row0;
-        j.np = t.nrows;
-        j.nc = a.C;
-        j.p = a.p + (int64_t)t.row0 * a.ldp;
-        j.q = a.q + (int64_t)t.g * a.qstride + (WAY == WAY_DX ? (int64_t)q0 : (int64_t)q0 * a.ldq);
-        j.out = (int64_t)t.row0 * a.ldo + q0;
-    }
-    return j;
-}
 
 template <bool F32>
 __device__ __forceinline__ void put(const Mm16Args &a, int64_t at, float v)
@@ -124,7 +77,7 @@ __device__ __forceinline__ void any_store(uint16_t *s, int r, int c, u16x8 v)
 template <int WAY, bool F32>
 __global__ __launch_bounds__(256) void mm16_any(Mm16Args a, int tiles)
 {
-    constexpr bool PA = WAY != WAY_DW, QA = WAY == WAY_Y;
+    constexpr bool PA = WAY != MM_DW, QA = WAY == MM_Y;
     __shared__ __attribute__((aligned(16))) uint16_t sp[ANY_T * ANY_LD], sq[ANY_T * ANY_LD];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4, w = tid >> 6;
     const int wp = (w & 1) * 32, wq = (w >> 1) * 32;
@@ -132,7 +85,7 @@ __global__ __launch_bounds__(256) void mm16_any(Mm16Args a, int tiles)
     const int pr = PA ? tid >> 2 : (tid & 7) * 8, pc = PA ? (tid & 3) * 8 : tid >> 3;
     const int qr = QA ? tid >> 2 : (tid & 7) * 8, qc = QA ? (tid & 3) * 8 : tid >> 3;
     for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
-        const Job j = find_job<WAY, ANY_T, ANY_T>(a, id);
+        const Mm16Job j = find_job<WAY, ANY_T, ANY_T>(a, id);
         if (!j.there)
             continue;
         floatx4 acc[2][2] = {};
@@ -172,18 +125,10 @@ __global__ __launch_bounds__(256) void mm16_any(Mm16Args a, int tiles)
     }
 }
 
-int64_t tile_count(const Mm16Args &a, int bp, int bq)
-{
-    const int64_t ntq = ((int64_t)a.Q + bq - 1) / bq;
-    if (a.way == MM_DW)
-        return a.G * (((int64_t)a.P + bp - 1) / bp) * ntq;
-    return (a.G > 1 ? a.M / bp + a.G : ((int64_t)a.M + bp - 1) / bp) * ntq;
-}
-
 template <int WAY>
 void launch_any(const Mm16Args &a, hipStream_t st)
 {
-    const int64_t tiles = tile_count(a, ANY_T, ANY_T);
+    const int64_t tiles = mm16_tile_count(a, ANY_T, ANY_T);
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
     if (a.out_f32)
         mm16_any<WAY, true><<<grid, 256, 0, st>>>(a, (int)tiles);
@@ -193,16 +138,18 @@ void launch_any(const Mm16Args &a, hipStream_t st)
 
 }  // namespace
 
-int64_t mm16_most_tiles(const Mm16Args &a) { return tile_count(a, 16, 16); }
+int64_t mm16_most_tiles(const Mm16Args &a) { return mm16_tile_count(a, 16, 16); }
 
 void launch_mm16(const Mm16Args &a, hipStream_t st)
 {
+    if (mm16_tiles_ok(a))
+        return launch_mm16_tiles(a, st);
     if (a.way == MM_Y)
-        launch_any<WAY_Y>(a, st);
+        launch_any<MM_Y>(a, st);
     else if (a.way == MM_DX)
-        launch_any<WAY_DX>(a, st);
+        launch_any<MM_DX>(a, st);
     else
-        launch_any<WAY_DW>(a, st);
+        launch_any<MM_DW>(a, st);
 }
 
 }  // namespace moe

@@ -1,0 +1,471 @@
+// The grouped bf16 products where both operands can be copied to LDS in pieces
+// of 16 bytes (the form of the products is in matmul_bf16.hip).
+//
+// A workgroup of WP x WQ waves owns BP x BQ outputs and steps through c 64 at a
+// time, with ST stages of both operands in LDS, filled by asynchronous copies.
+// An operand with c adjacent lies there in rows of 64 c, one with p or q adjacent
+// as it comes, 64 rows of c, and is transposed by the LDS read itself
+// (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 elements and get columns of 4).
+// Pieces of 16 bytes are rotated (XOR) by their row so that the lanes of one read
+// fall on distinct banks: 2.3 cycles for a wave's 512 bytes transposed (15.8
+// unrotated), 4.1 for its 1024 bytes in rows.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.h"
+#include "fp8.h"
+#include "kernels.h"
+#include "mm16.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int STEP = 64;  // depth of a stage
+constexpr int DROP = (int)0x80000000;  // an offset outside every buffer: loads give 0, stores do nothing
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Buffer of the bytes from p on.
+__device__ __forceinline__ intx4 buffer_words(const void *p)
+{
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    return intx4{(int)b, (int)(b >> 32) & 0xFFFF, 0x7FFFFFFF, 0x00027000};
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rsrc(const void *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00027000);
+}
+
+// As dma16 (fp8.h), through a buffer: an offset of DROP writes zeros to LDS.
+__device__ __forceinline__ void dma16_buffer(intx4 rsrc, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
+                 "s"(rsrc)
+                 : "memory", "m0");
+}
+
+// The element that row r of block b of 16 holds where the two are not alike: pairs
+// of blocks share 32 elements such that a lane's results of a pair are 8 adjacent
+// ones, and the rows of a block read both halves of the pieces of 8 elements (so
+// that a transposing read falls on all banks).
+__device__ __forceinline__ int paired(int b, int r)
+{
+    return (b >> 1) * 32 + (r >> 2) * 8 + (((b ^ (r >> 2)) & 1) << 2) + (r & 3);
+}
+
+template <int I>
+using Int = std::integral_constant<int, I>;
+
+// f(Int<B>) .. f(Int<E - 1>)
+template <int B, int E, class F>
+__device__ __forceinline__ void each(F &&f)
+{
+    if constexpr (B < E) {
+        f(Int<B>{});
+        each<B + 1, E>(f);
+    }
+}
+
+// One operand's tile of XN elements by 64 c in LDS, in blocks of 16 elements whose
+// order is that of paired() where PAIR says so (always where the read transposes).
+template <int XN, bool ADJ, bool PAIR>
+struct Operand {
+    static constexpr int BYTES = XN * STEP * 2, COPIES = BYTES / 1024;
+    static constexpr int ROW = ADJ ? 128 : XN * 2;     // bytes of a row in LDS
+    static constexpr int PER = 1024 / ROW;             // rows of a copy
+    static_assert(XN % (PAIR ? 32 : 16) == 0 && (ADJ || (PAIR && XN % 64 == 0)), "whole blocks, and whole rotations");
+
+    // What the pieces of a row are rotated by.
+    __device__ static __forceinline__ int key(int row)
+    {
+        if (ADJ)
+            return (row >> 1) & 7;
+        return XN >= 128 ? (row & 3) << 2 | ((row >> 3) & 1) : (row & 2) << 1 | ((row >> 3) & 1);
+    }
+    // Copy i of the tile: the lane's element and c.
+    struct Piece {
+        int x, c;
+    };
+    __device__ static __forceinline__ Piece piece(int i, int lane)
+    {
+        const int row = i * PER + lane / (64 / PER), at = (lane % (64 / PER)) ^ key(row);
+        if (!ADJ)
+            return Piece{at * 8, row};
+        return Piece{PAIR ? paired(row >> 4, row & 15) : row, at * 8};
+    }
+    // Byte offset in LDS of the lane's fragment of block b: 8 c of one element, c
+    // from 8 * (lane / 16) on.
+    __device__ static __forceinline__ int where(int b, int lane)
+    {
+        const int l16 = lane & 15, lg = lane >> 4;
+        if (ADJ)
+            return b * 2048 + l16 * 128 + ((lg ^ key(l16)) << 4);
+        // 16 lanes read 4 c of 16 elements, 4 elements a lane, and get 4 c of one
+        const int row = lg * 8 + (l16 >> 2), e = (b >> 1) * 32 + (l16 & 3) * 8;
+        return row * ROW + (((e >> 3) ^ key(row)) << 4) + (((b ^ l16) & 1) << 3);
+    }
+    // The fragment of the 32 c of half h of the step.
+    __device__ static __forceinline__ bf16x8 read(const uint8_t *tile, int at, int h)
+    {
+        if (ADJ)
+            return *(const bf16x8 *)(tile + (at ^ (h << 6)));
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) bf16x4 *Ptr;
+        const auto p = (__attribute__((address_space(3))) const uint8_t *)tile + at + h * (32 * ROW);
+        const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Ptr)p);
+        const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Ptr)(p + 4 * ROW));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX>
+struct Tiling {
+    static constexpr int NW = WP * WQ, MB = BP / 16 / WP, NB = BQ / 16 / WQ;
+    using P = Operand<BP, WAY != MM_DW, WAY == MM_DW>;
+    using Q = Operand<BQ, WAY == MM_Y, true>;
+    static constexpr int PI = (P::COPIES + NW - 1) / NW, QI = (Q::COPIES + NW - 1) / NW, L = PI + QI;
+    static constexpr int O_Q = (ST + EX) * P::BYTES, LDS = O_Q + ST * Q::BYTES;
+    static constexpr int OCC = 163840 / LDS;
+    static constexpr int NS = MB * (NB / 2) * (F32 ? 2 : 1);  // stores of a wave and tile
+    static_assert(MB * WP * 16 == BP && NB * WQ * 16 == BQ && NB % 2 == 0, "whole blocks");
+    static_assert(WAY != MM_DW || MB % 2 == 0, "whole pairs");
+    static_assert((ST - 1) * L + EX * PI < 64 && (ST - 2) * L + EX * PI + NS < 64, "the counter of outstanding operations holds 63");
+};
+
+// Persistent workgroups.
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX>
+__global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles)
+{
+    using C = Tiling<WAY, F32, BP, BQ, WP, WQ, ST, EX>;
+    using P = typename C::P;
+    using Q = typename C::Q;
+    constexpr int MB = C::MB, NB = C::NB, L = C::L, NS = C::NS;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wq = w % WQ, wp = w / WQ;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+    // ---- tiles: contiguous runs per XCD, dealt in turn to its workgroups ----
+    // Panels of 4 row tiles by all column tiles, so that what an XCD works on at
+    // a time is about square.
+    const int ntq = (a.Q + BQ - 1) / BQ;
+    const int total = mtiles * ntq, per = (total + 7) / 8;
+    const int first = ((int)blockIdx.x & 7) * per, step_q = (int)gridDim.x >> 3;
+    auto find = [&](int q) {
+        for (; q < per && first + q < total; q += step_q) {
+            const int id = first + q, panel = id / (4 * ntq), in = id - panel * 4 * ntq;
+            const int rows = min(4, mtiles - panel * 4), tq = in / rows, tp = panel * 4 + (in - tq * rows);
+            Mm16Job j = find_job<WAY, BP, BQ>(a, tp * ntq + tq);
+            j.next = q + step_q;
+            if (j.there)
+                return j;
+        }
+        return Mm16Job{};
+    };
+
+    // ---- copies, on into the next tiles: ST stages of Q and EX more of P ----
+    // Each stage of Q is copied behind the same one of P, and so finds the tile
+    // that it belongs to as that of P.  Behind the last tile the copies go on with
+    // offsets outside the buffer, which write zeros into free stages and read
+    // nothing: every step issues the same copies, without a branch.
+    uint32_t poff[C::PI], qoff[C::QI];
+    const uint16_t *gp = a.p, *gq = a.q, *gq_first = a.q;
+    int pleft = 0, qleft = 0, nc = 0, nq = 0;  // c not yet copied; c and columns of P's tile
+    uint32_t pst = 0, qst = 0;                 // byte of the next stage
+    int pnext = (int)blockIdx.x >> 3;
+    // The next stage of P: its tile, zeros behind the last c.
+    auto next_p = [&]() {
+        if (pleft > 0 && pleft >= STEP)
+            return;
+        int ln = lane;  // hidden from the compiler, which would keep what depends on it in registers
+        asm volatile("" : "+v"(ln));
+        if (pleft <= 0) {
+            Mm16Job j;
+            do {
+                j = find(pnext);
+                pnext = j.next;
+            } while (j.there && j.nc == 0);
+            if (j.there) {
+                gp = j.p;
+                gq_first = j.q;
+            }
+            nc = j.there ? j.nc : 1 << 30;
+            nq = j.nq;
+            pleft = nc;
+#pragma unroll
+            for (int i = 0; i < C::PI; ++i) {
+                const auto s = P::piece((w * C::PI + i) % P::COPIES, ln);
+                const uint32_t at = WAY == MM_DW ? s.c * (uint32_t)a.ldp + s.x : s.x * (uint32_t)a.ldp + s.c;
+                poff[i] = s.x < j.np ? at * 2 : (uint32_t)DROP;
+            }
+        }
+        if (pleft < STEP)
+#pragma unroll
+            for (int i = 0; i < C::PI; ++i)
+                if (P::piece((w * C::PI + i) % P::COPIES, ln).c >= pleft)
+                    poff[i] = (uint32_t)DROP;
+    };
+    auto next_q = [&]() {
+        if (qleft > 0 && qleft >= STEP)
+            return;
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        if (qleft <= 0) {
+            gq = gq_first;
+            qleft = nc;
+#pragma unroll
+            for (int i = 0; i < C::QI; ++i) {
+                const auto s = Q::piece((w * C::QI + i) % Q::COPIES, ln);
+                const uint32_t at = WAY != MM_Y ? s.c * (uint32_t)a.ldq + s.x : s.x * (uint32_t)a.ldq + s.c;
+                qoff[i] = s.x < nq ? at * 2 : (uint32_t)DROP;
+            }
+        }
+        if (qleft < STEP)
+#pragma unroll
+            for (int i = 0; i < C::QI; ++i)
+                if (Q::piece((w * C::QI + i) % Q::COPIES, ln).c >= qleft)
+                    qoff[i] = (uint32_t)DROP;
+    };
+    // part J of N of a stage's copies
+    auto issue_p = [&](auto part, auto parts) {
+        constexpr int J = decltype(part)::value, N = decltype(parts)::value;
+        if constexpr (J == 0)
+            next_p();
+#pragma unroll
+        for (int i = 0; i < C::PI; ++i)
+            if (i * N / C::PI == J)
+                dma16_buffer(buffer_words(gp), poff[i], lds + pst + (uint32_t)((w * C::PI + i) % P::COPIES) * 1024u);
+        if constexpr (J == N - 1) {
+            gp += WAY == MM_DW ? (int64_t)STEP * a.ldp : STEP;
+            pleft -= STEP;
+            pst = pst + P::BYTES == C::O_Q ? 0 : pst + P::BYTES;
+        }
+    };
+    auto issue_q = [&](auto part, auto parts) {
+        constexpr int J = decltype(part)::value, N = decltype(parts)::value;
+        if constexpr (J == 0)
+            next_q();
+#pragma unroll
+        for (int i = 0; i < C::QI; ++i)
+            if (i * N / C::QI == J)
+                dma16_buffer(buffer_words(gq), qoff[i],
+                             lds + C::O_Q + qst + (uint32_t)((w * C::QI + i) % Q::COPIES) * 1024u);
+        if constexpr (J == N - 1) {
+            gq += WAY != MM_Y ? (int64_t)STEP * a.ldq : STEP;
+            qleft -= STEP;
+            qst = qst + Q::BYTES == ST * Q::BYTES ? 0 : qst + Q::BYTES;
+        }
+    };
+    constexpr Int<0> all{};
+    constexpr Int<1> once{};
+
+    Mm16Job cur = find((int)blockIdx.x >> 3);
+    if (!cur.there)
+        return;
+    // up to where a step's first copies go on
+    for (int s = 0; s < ST; ++s) {
+        issue_p(all, once);
+        if (EX || s + 1 < ST)
+            issue_q(all, once);
+    }
+    int pat[MB], qat[NB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+        pat[m] = P::where(wp * MB + m, lane);
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+        qat[c] = C::O_Q + Q::where(wq * NB + c, lane);
+
+    // A step is U units: the 16 rows of block u % MB against all columns over half
+    // u / MB of the 64 c.  A unit's rows are read D units before, the columns of the
+    // second half during the first.  Once the last rows of a stage are read, D units
+    // before the step's end, the workgroup turns to the next stage: it is there for
+    // every wave, this one's buffer falls free, and the first fragments of the next
+    // stage are under way while the last units are multiplied.
+    constexpr int U = 2 * MB, D = MB >= 4 ? 3 : 1;
+    static_assert(U % (D + 1) == 0 && D <= MB && (EX || ST >= 3), "the ring of rows goes on from step to step");
+    bf16x8 qf[2][NB], pf[D + 1];
+    uint32_t pc = 0, qc = 0;  // byte of the stage that is multiplied
+    auto load_q = [&](int c, int h) { qf[h & 1][c] = Q::read(smem + qc, qat[c], h); };
+    auto load_p = [&](auto unit) {  // unit U + u: of the next stage, which is the one multiplied by then
+        constexpr int u = decltype(unit)::value;
+        pf[u % (D + 1)] = P::read(smem + pc, pat[u % MB], u / MB % 2);
+    };
+    dma_wait_barrier<EX ? (ST - 1) * L : (ST - 2) * L + C::PI>();
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+        load_q(c, 0);
+    each<0, D>(load_p);
+
+    // Copies hold up what the wave issues behind them while the memory system is
+    // busy, so they are spread: the operand whose stage is needed first over the
+    // units behind the barrier that frees its buffer, the other one over the next
+    // step's units.
+    auto copies = [&](auto unit) {
+        constexpr int u = decltype(unit)::value;
+        if constexpr (u >= U - D) {
+            if constexpr (EX)
+                issue_q(Int<u - (U - D)>{}, Int<D>{});
+            else
+                issue_p(Int<u - (U - D)>{}, Int<D>{});
+        } else {
+            if constexpr (EX)
+                issue_p(Int<u>{}, Int<U - D>{});
+            else
+                issue_q(Int<u>{}, Int<U - D>{});
+        }
+    };
+
+    bool stored = false;  // NS stores were issued behind the copies of this tile's first ST - 1 stages
+    for (;;) {
+        floatx4 acc[NB][MB];
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                acc[c][m] = floatx4{0, 0, 0, 0};
+        const int n = (cur.nc + STEP - 1) / STEP;
+        for (int s = 0; s < n; ++s) {
+            each<0, U>([&](auto unit) {
+                constexpr int u = decltype(unit)::value;
+                if constexpr (u < MB) {  // the columns of the second half
+#pragma unroll
+                    for (int c = 0; c < NB; ++c)
+                        if (c * std::min(MB, 4) / NB == u)
+                            load_q(c, 1);
+                }
+                if constexpr (u == U - D) {
+                    // older than what may be under way: the next stage
+                    if (s + 2 - EX < ST && stored)
+                        dma_wait_barrier<(ST - 2) * L + EX * C::PI + NS>();
+                    else
+                        dma_wait_barrier<(ST - 2) * L + EX * C::PI>();
+                    pc = pc + P::BYTES == C::O_Q ? 0 : pc + P::BYTES;
+                    qc = qc + Q::BYTES == ST * Q::BYTES ? 0 : qc + Q::BYTES;
+                }
+                if constexpr (u >= U - D) {
+#pragma unroll
+                    for (int c = 0; c < NB; ++c)
+                        if (c * D / NB == u - (U - D))
+                            load_q(c, 0);
+                }
+                load_p(Int<u + D>{});
+                copies(unit);
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                    acc[c][u % MB] = mfma16(qf[u / MB][c], pf[u % (D + 1)], acc[c][u % MB]);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
+        mfma_acc_drain();
+        const Mm16Job next = find(cur.next);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // ---- results: 8 adjacent columns of a row from a pair of blocks.  Lanes
+        // outside the output store out of the buffer's range, so that every wave issues
+        // the same number of stores and the waits above can count them.
+        int e16 = lane & 15, eg = lane >> 4;  // hidden as in next_p()
+        asm volatile("" : "+v"(e16), "+v"(eg));
+        constexpr int esz = F32 ? 4 : 2, V = F32 ? 2 : 1;  // 16-byte stores of a pair
+        const auto ro = out_rsrc((const char *)a.out + cur.out * esz);
+        const auto ra = out_rsrc((const char *)(a.add ? a.add : a.out) + cur.out * esz);
+        const int pitch = (int)a.ldo * esz;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            const int p = wp * (16 * MB) + (WAY == MM_DW ? paired(m, e16) : m * 16 + e16);
+            int at[NB / 2];
+            u32x4 add[NB / 2][V];
+#pragma unroll
+            for (int c = 0; c < NB / 2; ++c) {
+                const int q = wq * (16 * NB) + c * 32 + eg * 8;
+                at[c] = p < cur.np && q < cur.nq ? p * pitch + q * esz : DROP;
+                if (a.add)
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        add[c][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at[c], 16 * i, 0));
+            }
+#pragma unroll
+            for (int c = 0; c < NB / 2; ++c) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = acc[2 * c][m][i], y = acc[2 * c + 1][m][i];
+                    v[i] = eg & 1 ? y : x;
+                    v[4 + i] = eg & 1 ? x : y;
+                }
+                if (a.add)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] += F32 ? __uint_as_float(add[c][F32 ? i >> 2 : 0][i & 3])
+                                    : __uint_as_float(i & 1 ? add[c][0][i >> 1] & 0xFFFF0000u : add[c][0][i >> 1] << 16);
+                if constexpr (F32) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])},
+                            ro, at[c], 16 * i, 0);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        u32x4{cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7])},
+                        ro, at[c], 0, 0);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (!next.there) {
+            dma_wait_barrier<0>();  // no copy outlives the workgroup
+            break;
+        }
+        cur = next;
+        stored = true;
+    }
+}
+
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX>
+void launch_tiling(const Mm16Args &a, hipStream_t st)
+{
+    using C = Tiling<WAY, F32, BP, BQ, WP, WQ, ST, EX>;
+    const int64_t tiles = mm16_tile_count(a, BP, BQ);
+    const int ntq = (a.Q + BQ - 1) / BQ;
+    const unsigned grid = (unsigned)(std::min<int64_t>(tiles, 256 * C::OCC) + 7) / 8 * 8;
+    mm16_tile<WAY, F32, BP, BQ, WP, WQ, ST, EX><<<grid, 64 * C::NW, 0, st>>>(a, (int)(tiles / ntq));
+}
+
+template <int WAY, bool F32>
+void launch_way(const Mm16Args &a, hipStream_t st)
+{
+    launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1>(a, st);
+}
+
+}  // namespace
+
+// Whole pieces of 16 bytes along every row, and offsets inside a tile that fit 31
+// bits.
+bool mm16_tiles_ok(const Mm16Args &a)
+{
+    auto on16 = [](const void *p) { return ((uintptr_t)p & 15) == 0; };
+    const int esz = a.out_f32 ? 4 : 2;
+    const bool sizes = a.Q % 8 == 0 && (a.way == MM_DW ? a.P % 8 == 0 : a.C % 8 == 0);
+    return sizes && a.ldp % 8 == 0 && a.ldq % 8 == 0 && a.ldo * esz % 16 == 0 && std::max({a.ldp, a.ldq, a.ldo}) < 1 << 20 &&
+           on16(a.p) && on16(a.q) && on16(a.out) && on16(a.add);
+}
+
+void launch_mm16_tiles(const Mm16Args &a, hipStream_t st)
+{
+    auto typed = [&](auto way) {
+        constexpr int WAY = decltype(way)::value;
+        a.out_f32 ? launch_way<WAY, true>(a, st) : launch_way<WAY, false>(a, st);
+    };
+    if (a.way == MM_Y)
+        typed(std::integral_constant<int, MM_Y>{});
+    else if (a.way == MM_DX)
+        typed(std::integral_constant<int, MM_DX>{});
+    else
+        typed(std::integral_constant<int, MM_DW>{});
+}
+
+}  // namespace moe
