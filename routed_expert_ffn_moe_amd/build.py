@@ -21,7 +21,7 @@ SOURCES = ["probe.hip", "router.hip", "route_small.hip", "permute.hip", "expert_
            "expert_stream.hip", "mxfp4.hip", "select.hip", "quant_fp8.hip", "matmul_fp8.hip",
            "matmul_fp8_small.hip",
            "experts_given.hip", "dispatch.hip", "swiglu.hip", "select_grad.hip", "matmul_bf16.hip",
-           "matmul_bf16_tile.hip",
+           "matmul_bf16_y.hip", "matmul_bf16_dx.hip", "matmul_bf16_dw.hip",
            "moe_api.cpp", "moe_ops.cpp", "moe_train.cpp", "noalloc.hip"]
 
 FLAGS = [

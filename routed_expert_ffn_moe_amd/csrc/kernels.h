@@ -323,9 +323,11 @@ struct Mm16Args {
 };
 int64_t mm16_most_tiles(const Mm16Args &a);  // bound of the tiles of any variant
 void launch_mm16(const Mm16Args &a, hipStream_t st);
-// Operands whose rows can be copied in pieces of 16 bytes (matmul_bf16_tile.hip).
-bool mm16_tiles_ok(const Mm16Args &a);
-void launch_mm16_tiles(const Mm16Args &a, hipStream_t st);
+// Operands whose rows can be copied in pieces of 16 bytes, by tiles of a shape
+// (matmul_bf16_y.hip, _dx.hip, _dw.hip).
+void launch_mm16_y(const Mm16Args &a, int shape, hipStream_t st);
+void launch_mm16_dx(const Mm16Args &a, int shape, hipStream_t st);
+void launch_mm16_dw(const Mm16Args &a, int shape, hipStream_t st);
 
 // Measurement aids (probe.hip): the device's HBM read (sequential and
 // scattered), MXFP4 dequantisation stream and bf16 MFMA ceilings.

@@ -10,6 +10,7 @@
 //
 // Sums in fp32, the addend joined in fp32, rounded once.
 #include <algorithm>
+#include <cmath>
 
 #include "common.h"
 #include "fp8.h"
@@ -85,7 +86,16 @@ __global__ __launch_bounds__(256) void mm16_any(Mm16Args a, int tiles)
     const int pr = PA ? tid >> 2 : (tid & 7) * 8, pc = PA ? (tid & 3) * 8 : tid >> 3;
     const int qr = QA ? tid >> 2 : (tid & 7) * 8, qc = QA ? (tid & 3) * 8 : tid >> 3;
     for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
-        const Mm16Job j = find_job<WAY, ANY_T, ANY_T>(a, id);
+        const int ntq = (a.Q + ANY_T - 1) / ANY_T, tp = id / ntq, tq = id - tp * ntq;
+        Mm16Job j;
+        if constexpr (WAY == MM_DW) {
+            j = mm16_dw_job<ANY_T, ANY_T>(a, tp, tq);
+        } else {
+            Where t{0, tp * ANY_T, min(ANY_T, a.M - tp * ANY_T), 0, 0};
+            if (a.offsets)
+                t = find_rows<ANY_T>(a.offsets, a.G, a.M, tp);
+            j = mm16_row_job<WAY, ANY_T>(a, t, tq);
+        }
         if (!j.there)
             continue;
         floatx4 acc[2][2] = {};
@@ -138,18 +148,85 @@ void launch_any(const Mm16Args &a, hipStream_t st)
 
 }  // namespace
 
+namespace {
+
+// Tiles of the variants for whole pieces of 16 bytes (matmul_bf16_tile.h), with what
+// 64 of c cost in us: a tile alone, and on all CUs each of 256 tiles (several small
+// ones share a CU).
+struct Shape {
+    int bp, bq;
+    double alone, busy, end;
+};
+
+// Fitted to 56 products of each way, of 1 to 65536 rows in 1 to 256 groups, N and K
+// from 72 to 4096, each with all tiles: the pick's time is on average 4% (y), 5% (dx)
+// and 2% (dw) above the best tile's.  In us, largest against smallest tiles of that
+// list: 8192 x 4096 x 4096 201 against 1456 (y), 48 rows of 256 groups, N=768, K=2048
+// 138 against 59.  dx has no tiles of 16 columns, whose rows of c would be 32 bytes;
+// of dw, whose depth is the group's rows, the small tiles' outputs cost most (`end`):
+// 256 groups of 64 rows 236 against 388.
+constexpr Shape SHAPES_Y[] = {{256, 256, 1.4, 1.9, 0}, {128, 256, 1.0, 1.08, 0}, {64, 256, 0.89, 0.8, 0},
+                              {64, 128, 0.64, 0.44, 0}, {64, 64, 0.40, 0.34, 0}, {16, 64, 0.29, 0.21, 0},
+                              {16, 16, 0.166, 0.08, 0}};
+constexpr Shape SHAPES_DX[] = {{256, 256, 1.6, 1.95, 0}, {128, 256, 1.1, 1.15, 0}, {64, 256, 0.95, 0.87, 0},
+                               {64, 128, 0.73, 0.48, 0}, {64, 64, 0.50, 0.41, 0}, {16, 64, 0.44, 0.28, 0}};
+constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.57, 1.8}, {64, 64, 0.51, 0.275, 0.66}};
+
+// The shape that takes least time.  Groups whose balanced rows (1.4 standard
+// deviations above the mean) fit into a tile have one, larger ones leave half a tile
+// empty.
+template <int N>
+int mm16_shape(const Mm16Args &a, const Shape (&shapes)[N])
+{
+    int best = 0;
+    double least = 1e300;
+    const double per = (double)a.M / a.G;
+    for (int i = 0; i < N; ++i) {
+        const Shape &s = shapes[i];
+        const double tq = (double)((a.Q + s.bq - 1) / s.bq);
+        double tiles, steps;
+        if (a.way == MM_DW) {
+            tiles = a.G * tq * ((a.P + s.bp - 1) / s.bp);
+            steps = std::max(1.0, std::ceil(per / 64));
+        } else {
+            tiles = tq * (a.G == 1                                ? (double)((a.M + s.bp - 1) / s.bp)
+                          : per + 1.4 * std::sqrt(per) <= s.bp ? (double)std::min(a.M, a.G)
+                                                                  : (double)a.M / s.bp + 0.5 * a.G);
+            steps = std::ceil(a.C / 64.0);
+        }
+        const double t = steps * std::max(s.alone, s.busy * tiles / 256) + s.end * std::max(1.0, tiles / 256);
+        if (t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    return best;
+}
+
+// Whole pieces of 16 bytes along every row, and offsets inside a tile that fit 31
+// bits.
+bool whole_pieces(const Mm16Args &a)
+{
+    auto on16 = [](const void *p) { return ((uintptr_t)p & 15) == 0; };
+    const int esz = a.out_f32 ? 4 : 2;
+    const bool sizes = a.Q % 8 == 0 && (a.way == MM_DW ? a.P % 8 == 0 : a.C % 8 == 0);
+    return sizes && a.ldp % 8 == 0 && a.ldq % 8 == 0 && a.ldo * esz % 16 == 0 &&
+           std::max({a.ldp, a.ldq, a.ldo}) < 1 << 20 && on16(a.p) && on16(a.q) && on16(a.out) && on16(a.add);
+}
+
+}  // namespace
+
 int64_t mm16_most_tiles(const Mm16Args &a) { return mm16_tile_count(a, 16, 16); }
 
 void launch_mm16(const Mm16Args &a, hipStream_t st)
 {
-    if (mm16_tiles_ok(a))
-        return launch_mm16_tiles(a, st);
+    const bool whole = whole_pieces(a);
     if (a.way == MM_Y)
-        launch_any<MM_Y>(a, st);
+        whole ? launch_mm16_y(a, mm16_shape(a, SHAPES_Y), st) : launch_any<MM_Y>(a, st);
     else if (a.way == MM_DX)
-        launch_any<MM_DX>(a, st);
+        whole ? launch_mm16_dx(a, mm16_shape(a, SHAPES_DX), st) : launch_any<MM_DX>(a, st);
     else
-        launch_any<MM_DW>(a, st);
+        whole ? launch_mm16_dw(a, mm16_shape(a, SHAPES_DW), st) : launch_any<MM_DW>(a, st);
 }
 
 }  // namespace moe

@@ -2,13 +2,16 @@
 // of 16 bytes (the form of the products is in matmul_bf16.hip).
 //
 // A workgroup of WP x WQ waves owns BP x BQ outputs and steps through c 64 at a
-// time, with ST stages of both operands in LDS, filled by asynchronous copies.
+// time, with ST stages of both operands in LDS, filled by asynchronous copies.  Of
+// WK groups of such waves each takes every WK-th 64 of c; their sums are joined.
 // An operand with c adjacent lies there in rows of 64 c, one with p or q adjacent
 // as it comes, 64 rows of c, and is transposed by the LDS read itself
 // (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 elements and get columns of 4).
 // Pieces of 16 bytes are rotated (XOR) by their row so that the lanes of one read
 // fall on distinct banks: 2.3 cycles for a wave's 512 bytes transposed (15.8
 // unrotated), 4.1 for its 1024 bytes in rows.
+#pragma once
+
 #include <algorithm>
 #include <type_traits>
 
@@ -24,6 +27,7 @@ namespace {
 constexpr int STEP = 64;  // depth of a stage
 constexpr int DROP = (int)0x80000000;  // an offset outside every buffer: loads give 0, stores do nothing
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Buffer of the bytes from p on.
@@ -66,6 +70,17 @@ __device__ __forceinline__ void each(F &&f)
         f(Int<B>{});
         each<B + 1, E>(f);
     }
+}
+
+// Waits until at most N copies and stores of this wave are outstanding and its LDS
+// reads are done, then, unless each wave has stages of its own, for the workgroup.
+template <int N, bool ALONE>
+__device__ __forceinline__ void stage_wait()
+{
+    if constexpr (ALONE)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    else
+        dma_wait_barrier<N>();
 }
 
 // One operand's tile of XN elements by 64 c in LDS, in blocks of 16 elements whose
@@ -120,45 +135,110 @@ struct Operand {
     }
 };
 
-template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX>
+constexpr int TAB_GROUPS = 512;  // groups that the table has room for
+constexpr int TAB_BYTES = 2 * 4 * (TAB_GROUPS + 1) + 64;
+
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX, int WK>
 struct Tiling {
     static constexpr int NW = WP * WQ, MB = BP / 16 / WP, NB = BQ / 16 / WQ;
     using P = Operand<BP, WAY != MM_DW, WAY == MM_DW>;
-    using Q = Operand<BQ, WAY == MM_Y, true>;
+    using Q = Operand<BQ, WAY == MM_Y, (NB > 1)>;
     static constexpr int PI = (P::COPIES + NW - 1) / NW, QI = (Q::COPIES + NW - 1) / NW, L = PI + QI;
-    static constexpr int O_Q = (ST + EX) * P::BYTES, LDS = O_Q + ST * Q::BYTES;
+    static constexpr int O_Q = (ST + EX) * P::BYTES, RING = O_Q + ST * Q::BYTES;  // of a group
+    static constexpr int O_SUM = WK * RING, O_TAB = O_SUM + (WK - 1) * BP * BQ * 4;
+    // Row tiles by group, where there is room: a number for each of them, none for
+    // empty groups, and found in LDS.
+    static constexpr bool TAB = WAY != MM_DW && O_TAB + TAB_BYTES <= 163840;
+    static constexpr int LDS = O_TAB + (TAB ? TAB_BYTES : 0);
+    static_assert(LDS <= 163840, "LDS of one workgroup");
     static constexpr int OCC = 163840 / LDS;
-    static constexpr int NS = MB * (NB / 2) * (F32 ? 2 : 1);  // stores of a wave and tile
-    static_assert(MB * WP * 16 == BP && NB * WQ * 16 == BQ && NB % 2 == 0, "whole blocks");
+    static constexpr int NS = MB * (NB > 1 ? NB / 2 * (F32 ? 2 : 1) : 1);  // stores of a wave and tile
+    static_assert(MB * WP * 16 == BP && NB * WQ * 16 == BQ && (NB % 2 == 0 || NB == 1), "whole blocks");
     static_assert(WAY != MM_DW || MB % 2 == 0, "whole pairs");
     static_assert((ST - 1) * L + EX * PI < 64 && (ST - 2) * L + EX * PI + NS < 64, "the counter of outstanding operations holds 63");
 };
 
 // Persistent workgroups.
-template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX>
-__global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles)
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX, int WK>
+__global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_tile(Mm16Args a, int mtiles)
 {
-    using C = Tiling<WAY, F32, BP, BQ, WP, WQ, ST, EX>;
+    using C = Tiling<WAY, F32, BP, BQ, WP, WQ, ST, EX, WK>;
     using P = typename C::P;
     using Q = typename C::Q;
     constexpr int MB = C::MB, NB = C::NB, L = C::L, NS = C::NS;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % C::NW, kg = wave / C::NW;
     const int wq = w % WQ, wp = w / WQ;
-    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+    uint8_t *const ring = smem + kg * C::RING;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(ring));
+    constexpr int DEEP = WK * STEP;  // depth of a step of all groups
 
     // ---- tiles: contiguous runs per XCD, dealt in turn to its workgroups ----
     // Panels of 4 row tiles by all column tiles, so that what an XCD works on at
     // a time is about square.
     const int ntq = (a.Q + BQ - 1) / BQ;
+    int *const tab = (int *)(smem + C::O_TAB), *const ends = tab + TAB_GROUPS + 1;
+    const bool listed = C::TAB && a.offsets && a.G <= TAB_GROUPS;
+    if (listed) {
+        int *const part = ends + TAB_GROUPS + 1;  // of each wave
+        constexpr int NT = 64 * C::NW * WK;
+        int run = 0;
+        for (int g0 = 0; g0 < a.G; g0 += NT) {
+            const int g = g0 + tid;
+            int lo = 0, hi = 0;
+            if (g < a.G) {
+                lo = min(max(a.offsets[g], 0), a.M);
+                hi = max(lo, min(a.offsets[g + 1], a.M));
+            }
+            const int n = (hi - lo + BP - 1) / BP, inc = wave_scan_add(n);
+            if (lane == 63)
+                part[wave] = inc;
+            __syncthreads();
+            int before = run;
+            for (int i = 0; i < C::NW * WK; ++i) {
+                before += i < wave ? part[i] : 0;
+                run += part[i];
+            }
+            if (g < a.G) {
+                tab[g] = before + inc - n;
+                ends[g] = lo;
+                if (g == a.G - 1)
+                    ends[a.G] = hi;
+            }
+            __syncthreads();
+        }
+        mtiles = __builtin_amdgcn_readfirstlane(run);
+    }
+    // Row tile mt of the table: its group is the last one that does not begin behind it.
+    auto listed_rows = [&](int mt) {
+        int lo = 0, hi = a.G - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (__builtin_amdgcn_readfirstlane(tab[mid]) <= mt)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int row0 = __builtin_amdgcn_readfirstlane(ends[lo]) + (mt - __builtin_amdgcn_readfirstlane(tab[lo])) * BP;
+        const int end = min(uniform_load(a.offsets + lo + 1), a.M);
+        return Where{lo, row0, min(BP, end - row0), 0, 0};
+    };
     const int total = mtiles * ntq, per = (total + 7) / 8;
     const int first = ((int)blockIdx.x & 7) * per, step_q = (int)gridDim.x >> 3;
     auto find = [&](int q) {
         for (; q < per && first + q < total; q += step_q) {
             const int id = first + q, panel = id / (4 * ntq), in = id - panel * 4 * ntq;
             const int rows = min(4, mtiles - panel * 4), tq = in / rows, tp = panel * 4 + (in - tq * rows);
-            Mm16Job j = find_job<WAY, BP, BQ>(a, tp * ntq + tq);
+            Mm16Job j;
+            if constexpr (WAY == MM_DW)
+                j = mm16_dw_job<BP, BQ>(a, tp, tq);
+            else if (listed)
+                j = mm16_row_job<WAY, BQ>(a, listed_rows(tp), tq);
+            else if (a.offsets)
+                j = mm16_row_job<WAY, BQ>(a, find_rows<BP>(a.offsets, a.G, a.M, tp), tq);
+            else
+                j = mm16_row_job<WAY, BQ>(a, Where{0, tp * BP, min(BP, a.M - tp * BP), 0, 0}, tq);
             j.next = q + step_q;
             if (j.there)
                 return j;
@@ -178,7 +258,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
     int pnext = (int)blockIdx.x >> 3;
     // The next stage of P: its tile, zeros behind the last c.
     auto next_p = [&]() {
-        if (pleft > 0 && pleft >= STEP)
+        if (pleft >= DEEP)
             return;
         int ln = lane;  // hidden from the compiler, which would keep what depends on it in registers
         asm volatile("" : "+v"(ln));
@@ -189,8 +269,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
                 pnext = j.next;
             } while (j.there && j.nc == 0);
             if (j.there) {
-                gp = j.p;
-                gq_first = j.q;
+                gp = j.p + (WAY == MM_DW ? (int64_t)(kg * STEP) * a.ldp : kg * STEP);
+                gq_first = j.q + (WAY != MM_Y ? (int64_t)(kg * STEP) * a.ldq : kg * STEP);
             }
             nc = j.there ? j.nc : 1 << 30;
             nq = j.nq;
@@ -202,14 +282,14 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
                 poff[i] = s.x < j.np ? at * 2 : (uint32_t)DROP;
             }
         }
-        if (pleft < STEP)
+        if (pleft < DEEP)
 #pragma unroll
             for (int i = 0; i < C::PI; ++i)
-                if (P::piece((w * C::PI + i) % P::COPIES, ln).c >= pleft)
+                if (P::piece((w * C::PI + i) % P::COPIES, ln).c >= pleft - kg * STEP)
                     poff[i] = (uint32_t)DROP;
     };
     auto next_q = [&]() {
-        if (qleft > 0 && qleft >= STEP)
+        if (qleft >= DEEP)
             return;
         int ln = lane;
         asm volatile("" : "+v"(ln));
@@ -223,10 +303,10 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
                 qoff[i] = s.x < nq ? at * 2 : (uint32_t)DROP;
             }
         }
-        if (qleft < STEP)
+        if (qleft < DEEP)
 #pragma unroll
             for (int i = 0; i < C::QI; ++i)
-                if (Q::piece((w * C::QI + i) % Q::COPIES, ln).c >= qleft)
+                if (Q::piece((w * C::QI + i) % Q::COPIES, ln).c >= qleft - kg * STEP)
                     qoff[i] = (uint32_t)DROP;
     };
     // part J of N of a stage's copies
@@ -239,8 +319,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
             if (i * N / C::PI == J)
                 dma16_buffer(buffer_words(gp), poff[i], lds + pst + (uint32_t)((w * C::PI + i) % P::COPIES) * 1024u);
         if constexpr (J == N - 1) {
-            gp += WAY == MM_DW ? (int64_t)STEP * a.ldp : STEP;
-            pleft -= STEP;
+            gp += WAY == MM_DW ? (int64_t)DEEP * a.ldp : DEEP;
+            pleft -= DEEP;
             pst = pst + P::BYTES == C::O_Q ? 0 : pst + P::BYTES;
         }
     };
@@ -254,8 +334,8 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
                 dma16_buffer(buffer_words(gq), qoff[i],
                              lds + C::O_Q + qst + (uint32_t)((w * C::QI + i) % Q::COPIES) * 1024u);
         if constexpr (J == N - 1) {
-            gq += WAY != MM_Y ? (int64_t)STEP * a.ldq : STEP;
-            qleft -= STEP;
+            gq += WAY != MM_Y ? (int64_t)DEEP * a.ldq : DEEP;
+            qleft -= DEEP;
             qst = qst + Q::BYTES == ST * Q::BYTES ? 0 : qst + Q::BYTES;
         }
     };
@@ -289,12 +369,12 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
     static_assert(U % (D + 1) == 0 && D <= MB && (EX || ST >= 3), "the ring of rows goes on from step to step");
     bf16x8 qf[2][NB], pf[D + 1];
     uint32_t pc = 0, qc = 0;  // byte of the stage that is multiplied
-    auto load_q = [&](int c, int h) { qf[h & 1][c] = Q::read(smem + qc, qat[c], h); };
+    auto load_q = [&](int c, int h) { qf[h & 1][c] = Q::read(ring + qc, qat[c], h); };
     auto load_p = [&](auto unit) {  // unit U + u: of the next stage, which is the one multiplied by then
         constexpr int u = decltype(unit)::value;
-        pf[u % (D + 1)] = P::read(smem + pc, pat[u % MB], u / MB % 2);
+        pf[u % (D + 1)] = P::read(ring + pc, pat[u % MB], u / MB % 2);
     };
-    dma_wait_barrier<EX ? (ST - 1) * L : (ST - 2) * L + C::PI>();
+    stage_wait<EX ? (ST - 1) * L : (ST - 2) * L + C::PI, C::NW == 1>();
 #pragma unroll
     for (int c = 0; c < NB; ++c)
         load_q(c, 0);
@@ -327,7 +407,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
 #pragma unroll
             for (int m = 0; m < MB; ++m)
                 acc[c][m] = floatx4{0, 0, 0, 0};
-        const int n = (cur.nc + STEP - 1) / STEP;
+        const int n = (cur.nc + DEEP - 1) / DEEP;
         for (int s = 0; s < n; ++s) {
             each<0, U>([&](auto unit) {
                 constexpr int u = decltype(unit)::value;
@@ -340,9 +420,9 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
                 if constexpr (u == U - D) {
                     // older than what may be under way: the next stage
                     if (s + 2 - EX < ST && stored)
-                        dma_wait_barrier<(ST - 2) * L + EX * C::PI + NS>();
+                        stage_wait<(ST - 2) * L + EX * C::PI + NS, C::NW == 1>();
                     else
-                        dma_wait_barrier<(ST - 2) * L + EX * C::PI>();
+                        stage_wait<(ST - 2) * L + EX * C::PI, C::NW == 1>();
                     pc = pc + P::BYTES == C::O_Q ? 0 : pc + P::BYTES;
                     qc = qc + Q::BYTES == ST * Q::BYTES ? 0 : qc + Q::BYTES;
                 }
@@ -361,6 +441,29 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
             });
         }
         mfma_acc_drain();
+        if constexpr (WK > 1) {
+            // the groups' sums, joined in their order by the first one
+            if (n > 0) {
+                if (C::NW == 1)
+                    lds_barrier();  // the first group has read the tile before
+                floatx4 *sum = (floatx4 *)(smem + C::O_SUM) + w * (NB * MB * 64) + lane;
+                if (kg > 0)
+#pragma unroll
+                    for (int c = 0; c < NB; ++c)
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+                            sum[((kg - 1) * C::NW * NB * MB + c * MB + m) * 64] = acc[c][m];
+                lds_barrier();
+                if (kg == 0)
+#pragma unroll
+                    for (int g = 0; g < WK - 1; ++g)
+#pragma unroll
+                        for (int c = 0; c < NB; ++c)
+#pragma unroll
+                            for (int m = 0; m < MB; ++m)
+                                acc[c][m] += sum[(g * C::NW * NB * MB + c * MB + m) * 64];
+            }
+        }
         const Mm16Job next = find(cur.next);
         __builtin_amdgcn_sched_barrier(0);
 
@@ -373,11 +476,33 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
         const auto ro = out_rsrc((const char *)a.out + cur.out * esz);
         const auto ra = out_rsrc((const char *)(a.add ? a.add : a.out) + cur.out * esz);
         const int pitch = (int)a.ldo * esz;
+        if constexpr (NB == 1) {  // 4 adjacent columns of a row
+            if (kg == 0)
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const int p = wp * (16 * MB) + m * 16 + e16, q = wq * 16 + eg * 4;
+                    const int at = p < cur.np && q < cur.nq ? p * pitch + q * esz : DROP;
+                    floatx4 v = acc[0][m];
+                    if constexpr (F32) {
+                        if (a.add)
+                            v += __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(ra, at, 0, 0));
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ro, at, 0, 0);
+                    } else {
+                        if (a.add) {
+                            const u32x2 d = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, at, 0, 0));
+                            v += floatx4{__uint_as_float(d[0] << 16), __uint_as_float(d[0] & 0xFFFF0000u),
+                                         __uint_as_float(d[1] << 16), __uint_as_float(d[1] & 0xFFFF0000u)};
+                        }
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3])}, ro, at,
+                                                              0, 0);
+                    }
+                }
+        } else if (kg == 0)
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int p = wp * (16 * MB) + (WAY == MM_DW ? paired(m, e16) : m * 16 + e16);
-            int at[NB / 2];
-            u32x4 add[NB / 2][V];
+            int at[(NB + 1) / 2];
+            u32x4 add[(NB + 1) / 2][V];
 #pragma unroll
             for (int c = 0; c < NB / 2; ++c) {
                 const int q = wq * (16 * NB) + c * 32 + eg * 8;
@@ -417,55 +542,49 @@ __global__ __launch_bounds__(64 * WP * WQ) void mm16_tile(Mm16Args a, int mtiles
         }
         __builtin_amdgcn_sched_barrier(0);
         if (!next.there) {
-            dma_wait_barrier<0>();  // no copy outlives the workgroup
+            stage_wait<0, true>();  // no copy outlives the workgroup
             break;
         }
         cur = next;
-        stored = true;
+        stored = kg == 0;
     }
 }
 
-template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX>
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX, int WK>
 void launch_tiling(const Mm16Args &a, hipStream_t st)
 {
-    using C = Tiling<WAY, F32, BP, BQ, WP, WQ, ST, EX>;
+    using C = Tiling<WAY, F32, BP, BQ, WP, WQ, ST, EX, WK>;
     const int64_t tiles = mm16_tile_count(a, BP, BQ);
     const int ntq = (a.Q + BQ - 1) / BQ;
     const unsigned grid = (unsigned)(std::min<int64_t>(tiles, 256 * C::OCC) + 7) / 8 * 8;
-    mm16_tile<WAY, F32, BP, BQ, WP, WQ, ST, EX><<<grid, 64 * C::NW, 0, st>>>(a, (int)(tiles / ntq));
-}
-
-template <int WAY, bool F32>
-void launch_way(const Mm16Args &a, hipStream_t st)
-{
-    launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1>(a, st);
+    mm16_tile<WAY, F32, BP, BQ, WP, WQ, ST, EX, WK><<<grid, 64 * C::NW * WK, 0, st>>>(a, (int)(tiles / ntq));
 }
 
 }  // namespace
 
-// Whole pieces of 16 bytes along every row, and offsets inside a tile that fit 31
-// bits.
-bool mm16_tiles_ok(const Mm16Args &a)
+// The tiles of mm16_shape() by their number.
+template <int WAY, bool F32>
+void launch_shape(const Mm16Args &a, int shape, hipStream_t st)
 {
-    auto on16 = [](const void *p) { return ((uintptr_t)p & 15) == 0; };
-    const int esz = a.out_f32 ? 4 : 2;
-    const bool sizes = a.Q % 8 == 0 && (a.way == MM_DW ? a.P % 8 == 0 : a.C % 8 == 0);
-    return sizes && a.ldp % 8 == 0 && a.ldq % 8 == 0 && a.ldo * esz % 16 == 0 && std::max({a.ldp, a.ldq, a.ldo}) < 1 << 20 &&
-           on16(a.p) && on16(a.q) && on16(a.out) && on16(a.add);
-}
-
-void launch_mm16_tiles(const Mm16Args &a, hipStream_t st)
-{
-    auto typed = [&](auto way) {
-        constexpr int WAY = decltype(way)::value;
-        a.out_f32 ? launch_way<WAY, true>(a, st) : launch_way<WAY, false>(a, st);
-    };
-    if (a.way == MM_Y)
-        typed(std::integral_constant<int, MM_Y>{});
-    else if (a.way == MM_DX)
-        typed(std::integral_constant<int, MM_DX>{});
-    else
-        typed(std::integral_constant<int, MM_DW>{});
+    if constexpr (WAY == MM_DW) {
+        switch (shape) {
+        case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
+        case 1: launch_tiling<WAY, F32, 128, 128, 2, 2, 2, 1, 1>(a, st); break;
+        default: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 1>(a, st); break;
+        }
+    } else {
+        switch (shape) {
+        case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
+        case 1: launch_tiling<WAY, F32, 128, 256, 2, 4, 3, 0, 1>(a, st); break;
+        case 2: launch_tiling<WAY, F32, 64, 256, 2, 4, 3, 0, 1>(a, st); break;
+        case 3: launch_tiling<WAY, F32, 64, 128, 2, 2, 3, 0, 1>(a, st); break;
+        case 4: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
+        case 5: launch_tiling<WAY, F32, 16, 64, 1, 2, 3, 0, 4>(a, st); break;
+        default:
+            if constexpr (WAY == MM_Y)
+                launch_tiling<WAY, F32, 16, 16, 1, 1, 4, 0, 4>(a, st);
+        }
+    }
 }
 
 }  // namespace moe

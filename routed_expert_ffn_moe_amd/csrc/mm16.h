@@ -7,49 +7,50 @@
 
 namespace moe {
 
-// What a tile multiplies (kernels.h says what P, Q and c are): P rows p0 .. p0 + np - 1 against Q rows from q0, over c.
+// What a tile multiplies (kernels.h says what P, Q and c are): np rows of P against nq of Q,
+// over nc of c, all from where p and q point.
 struct Mm16Job {
     const uint16_t *p, *q;
     int64_t out;      // element of the tile's first row
-    int np, nq, nc, p0, q0;
+    int np, nq, nc;
     bool there;
     int next;         // where the workgroup goes on
 };
 
-// Tile `id`; the tiles of neighbouring numbers share their group.
-template <int WAY, int BP, int BQ>
-__device__ __forceinline__ Mm16Job find_job(const Mm16Args &a, int id)
+// Rows t of a group against column tile tq (y, dx); the weights' c are adjacent in y.
+template <int WAY, int BQ>
+__device__ __forceinline__ Mm16Job mm16_row_job(const Mm16Args &a, Where t, int tq)
 {
     Mm16Job j{};
-    const int ntq = (a.Q + BQ - 1) / BQ, tp = id / ntq, q0 = (id - tp * ntq) * BQ;
-    j.q0 = q0;
+    const int q0 = tq * BQ;
+    j.there = t.g >= 0;
+    j.np = t.nrows;
     j.nq = min(BQ, a.Q - q0);
-    if constexpr (WAY == MM_DW) {
-        const int ntp = (a.P + BP - 1) / BP, g = tp / ntp;
-        int lo = 0, hi = a.M;
-        if (a.offsets) {
-            lo = min(max(uniform_load(a.offsets + g), 0), a.M);
-            hi = min(uniform_load(a.offsets + g + 1), a.M);
-        }
-        j.p0 = (tp - g * ntp) * BP;
-        j.np = min(BP, a.P - j.p0);
-        j.nc = max(hi - lo, 0);
-        j.p = a.p + (int64_t)lo * a.ldp + j.p0;
-        j.q = a.q + (int64_t)lo * a.ldq + q0;
-        j.out = (int64_t)g * a.ostride + (int64_t)j.p0 * a.ldo + q0;
-        j.there = true;
-    } else {
-        Where t{0, tp * BP, min(BP, a.M - tp * BP), 0, 0};
-        if (a.offsets)
-            t = find_rows<BP>(a.offsets, a.G, a.M, tp);
-        j.there = t.g >= 0;
-        j.p0 = t.row0;
-        j.np = t.nrows;
-        j.nc = a.C;
-        j.p = a.p + (int64_t)t.row0 * a.ldp;
-        j.q = a.q + (int64_t)t.g * a.qstride + (WAY == MM_DX ? (int64_t)q0 : (int64_t)q0 * a.ldq);
-        j.out = (int64_t)t.row0 * a.ldo + q0;
+    j.nc = a.C;
+    j.p = a.p + (int64_t)t.row0 * a.ldp;
+    j.q = a.q + (int64_t)t.g * a.qstride + (WAY == MM_DX ? (int64_t)q0 : (int64_t)q0 * a.ldq);
+    j.out = (int64_t)t.row0 * a.ldo + q0;
+    return j;
+}
+
+// Tile (tp, tq) of the matrices dw, whose row tiles are numbered on from group to group.
+template <int BP, int BQ>
+__device__ __forceinline__ Mm16Job mm16_dw_job(const Mm16Args &a, int tp, int tq)
+{
+    Mm16Job j{};
+    const int ntp = (a.P + BP - 1) / BP, g = tp / ntp, p0 = (tp - g * ntp) * BP, q0 = tq * BQ;
+    int lo = 0, hi = a.M;
+    if (a.offsets) {
+        lo = min(max(uniform_load(a.offsets + g), 0), a.M);
+        hi = min(uniform_load(a.offsets + g + 1), a.M);
     }
+    j.there = true;
+    j.np = min(BP, a.P - p0);
+    j.nq = min(BQ, a.Q - q0);
+    j.nc = max(hi - lo, 0);
+    j.p = a.p + (int64_t)lo * a.ldp + p0;
+    j.q = a.q + (int64_t)lo * a.ldq + q0;
+    j.out = (int64_t)g * a.ostride + (int64_t)p0 * a.ldo + q0;
     return j;
 }
 
