@@ -24,12 +24,12 @@ namespace {
 
 // ---- the order --------------------------------------------------------------
 
-// Passes of at most this many pairs are sorted by counting in every workgroup
-// of the launch that also copies the rows.
+// Passes of at most this many pairs are sorted by comparing all pairs in every
+// workgroup of the launch that also copies the rows.
 constexpr int TINY_PAIRS = 128;
-// Most blocks of pairs that each placing workgroup counts by itself; that work
-// grows with the square of their number.
-constexpr int COUNT_BLOCKS = 16;
+// Most blocks of pairs that each placing workgroup counts by itself, and whose
+// histograms it sums by itself; that work grows with the square of their number.
+constexpr int COUNT_BLOCKS = 4, SUM_BLOCKS = 64;
 
 // Pairs of a block: whole tokens, at most 1024.
 int block_pairs(int k) { return 1024 / k * k; }
@@ -89,9 +89,11 @@ __global__ __launch_bounds__(1024) void sort_prefix(SortArgs a, int nblk)
 // the expert's offset (prefix over the experts' totals) plus the expert's pairs
 // in earlier blocks; inside the block the waves follow in order, and a wave's
 // lanes of one expert are ranked by a mask that ballots on the expert's bits
-// build.  COUNT: totals and earlier blocks' pairs are counted here, from all
-// pairs; else they come from blk.
-template <bool COUNT>
+// build.  Totals and earlier blocks' pairs are counted here from all pairs (COUNT),
+// summed here over the blocks' histograms (SUM), or come from sort_prefix.
+enum { COUNT = 0, SUM = 1, PREFIX = 2 };
+
+template <int FROM>
 __global__ __launch_bounds__(1024) void sort_place(SortArgs a, int n, int per, int nblk)
 {
     __shared__ int32_t s_start[1024];
@@ -102,9 +104,9 @@ __global__ __launch_bounds__(1024) void sort_place(SortArgs a, int n, int per, i
     const bool mine = tid < per && p < n;
     const int e = mine ? expert_of(a.idx, p, n, a.E) : -1;
     int total = 0, before = 0;
-    if constexpr (COUNT) {
-        __shared__ int32_t s_total[1024], s_before[1024];
-        s_total[tid] = s_before[tid] = 0;
+    if constexpr (FROM == COUNT) {
+        __shared__ int32_t s_before[1024], s_rest[1024];
+        s_before[tid] = s_rest[tid] = 0;
         __syncthreads();
         int ev[COUNT_BLOCKS];  // all reads in flight together
 #pragma unroll
@@ -112,17 +114,29 @@ __global__ __launch_bounds__(1024) void sort_place(SortArgs a, int n, int per, i
             ev[i] = tid < per ? expert_of(a.idx, i * per + tid, n, a.E) : -1;
 #pragma unroll
         for (int i = 0; i < COUNT_BLOCKS; ++i)
-            if (ev[i] >= 0) {
-                atomicAdd(&s_total[ev[i]], 1);
-                if (i < b)
-                    atomicAdd(&s_before[ev[i]], 1);
-            }
+            if (ev[i] >= 0)
+                atomicAdd(i < b ? &s_before[ev[i]] : &s_rest[ev[i]], 1);  // integer counts: order-free
         __syncthreads();
-        total = s_total[tid];
         before = s_before[tid];
+        total = before + s_rest[tid];
     } else if (tid < a.E) {
-        total = a.blk[(int64_t)nblk * a.E + tid];
-        before = a.blk[(int64_t)b * a.E + tid];
+        if constexpr (FROM == SUM) {
+            constexpr int AT = 16;
+            for (int b0 = 0; b0 < nblk; b0 += AT) {
+                int c[AT];
+#pragma unroll
+                for (int i = 0; i < AT; ++i)  // all reads in flight together
+                    c[i] = b0 + i < nblk ? a.blk[(int64_t)(b0 + i) * a.E + tid] : 0;
+#pragma unroll
+                for (int i = 0; i < AT; ++i) {
+                    total += c[i];
+                    before += b0 + i < b ? c[i] : 0;
+                }
+            }
+        } else {
+            total = a.blk[(int64_t)nblk * a.E + tid];
+            before = a.blk[(int64_t)b * a.E + tid];
+        }
     }
 #pragma unroll
     for (int w = 0; w < 16; ++w)
@@ -243,13 +257,17 @@ __device__ __forceinline__ void store_one(float v, void *p, int64_t at)
         ((uint16_t *)p)[at] = (uint16_t)cvt_bf2(v, 0.0f);
 }
 
+// First column of the 8 from c on, moved back to where 8 are inside the row (there
+// are 8 at least): those in front of c are handled twice, with the same results.
+__device__ __forceinline__ int inside(int c, int H) { return min(c, H - 8); }
+
 // Columns c .. c + 7 of token t of x to the rows place(0) .. place(k - 1), those
 // of them that are rows.
 template <int SRC, bool F32, class Place>
 __device__ __forceinline__ void gather_columns(const GatherArgs &a, int64_t t, int c, Place place)
 {
     Raw8<F32> v;
-    const int left = a.H - c;
+    int left = a.H - c;
     if constexpr (SRC == GATHER_FP8) {
         const uint2 u = *(const uint2 *)((const uint8_t *)a.x + t * a.ldx + c);  // whole blocks: no tail
         const float f = a.sx[t * ((a.H + FP8_BLOCK - 1) / FP8_BLOCK) + c / FP8_BLOCK];
@@ -262,7 +280,9 @@ __device__ __forceinline__ void gather_columns(const GatherArgs &a, int64_t t, i
             x[2 * i + 1] = two[1] * f;
         }
         v = make_raw<F32>(x);
-    } else if (left >= 8) {
+    } else if (a.H >= 8) {
+        c = inside(c, a.H);
+        left = 8;
         v = load_raw<F32>(a.x, t * a.ldx + c);
     } else {  // the bits of what there is
 #pragma unroll
@@ -299,30 +319,38 @@ __device__ __forceinline__ void gather_columns(const GatherArgs &a, int64_t t, i
 template <int SRC, bool F32>
 __global__ __launch_bounds__(256) void dispatch_tiny(SortArgs s, GatherArgs a)
 {
-    __shared__ int s_e[TINY_PAIRS], s_at[TINY_PAIRS];
-    const int n = s.T * s.k, tid = threadIdx.x;
-    if (tid < n) {
-        const int e = expert_of(s.idx, tid, n, s.E);
-        s_e[tid] = e < 0 ? s.E : e;  // empty slots behind all others
+    __shared__ __attribute__((aligned(16))) int s_e[TINY_PAIRS];
+    __shared__ int s_at[TINY_PAIRS];
+    const int n = s.T * s.k, n4 = (n + 3) & ~3, tid = threadIdx.x;
+    for (int p = tid; p < n4; p += 256) {
+        const int e = expert_of(s.idx, p, n, s.E);
+        s_e[p] = e < 0 ? s.E : e;  // empty slots (and what fills up a word) behind all others
     }
     __syncthreads();
-    if (tid < n) {
-        const int e = s_e[tid];
+    for (int p = tid; p < n; p += 256) {
+        const int e = s_e[p];
         int at = 0;
-        for (int q = 0; q < n; ++q)
-            at += s_e[q] < e || (s_e[q] == e && q < tid) ? 1 : 0;
-        s_at[tid] = at = e < s.E ? at : -1;
+#pragma unroll 8
+        for (int q = 0; q < n4; q += 4) {
+            const int4 o = *(const int4 *)(s_e + q);
+            at += (o.x < e || (o.x == e && q < p)) + (o.y < e || (o.y == e && q + 1 < p)) +
+                  (o.z < e || (o.z == e && q + 2 < p)) + (o.w < e || (o.w == e && q + 3 < p));
+        }
+        s_at[p] = at = e < s.E ? at : -1;
         if (blockIdx.x == 0) {
-            s.row_of[tid] = at;
+            s.row_of[p] = at;
             if (s.row_src && at >= 0)
-                s.row_src[at] = tid;
+                s.row_src[at] = p;
         }
     }
     if (blockIdx.x == 0)
         for (int e = tid; e <= s.E; e += 256) {
             int before = 0;
-            for (int q = 0; q < n; ++q)
-                before += s_e[q] < e ? 1 : 0;
+#pragma unroll 8
+            for (int q = 0; q < n4; q += 4) {
+                const int4 o = *(const int4 *)(s_e + q);
+                before += (o.x < e) + (o.y < e) + (o.z < e) + (o.w < e);
+            }
             s.offsets[e] = before;
         }
     if (!a.x)
@@ -362,6 +390,17 @@ __device__ __forceinline__ void load_slots(const CombineRowsArgs &a, int64_t t, 
         row[j] = (unsigned)row[j] < (unsigned)a.R ? row[j] : -1;
 }
 
+// Columns c .. c + 7 of the slots' rows, all reads in flight together: an empty
+// slot reads the first row, which is not used (R > 0).
+template <int KM, bool F32>
+__device__ __forceinline__ void load_rows(const CombineRowsArgs &a, const int (&row)[KM], int c, Raw8<F32> (&v)[KM])
+{
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+        if (j < a.k)
+            v[j] = load_raw<F32>(a.rows, (int64_t)max(row[j], 0) * a.ldr + c);
+}
+
 template <int KM, bool F32>
 __global__ __launch_bounds__(256) void combine_rows(CombineRowsArgs a, int shift)
 {
@@ -371,33 +410,52 @@ __global__ __launch_bounds__(256) void combine_rows(CombineRowsArgs a, int shift
         int row[KM];
         float w[KM];
         load_slots<KM>(a, t, row, w);
-        for (int c = sub * 8; c < a.H; c += 8 << shift) {
+        for (int c0 = sub * 8; c0 < a.H; c0 += 8 << shift) {
             float acc[8] = {};
-            if (c + 8 <= a.H) {
-                Raw8<F32> v[KM];
+            if (a.H >= 8) {
+                const int c = inside(c0, a.H);
+                if (a.R > 0) {
+                    Raw8<F32> v[KM];
+                    load_rows<KM, F32>(a, row, c, v);
 #pragma unroll
-                for (int j = 0; j < KM; ++j)  // all reads in flight together
-                    if (row[j] >= 0)
-                        v[j] = load_raw<F32>(a.rows, (int64_t)row[j] * a.ldr + c);
+                    for (int j = 0; j < KM; ++j)
+                        if (j < a.k && row[j] >= 0)
 #pragma unroll
-                for (int j = 0; j < KM; ++j)
-                    if (row[j] >= 0)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            acc[i] = fmaf(w[j], elem(v[j], i), acc[i]);
+                            for (int i = 0; i < 8; ++i)
+                                acc[i] = fmaf(w[j], elem(v[j], i), acc[i]);
+                }
                 store_raw(make_raw<F32>(acc), a.y, t * a.ldy + c);
             } else {
-                for (int i = 0; c + i < a.H; ++i) {
+                for (int i = 0; i < a.H; ++i) {
                     float s = 0.0f;
 #pragma unroll
                     for (int j = 0; j < KM; ++j)
                         if (row[j] >= 0)
-                            s = fmaf(w[j], load_one<F32>(a.rows, (int64_t)row[j] * a.ldr + c + i), s);
-                    store_one<F32>(s, a.y, t * a.ldy + c + i);
+                            s = fmaf(w[j], load_one<F32>(a.rows, (int64_t)row[j] * a.ldr + i), s);
+                    store_one<F32>(s, a.y, t * a.ldy + i);
                 }
             }
         }
     }
+}
+
+// Sum over each 1 << shift lanes (16, 32 or 64), in the last of them.
+__device__ __forceinline__ float lanes_sum(float v, int shift)
+{
+    auto add = [&](auto ctrl, auto rows) {
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
+                                                        decltype(rows)::value, 0xf, false));
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    if (shift > 4)
+        add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+    if (shift > 5)
+        add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+    return v;
 }
 
 template <int KM, bool F32>
@@ -414,26 +472,24 @@ __global__ __launch_bounds__(256) void combine_rows_grad(CombineRowsArgs a, int 
         float w[KM], dot[KM] = {};
         if (there) {
             load_slots<KM>(a, t, row, w);
-            for (int c = sub * 8; c < a.H; c += 8 << shift) {
-                if (c + 8 <= a.H) {
+            for (int c0 = sub * 8; c0 < a.H; c0 += 8 << shift) {
+                if (a.H >= 8) {
+                    const int c = inside(c0, a.H);
                     const Raw8<F32> d = load_raw<F32>(a.dy, t * a.ldy + c);
-                    if (a.dw) {
+                    if (a.dw && a.R > 0) {
                         Raw8<F32> v[KM];
+                        load_rows<KM, F32>(a, row, c, v);
 #pragma unroll
                         for (int j = 0; j < KM; ++j)
-                            if (row[j] >= 0)
-                                v[j] = load_raw<F32>(a.rows, (int64_t)row[j] * a.ldr + c);
+                            if (j < a.k && row[j] >= 0)
 #pragma unroll
-                        for (int j = 0; j < KM; ++j)
-                            if (row[j] >= 0)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    dot[j] = fmaf(elem(d, i), elem(v[j], i), dot[j]);
+                                for (int i = 0; i < 8; ++i)  // those in front of c0 are another thread's
+                                    dot[j] = c + i < c0 ? dot[j] : fmaf(elem(d, i), elem(v[j], i), dot[j]);
                     }
                     if (a.drows)
 #pragma unroll
                         for (int j = 0; j < KM; ++j)
-                            if (row[j] >= 0) {
+                            if (j < a.k && row[j] >= 0) {
                                 float f[8];
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
@@ -441,12 +497,12 @@ __global__ __launch_bounds__(256) void combine_rows_grad(CombineRowsArgs a, int 
                                 store_raw(make_raw<F32>(f), a.drows, (int64_t)row[j] * a.ldr + c);
                             }
                 } else {
-                    for (int i = 0; c + i < a.H; ++i) {
-                        const float d = load_one<F32>(a.dy, t * a.ldy + c + i);
+                    for (int i = 0; i < a.H; ++i) {
+                        const float d = load_one<F32>(a.dy, t * a.ldy + i);
 #pragma unroll
                         for (int j = 0; j < KM; ++j)
                             if (row[j] >= 0) {
-                                const int64_t at = (int64_t)row[j] * a.ldr + c + i;
+                                const int64_t at = (int64_t)row[j] * a.ldr + i;
                                 if (a.dw)
                                     dot[j] = fmaf(d, load_one<F32>(a.rows, at), dot[j]);
                                 if (a.drows)
@@ -458,13 +514,12 @@ __global__ __launch_bounds__(256) void combine_rows_grad(CombineRowsArgs a, int 
         }
         if (!a.dw)
             continue;
-        const int span = min(64, 1 << shift);
 #pragma unroll
         for (int j = 0; j < KM; ++j)
-            for (int d = 1; d < span; d <<= 1)
-                dot[j] += __shfl_xor(dot[j], d);
+            if (j < a.k)
+                dot[j] = lanes_sum(dot[j], shift);
         if (shift > 6) {  // a token over several waves
-            if (lane == 0)
+            if (lane == 63)
 #pragma unroll
                 for (int j = 0; j < KM; ++j)
                     s_dot[wv][j] = dot[j];
@@ -476,10 +531,10 @@ __global__ __launch_bounds__(256) void combine_rows_grad(CombineRowsArgs a, int 
                 a.dw[t * a.k + sub] = s;
             }
             __syncthreads();
-        } else if (there) {
+        } else if (there && sub == (1 << shift) - 1) {
 #pragma unroll
             for (int j = 0; j < KM; ++j)
-                if (sub == j && j < a.k)
+                if (j < a.k)
                     a.dw[t * a.k + j] = dot[j];
         }
     }
@@ -517,10 +572,16 @@ template <class Run>
 void with_slots(const CombineRowsArgs &a, Run run)
 {
     auto typed = [&](auto km) { a.f32 ? run(km, std::true_type{}) : run(km, std::false_type{}); };
-    if (a.k <= 4)
+    if (a.k <= 2)
+        typed(std::integral_constant<int, 2>{});
+    else if (a.k <= 4)
         typed(std::integral_constant<int, 4>{});
+    else if (a.k <= 6)
+        typed(std::integral_constant<int, 6>{});
     else if (a.k <= 8)
         typed(std::integral_constant<int, 8>{});
+    else if (a.k <= 12)
+        typed(std::integral_constant<int, 12>{});
     else
         typed(std::integral_constant<int, 16>{});
 }
@@ -556,11 +617,15 @@ void launch_dispatch(const SortArgs &s, const GatherArgs &a, hipStream_t st)
     }
     const int per = block_pairs(s.k), nblk = (n + per - 1) / per;
     if (nblk <= COUNT_BLOCKS) {
-        sort_place<true><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+        sort_place<COUNT><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
     } else {
         sort_hist<<<nblk, 1024, 0, st>>>(s, n, per);
-        sort_prefix<<<(s.E + 63) / 64, 1024, 0, st>>>(s, nblk);
-        sort_place<false><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+        if (nblk <= SUM_BLOCKS) {
+            sort_place<SUM><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+        } else {
+            sort_prefix<<<(s.E + 63) / 64, 1024, 0, st>>>(s, nblk);
+            sort_place<PREFIX><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+        }
     }
     if (a.x)
         launch_gather(a, st);

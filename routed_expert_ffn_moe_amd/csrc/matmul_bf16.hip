@@ -11,6 +11,7 @@
 // Sums in fp32, the addend joined in fp32, rounded once.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.h"
 #include "fp8.h"
@@ -22,128 +23,201 @@ namespace moe {
 
 namespace {
 
-template <bool F32>
-__device__ __forceinline__ void put(const Mm16Args &a, int64_t at, float v)
-{
-    if constexpr (F32) {
-        if (a.add)
-            v += ((const float *)a.add)[at];
-        ((float *)a.out)[at] = v;
-    } else {
-        if (a.add)
-            v += bf2f(((const uint16_t *)a.add)[at]);
-        ((uint16_t *)a.out)[at] = (uint16_t)cvt_bf2(v, 0.0f);
-    }
-}
-
 // ---- any strides and alignment ----------------------------------------------
 
-// 64 x 64 tiles, 32 deep, through registers to LDS, where both operands lie with
-// c adjacent.  Elements outside the operands are 0.
-constexpr int ANY_T = 64, ANY_C = 32, ANY_LD = ANY_C + 8;
+// The tiles of mm16.h, staged through registers a step ahead: pieces of 8 elements
+// are read at any element's address, and one by one where they end outside the
+// operand (0 there).  Two stages in LDS, so that a step has one barrier.
 
-// Eight elements of an operand: along c of row `r` (c adjacent), or along the
-// rows from `r` at depth c.
+// Elements of a piece: along c of element x (c adjacent), or elements from x on at c.
 template <bool ADJ>
-__device__ __forceinline__ u16x8 any_load(const uint16_t *base, int64_t ld, int r, int c, int nr, int nc)
+__device__ __forceinline__ words4 fetch(const uint16_t *base, int64_t ld, int x, int c, int nx, int nc)
 {
-    u16x8 v{0, 0, 0, 0, 0, 0, 0, 0};
-    const int lim = ADJ ? nc - c : nr - r;
-    if (ADJ ? r >= nr : c >= nc)
+    words4 v{0, 0, 0, 0};
+    const int lim = ADJ ? nc - c : nx - x;
+    if (lim <= 0 || (ADJ ? x >= nx : c >= nc))
         return v;
-    const uint16_t *s = base + (ADJ ? (int64_t)r * ld + c : (int64_t)c * ld + r);
-    if (lim >= 8) {
-        const words4 w = *(const words4 *)s;
-        return __builtin_bit_cast(u16x8, w);
-    }
+    const uint16_t *s = base + (ADJ ? (int64_t)x * ld + c : (int64_t)c * ld + x);
+    if (lim >= 8)
+        return *(const words4 *)s;
 #pragma unroll
     for (int i = 0; i < 7; ++i)
         if (i < lim)
-            v[i] = s[i];
+            v[i >> 1] |= (uint32_t)s[i] << (i & 1) * 16;
     return v;
 }
 
-template <bool ADJ>
-__device__ __forceinline__ void any_store(uint16_t *s, int r, int c, u16x8 v)
+// 8 adjacent results, `left` of them inside the output.
+template <bool F32>
+__device__ __forceinline__ void put8(const Mm16Args &a, int64_t at, float (&v)[8], int left)
 {
-    if constexpr (ADJ) {
-        *(u16x8 *)(s + r * ANY_LD + c) = v;
-    } else {
+    if (left >= 8) {
+        if (a.add) {
+            float d[8];
+            load8<!F32, true>(d, a.add, at, 0, 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s[(r + i) * ANY_LD + c] = v[i];
+            for (int i = 0; i < 8; ++i)
+                v[i] += d[i];
+        }
+        if constexpr (F32) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *(words4 *)((float *)a.out + at + 4 * q) =
+                    words4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                           __float_as_uint(v[4 * q + 3])};
+        } else {
+            *(words4 *)((uint16_t *)a.out + at) =
+                words4{cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7])};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        if (i >= left)
+            continue;
+        if constexpr (F32)
+            ((float *)a.out)[at + i] = v[i] + (a.add ? ((const float *)a.add)[at + i] : 0.0f);
+        else
+            ((uint16_t *)a.out)[at + i] =
+                (uint16_t)cvt_bf2(v[i] + (a.add ? bf2f(((const uint16_t *)a.add)[at + i]) : 0.0f), 0.0f);
     }
 }
 
-template <int WAY, bool F32>
-__global__ __launch_bounds__(256) void mm16_any(Mm16Args a, int tiles)
+// WP x WQ waves a tile, and WK groups of them that take every WK-th 64 of c.
+template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int WK>
+__global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_any(Mm16Args a, int tiles)
 {
     constexpr bool PA = WAY != MM_DW, QA = WAY == MM_Y;
-    __shared__ __attribute__((aligned(16))) uint16_t sp[ANY_T * ANY_LD], sq[ANY_T * ANY_LD];
-    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4, w = tid >> 6;
-    const int wp = (w & 1) * 32, wq = (w >> 1) * 32;
-    // the thread's eight elements of each operand's step
-    const int pr = PA ? tid >> 2 : (tid & 7) * 8, pc = PA ? (tid & 3) * 8 : tid >> 3;
-    const int qr = QA ? tid >> 2 : (tid & 7) * 8, qc = QA ? (tid & 3) * 8 : tid >> 3;
+    constexpr int NW = WP * WQ, MB = BP / 16 / WP, NB = BQ / 16 / WQ;
+    using P = Operand<BP, PA, !PA>;
+    using Q = Operand<BQ, QA, true>;
+    constexpr int PI = P::COPIES / NW, QI = Q::COPIES / NW, STAGE = P::BYTES + Q::BYTES;
+    static_assert(P::COPIES % NW == 0 && Q::COPIES % NW == 0 && NB % 2 == 0 && (PA || MB % 2 == 0), "whole shares");
+    static_assert((WK - 1) * BP * BQ * 4 <= 2 * WK * STAGE, "the sums fit the stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * WK * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % NW, kg = wave / NW;
+    const int wq = w % WQ, wp = w / WQ;
+    uint8_t *const ring = smem + kg * 2 * STAGE;
     for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
-        const int ntq = (a.Q + ANY_T - 1) / ANY_T, tp = id / ntq, tq = id - tp * ntq;
+        const int ntq = (a.Q + BQ - 1) / BQ, tp = id / ntq, tq = id - tp * ntq;
         Mm16Job j;
         if constexpr (WAY == MM_DW) {
-            j = mm16_dw_job<ANY_T, ANY_T>(a, tp, tq);
+            j = mm16_dw_job<BP, BQ>(a, tp, tq);
         } else {
-            Where t{0, tp * ANY_T, min(ANY_T, a.M - tp * ANY_T), 0, 0};
+            Where t{0, tp * BP, min(BP, a.M - tp * BP), 0, 0};
             if (a.offsets)
-                t = find_rows<ANY_T>(a.offsets, a.G, a.M, tp);
-            j = mm16_row_job<WAY, ANY_T>(a, t, tq);
+                t = find_rows<BP>(a.offsets, a.G, a.M, tp);
+            j = mm16_row_job<WAY, BQ>(a, t, tq);
         }
         if (!j.there)
             continue;
-        floatx4 acc[2][2] = {};
-        u16x8 vp = any_load<PA>(j.p, a.ldp, pr, pc, j.np, j.nc);
-        u16x8 vq = any_load<QA>(j.q, a.ldq, qr, qc, j.nq, j.nc);
-        for (int c = 0; c < j.nc; c += ANY_C) {
-            __syncthreads();
-            any_store<PA>(sp, pr, pc, vp);
-            any_store<QA>(sq, qr, qc, vq);
-            __syncthreads();
-            if (c + ANY_C < j.nc) {
-                vp = any_load<PA>(j.p, a.ldp, pr, c + ANY_C + pc, j.np, j.nc);
-                vq = any_load<QA>(j.q, a.ldq, qr, c + ANY_C + qc, j.nq, j.nc);
-            }
-            bf16x8 fp[2], fq[2];
+        floatx4 acc[NB][MB];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fp[i] = *(const bf16x8 *)(sp + (wp + i * 16 + l16) * ANY_LD + lg * 8);
-                fq[i] = *(const bf16x8 *)(sq + (wq + i * 16 + l16) * ANY_LD + lg * 8);
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                acc[c][m] = floatx4{0, 0, 0, 0};
+        words4 vp[PI], vq[QI];
+        auto load = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < PI; ++i) {
+                const auto s = P::piece(w * PI + i, lane);
+                vp[i] = fetch<PA>(j.p, a.ldp, s.x, c0 + s.c, j.np, j.nc);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < QI; ++i) {
+                const auto s = Q::piece(w * QI + i, lane);
+                vq[i] = fetch<QA>(j.q, a.ldq, s.x, c0 + s.c, j.nq, j.nc);
+            }
+        };
+        const int n = (j.nc + WK * STEP - 1) / (WK * STEP);
+        __syncthreads();  // the tile before is done with LDS
+        if (n > 0)
+            load(kg * STEP);
+        for (int s = 0; s < n; ++s) {
+            uint8_t *const st = ring + (s & 1) * STAGE;
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    acc[i][k] = mfma16(fq[k], fp[i], acc[i][k]);
+            for (int i = 0; i < PI; ++i)
+                *(u32v<1> *)(st + (w * PI + i) * 1024 + lane * 16) = u32v<1>{vp[i][0], vp[i][1], vp[i][2], vp[i][3]};
+#pragma unroll
+            for (int i = 0; i < QI; ++i)
+                *(u32v<1> *)(st + P::BYTES + (w * QI + i) * 1024 + lane * 16) =
+                    u32v<1>{vq[i][0], vq[i][1], vq[i][2], vq[i][3]};
+            __syncthreads();
+            if (s + 1 < n)
+                load(((s + 1) * WK + kg) * STEP);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                bf16x8 qf[NB];
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                    qf[c] = Q::read(st + P::BYTES, Q::where(wq * NB + c, lane), h);
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const bf16x8 pf = P::read(st, P::where(wp * MB + m, lane), h);
+#pragma unroll
+                    for (int c = 0; c < NB; ++c)
+                        acc[c][m] = mfma16(qf[c], pf, acc[c][m]);
+                }
+            }
+        }
+        if constexpr (WK > 1) {  // the groups' sums, joined in their order by the first one
+            __syncthreads();
+            floatx4 *sum = (floatx4 *)smem + w * (NB * MB * 64) + lane;
+            if (kg > 0)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        sum[((kg - 1) * NW * NB * MB + c * MB + m) * 64] = acc[c][m];
+            __syncthreads();
+            if (kg > 0)
+                continue;
+#pragma unroll
+            for (int g = 0; g < WK - 1; ++g)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        acc[c][m] += sum[(g * NW * NB * MB + c * MB + m) * 64];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int m = 0; m < MB; ++m) {
+            const int p = wp * (16 * MB) + (PA ? m * 16 + l16 : paired(m, l16));
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int c = 0; c < NB / 2; ++c) {
+                const int q = wq * (16 * NB) + c * 32 + lg * 8;
+                float v[8];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int p = wp + i * 16 + l16, q = wq + k * 16 + lg * 4 + r;
-                    if (p < j.np && q < j.nq)
-                        put<F32>(a, j.out + (int64_t)p * a.ldo + q, acc[i][k][r]);
+                for (int i = 0; i < 4; ++i) {
+                    const float x = acc[2 * c][m][i], y = acc[2 * c + 1][m][i];
+                    v[i] = lg & 1 ? y : x;
+                    v[4 + i] = lg & 1 ? x : y;
                 }
+                if (p < j.np && q < j.nq)
+                    put8<F32>(a, j.out + (int64_t)p * a.ldo + q, v, j.nq - q);
+            }
+        }
     }
 }
 
+// Tiles of 128 x 128 where they give every CU one, else of 64 x 64 by two groups of
+// waves.
 template <int WAY>
 void launch_any(const Mm16Args &a, hipStream_t st)
 {
-    const int64_t tiles = mm16_tile_count(a, ANY_T, ANY_T);
+    const int64_t large = mm16_tile_count(a, 128, 128), small = mm16_tile_count(a, 64, 64);
+    const int64_t tiles = large >= 256 ? large : small;
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
-    if (a.out_f32)
-        mm16_any<WAY, true><<<grid, 256, 0, st>>>(a, (int)tiles);
-    else
-        mm16_any<WAY, false><<<grid, 256, 0, st>>>(a, (int)tiles);
+    auto run = [&](auto f32) {
+        constexpr bool F32 = decltype(f32)::value;
+        if (large >= 256)
+            mm16_any<WAY, F32, 128, 128, 2, 2, 1><<<grid, 256, 0, st>>>(a, (int)tiles);
+        else
+            mm16_any<WAY, F32, 64, 64, 2, 2, 2><<<grid, 512, 0, st>>>(a, (int)tiles);
+    };
+    a.out_f32 ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace

@@ -1,4 +1,5 @@
-// Tiles of the grouped bf16 products: what a tile number stands for.
+// Tiles of the grouped bf16 products: what a tile number stands for, and how an
+// operand lies in LDS.
 #pragma once
 
 #include "common.h"
@@ -62,5 +63,69 @@ inline int64_t mm16_tile_count(const Mm16Args &a, int bp, int bq)
         return a.G * (((int64_t)a.P + bp - 1) / bp) * ntq;
     return (a.G > 1 ? a.M / bp + a.G : ((int64_t)a.M + bp - 1) / bp) * ntq;
 }
+
+
+constexpr int STEP = 64;  // depth of a stage
+
+// The element that row r of block b of 16 holds where the two are not alike: pairs
+// of blocks share 32 elements such that a lane's results of a pair are 8 adjacent
+// ones, and the rows of a block read both halves of the pieces of 8 elements (so
+// that a transposing read falls on all banks).
+__device__ __forceinline__ int paired(int b, int r)
+{
+    return (b >> 1) * 32 + (r >> 2) * 8 + (((b ^ (r >> 2)) & 1) << 2) + (r & 3);
+}
+
+// One operand's tile of XN elements by 64 c in LDS, in blocks of 16 elements whose
+// order is that of paired() where PAIR says so (always where the read transposes).
+template <int XN, bool ADJ, bool PAIR>
+struct Operand {
+    static constexpr int BYTES = XN * STEP * 2, COPIES = BYTES / 1024;
+    static constexpr int ROW = ADJ ? 128 : XN * 2;     // bytes of a row in LDS
+    static constexpr int PER = 1024 / ROW;             // rows of a copy
+    static_assert(XN % (PAIR ? 32 : 16) == 0 && (ADJ || (PAIR && XN % 64 == 0)), "whole blocks, and whole rotations");
+
+    // What the pieces of a row are rotated by.
+    __device__ static __forceinline__ int key(int row)
+    {
+        if (ADJ)
+            return (row >> 1) & 7;
+        return XN >= 128 ? (row & 3) << 2 | ((row >> 3) & 1) : (row & 2) << 1 | ((row >> 3) & 1);
+    }
+    // Copy i of the tile: the lane's element and c.
+    struct Piece {
+        int x, c;
+    };
+    __device__ static __forceinline__ Piece piece(int i, int lane)
+    {
+        const int row = i * PER + lane / (64 / PER), at = (lane % (64 / PER)) ^ key(row);
+        if (!ADJ)
+            return Piece{at * 8, row};
+        return Piece{PAIR ? paired(row >> 4, row & 15) : row, at * 8};
+    }
+    // Byte offset in LDS of the lane's fragment of block b: 8 c of one element, c
+    // from 8 * (lane / 16) on.
+    __device__ static __forceinline__ int where(int b, int lane)
+    {
+        const int l16 = lane & 15, lg = lane >> 4;
+        if (ADJ)
+            return b * 2048 + l16 * 128 + ((lg ^ key(l16)) << 4);
+        // 16 lanes read 4 c of 16 elements, 4 elements a lane, and get 4 c of one
+        const int row = lg * 8 + (l16 >> 2), e = (b >> 1) * 32 + (l16 & 3) * 8;
+        return row * ROW + (((e >> 3) ^ key(row)) << 4) + (((b ^ l16) & 1) << 3);
+    }
+    // The fragment of the 32 c of half h of the step.
+    __device__ static __forceinline__ bf16x8 read(const uint8_t *tile, int at, int h)
+    {
+        if (ADJ)
+            return *(const bf16x8 *)(tile + (at ^ (h << 6)));
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) bf16x4 *Ptr;
+        const auto p = (__attribute__((address_space(3))) const uint8_t *)tile + at + h * (32 * ROW);
+        const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Ptr)p);
+        const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Ptr)(p + 4 * ROW));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
 
 }  // namespace moe

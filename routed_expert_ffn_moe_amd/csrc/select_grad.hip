@@ -22,6 +22,7 @@
 #include "common.h"
 #include "fp8.h"
 #include "kernels.h"
+#include "topk.h"
 
 namespace moe {
 
@@ -31,20 +32,29 @@ constexpr float LARGEST = 3.4028234e38f;
 // Logits whose 64-bit score is 0: selected ones have weight 0 and no gradient.
 constexpr float SIGMOID_ZERO = -709.78f, SOFTMAX_ZERO = -745.14f;
 
+// Sum and maximum over the wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        v += __shfl_xor(v, d);
-    return v;
+    auto add = [&](auto ctrl, auto rows) {
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
+                                                        decltype(rows)::value, 0xf, false));
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-__device__ __forceinline__ float wave_max(float v)
+__device__ __forceinline__ float wave_max(float v) { return key_value(wave_max_u32(order_key(v))); }
+
+// The value of lane i (the same i in every lane).
+__device__ __forceinline__ float from_lane(float v, int i)
 {
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
 }
 
 // Lane l's experts are l, l + 64, ...
@@ -93,7 +103,7 @@ __global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
             const float q = live ? expf(ls - most) : 0.0f;
             float total = 0.0f, sum = 0.0f;
             for (int i = 0; i < a.k; ++i) {
-                const float qi = __shfl(q, i), di = __shfl(d, i);
+                const float qi = from_lane(q, i), di = from_lane(d, i);
                 total += qi;
                 sum += qi > 0.0f ? qi * (d - di) : 0.0f;
             }
@@ -108,8 +118,8 @@ __global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
         for (int i = 0; i < PER; ++i)
             g[i] = out[i] = 0.0f;
         for (int j = 0; j < a.k; ++j) {
-            const int ej = __shfl(e, j);
-            const float v = __shfl(slot, j);
+            const int ej = __builtin_amdgcn_readlane(e, j);
+            const float v = from_lane(slot, j);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (ej == lane + 64 * i) {
@@ -140,7 +150,7 @@ __global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
                     }
                 }
                 const uint64_t who = __ballot(at_top);  // never empty unless all are NaN
-                ref = __shfl(ref, who ? __ffsll((unsigned long long)who) - 1 : 0);
+                ref = from_lane(ref, who ? __ffsll((unsigned long long)who) - 1 : 0);
                 sum = wave_sum(sum);
                 const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -156,8 +166,8 @@ __global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
             } else {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const float x = expf(-fabsf(l[i])), y = 1.0f + x;  // masked: 0
-                    out[i] += x > 0.0f ? g[i] * (x / (y * y)) : 0.0f;
+                    const float x = expf(-fabsf(l[i])), y = __builtin_amdgcn_rcpf(1.0f + x);  // masked: 0
+                    out[i] += x > 0.0f ? g[i] * (x * y * y) : 0.0f;
                 }
             }
         }
