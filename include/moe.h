@@ -324,7 +324,7 @@ int moe_matmul_fp8(const moe_matmul_t *matmul, const void *a, const float *sa, c
  * and scales of moe_quant_fp8 in 1 x 128 blocks (an 8-bit checkpoint of x), which
  * are multiplied in fp32 and rounded once to row_dtype. */
 typedef struct {
-    int32_t T, H;        /* tokens and columns                                  */
+    int32_t T, H;        /* tokens and columns (at most 2^30, as in all of these) */
     int32_t E, top_k;    /* experts, 1..1024; slots of a token, 1..16           */
     int32_t x_dtype;     /* MOE_F32, MOE_BF16 or MOE_FP8                        */
     int32_t row_dtype;   /* x_dtype; MOE_F32 or MOE_BF16 where x is MOE_FP8     */
@@ -421,7 +421,7 @@ int moe_select_grad(const moe_select_t *select, const void *logits, const float 
  * taken; strides that are multiples of 8 elements with pointers aligned to 16 bytes
  * are fast. */
 typedef struct {
-    int32_t M, N, K;     /* rows; rows and columns of each w                    */
+    int32_t M, N, K;     /* rows; rows and columns of each w; at most 2^30 each */
     int32_t G;           /* matrices w, 1..65535                                */
     int32_t out_dtype;   /* MOE_F32 or MOE_BF16                                 */
     int64_t ldx, ldw, ldy; /* row strides of x and dx, w and dw, y and dy, 0: K, K, N */

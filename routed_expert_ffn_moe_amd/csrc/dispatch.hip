@@ -357,9 +357,9 @@ __global__ __launch_bounds__(256) void dispatch_tiny(SortArgs s, GatherArgs a)
         return;
     __syncthreads();
     const int per_row = (a.H + 7) / 8;
-    for (int i = (int)blockIdx.x * 256 + tid; i < s.T * per_row; i += (int)gridDim.x * 256) {
-        const int t = i / per_row;
-        gather_columns<SRC, F32>(a, t, (i - t * per_row) * 8, [&](int j) { return s_at[t * s.k + j]; });
+    for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < (int64_t)s.T * per_row; i += (int64_t)gridDim.x * 256) {
+        const int t = (int)(i / per_row);
+        gather_columns<SRC, F32>(a, t, (int)(i - (int64_t)t * per_row) * 8, [&](int j) { return s_at[t * s.k + j]; });
     }
 }
 

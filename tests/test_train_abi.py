@@ -28,7 +28,7 @@ def call_dispatch(idx=ptr(1), x=ptr(2), sx=None, rows=ptr(3), offsets=ptr(4), sr
                                    ws_bytes, None)
 
 
-SIZES = [dict(T=-1), dict(H=0), dict(E=0), dict(E=1025), dict(top_k=0), dict(top_k=17),
+SIZES = [dict(T=-1), dict(H=0), dict(H=(1 << 30) + 1, T=1), dict(E=0), dict(E=1025), dict(top_k=0), dict(top_k=17),
          dict(T=(1 << 30) // 2 + 1), dict(x_dtype=2), dict(x_dtype=4), dict(x_dtype=0), dict(row_dtype=0),
          dict(x_dtype=3, row_dtype=3, sx=ptr(8)), dict(x_dtype=3, row_dtype=2, sx=ptr(8)), dict(ldx=199),
          dict(ldx=-1), dict(ldr=199), dict(ldx=(1 << 31) + 1), dict(ldr=(1 << 31) + 1),
@@ -89,7 +89,7 @@ def call_combine(rows=ptr(1), of=ptr(2), w=ptr(3), y=ptr(4), **kw):
     return moe.load().moe_combine(ctypes.byref(moe.moe_combine_t(**d)), rows, of, w, y, None)
 
 
-C_SIZES = [dict(T=-1), dict(H=0), dict(top_k=0), dict(top_k=17), dict(R=-1), dict(dtype=2), dict(dtype=3),
+C_SIZES = [dict(T=-1), dict(H=0), dict(H=(1 << 30) + 1), dict(top_k=0), dict(top_k=17), dict(R=-1), dict(dtype=2), dict(dtype=3),
            dict(ldr=99), dict(ldy=99), dict(ldy=-1), dict(ldr=(1 << 31) + 1), dict(T=1 << 30)]
 
 
@@ -127,7 +127,7 @@ def call_swiglu(gate=ptr(1), up=ptr(2), used=None, h=ptr(3), codes=ptr(4), scale
     return moe.load().moe_swiglu(ctypes.byref(moe.moe_swiglu_t(**d)), gate, up, used, h, codes, scales, None)
 
 
-S_SIZES = [dict(R=-1), dict(I=0), dict(dtype=2), dict(dtype=3), dict(ld=199), dict(ldh=199), dict(ld=-8),
+S_SIZES = [dict(R=-1), dict(I=0), dict(R=1, I=(1 << 30) + 1), dict(dtype=2), dict(dtype=3), dict(ld=199), dict(ldh=199), dict(ld=-8),
            dict(ld=(1 << 31) + 1), dict(R=1 << 30)]
 
 
@@ -193,7 +193,7 @@ def call_matmul(name, a=ptr(1), b=ptr(2), offsets=ptr(3), add=None, out=ptr(4), 
 
 @pytest.mark.parametrize("name", ["moe_matmul_bf16", "moe_matmul_bf16_dx", "moe_matmul_bf16_dw"])
 @pytest.mark.parametrize("bad", [
-    dict(M=-1), dict(N=0), dict(K=0), dict(G=0), dict(G=65536), dict(out_dtype=2), dict(out_dtype=3), dict(ldx=39),
+    dict(M=-1), dict(N=0), dict(K=0), dict(M=(1 << 30) + 1), dict(N=(1 << 30) + 1, G=1), dict(K=(1 << 30) + 1, G=1), dict(G=0), dict(G=65536), dict(out_dtype=2), dict(out_dtype=3), dict(ldx=39),
     dict(ldw=39), dict(ldy=47), dict(ldx=-8), dict(ldw=(1 << 31) + 1), dict(offsets=0),
     dict(N=1 << 30, ldw=1 << 31, G=9), dict(M=1 << 30, N=1 << 20, K=1 << 20), dict(a=0), dict(b=0), dict(out=0),
     dict(a=ptr(1) + 1), dict(b=ptr(2) + 1), dict(out=ptr(4) + 1), dict(out_dtype=0, out=ptr(4) + 2),

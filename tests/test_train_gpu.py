@@ -649,6 +649,115 @@ def test_matmul_dw_of_no_rows(M, out):
     assert torch.equal(dw, add)
 
 
+# Products that the rule of the tile shapes (mm16_shape) gives to each of them, as one matrix and as groups:
+# largest tiles first; the last sizes are the smallest tiles'.
+SHAPED = {
+    "y": [(2500, 4104, 136, 1), (2500, 4104, 136, 3), (9000, 1544, 200, 40), (1200, 4104, 136, 3), (2500, 2056, 1032, 1),
+          (9000, 520, 264, 40), (2500, 1544, 200, 1), (2500, 1544, 200, 9), (9000, 200, 1544, 600), (700, 4104, 136, 1),
+          (1200, 1544, 200, 3), (9000, 520, 264, 600), (500, 1544, 200, 1), (500, 2056, 1032, 3), (9000, 136, 72, 40),
+          (1200, 200, 1544, 1), (2500, 136, 4104, 1), (5000, 136, 72, 600), (37, 4104, 136, 3), (37, 264, 4104, 3),
+          (700, 200, 1544, 1), (37, 136, 72, 600)],
+    "dx": [(5000, 136, 4104, 1), (5000, 264, 4104, 3), (9000, 200, 1544, 40), (2500, 264, 4104, 1), (1200, 136, 4104, 3),
+           (5000, 200, 1544, 40), (1200, 264, 4104, 1), (700, 264, 4104, 9), (9000, 200, 1544, 600), (700, 136, 4104, 1),
+           (500, 264, 4104, 3), (9000, 520, 264, 600), (500, 2056, 1032, 1), (200, 264, 4104, 3), (9000, 136, 72, 40),
+           (1200, 4104, 136, 1), (37, 1544, 200, 3), (2500, 520, 264, 600)],
+    "dw": [(500, 2056, 1032, 9), (9000, 200, 1544, 600), (300, 2056, 1032, 3), (5000, 136, 72, 600), (200, 264, 4104, 3),
+           (9000, 136, 4104, 1), (37, 1544, 200, 3), (5000, 136, 72, 40), (1200, 1544, 200, 1)],
+}
+
+
+@pytest.mark.parametrize("way,M,N,K,G", [(w,) + c for w in WAYS for c in SHAPED[w]])
+def test_matmul_of_every_tile_shape(way, M, N, K, G):
+    ends = None
+    if G > 1:
+        g = gen(M + G)
+        ends = [1] + torch.randint(1, M - 7, (G - 1,), generator=g).sort().values.tolist() + [M - 7]
+    check_matmul(way, M, N, K, ends, out="bf16")
+    check_matmul(way, M, N, K, ends, out="f32", add=True)
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("C", [1, 8, 16, 56, 63, 64, 65, 72, 120, 128, 129, 136, 184, 192, 200, 248, 256, 264, 320, 520, 1000])
+def test_matmul_of_every_depth(C, way):
+    """The depth's last stages, which the groups of waves share out: few rows, some, many."""
+    for P, Q in ((9, 264), (70, 136), (330, 520), (1030, 1032)):
+        M, N, K = {"y": (P, Q, C), "dx": (P, C, Q), "dw": (C, P, Q)}[way]
+        check_matmul(way, M, N, K, out="f32")
+    M, N, K = {"y": (40, 136, C), "dx": (40, C, 136), "dw": (3 * C, 72, 136)}[way]
+    check_matmul(way, M, N, K, [0, M // 3, M // 3, 2 * (M // 3), M], out="f32")
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_matmul_odd_sizes_of_many_tiles(way):
+    check_matmul(way, 2111, 2049, 131, out="bf16")
+    check_matmul(way, 1501, 1311, 77, [3, 3, 700, 1111, 1490], out="f32", add=True)
+
+
+def test_matmul_beyond_32_bits():
+    """Matrices of more than 2^32 bytes: the last groups' products, and nothing in front of them."""
+    G, N, K, M = 300, 2048, 4096, 40
+    w = torch.zeros(G, N, K, dtype=torch.bfloat16, device="cuda")
+    g = gen(4)
+    w[-1] = ints(g, N, K, dtype=torch.bfloat16).cuda()
+    ends = torch.zeros(G + 1, dtype=torch.int32)
+    ends[-1] = M
+    off = ends.cuda()
+    x, dy = ints(g, M, K, dtype=torch.bfloat16), ints(g, M, N, dtype=torch.bfloat16)
+    m = moe.make_matmul_bf16(M, N, K, G=G, out="f32")
+    y, dx = torch.empty(M, N, device="cuda"), torch.empty(M, K, device="cuda")
+    moe.moe_matmul_bf16(m, x.cuda(), w, y, off)
+    moe.moe_matmul_bf16_dx(m, dy.cuda(), w, dx, off)
+    last = w[-1].cpu().double()
+    assert torch.equal(y.cpu().double(), x.double() @ last.t()) and torch.equal(dx.cpu().double(), dy.double() @ last)
+    moe.moe_matmul_bf16_dw(moe.make_matmul_bf16(M, N, K, G=G), dy.cuda(), x.cuda(), w, off)
+    assert torch.equal(w[-1].cpu().double(), (dy.double().t() @ x.double()).to(torch.bfloat16).double())
+    assert int(torch.count_nonzero(w[:-1].view(torch.int16).view(-1, 4096)[::64])) == 0
+
+
+def test_rows_beyond_32_bits():
+    """Rows past 2^32 bytes in moe_gather, moe_combine and its gradient, and in SwiGLU with its checkpoint."""
+    H, k = 8192, 2
+    T = 140_000
+    R = T * k
+    rows = torch.empty(R, H, dtype=torch.bfloat16, device="cuda")
+    x = torch.arange(T, device="cuda", dtype=torch.float32).remainder_(251).to(torch.bfloat16)[:, None].expand(T, H).contiguous()
+    of = torch.arange(R, dtype=torch.int32, device="cuda").view(T, k)
+    moe.moe_gather(moe.make_dispatch(T, H, 1, k), of, x, None, rows)
+    for r in (0, R // 2, R - 1):
+        assert (rows[r] == float((r // k) % 251)).all()
+    y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    c = moe.make_combine(T, H, k, R)
+    moe.moe_combine(c, rows, of, None, y)
+    assert torch.equal(y[-3:], 2 * x[-3:]) and torch.equal(y[:3], 2 * x[:3])
+    dw = torch.empty(T, k, device="cuda")
+    drows = torch.empty_like(rows)
+    moe.moe_combine_grad(c, x, rows, of, torch.full((T, k), 0.5, device="cuda"), drows, dw)
+    assert torch.equal(drows[-2:], 0.5 * x[-1:].expand(2, H))
+    v = float(x[-1, 0])
+    assert float(dw[-1, 1]) == v * v * H
+    s = moe.make_swiglu(R, H)
+    codes = torch.empty(R, 2 * H, dtype=F8, device="cuda")
+    scales = torch.empty(R, 2 * H // 128, device="cuda")
+    h = torch.empty_like(rows)
+    moe.moe_swiglu(s, rows, rows, h, codes, scales)
+    want = ref.swiglu(rows[-1].cpu(), rows[-1].cpu())
+    within(h[-1], want, want.abs() * (2.0 ** -20 + 2.0 ** -8 * 1.01) + TINY, "far swiglu")
+    moe.moe_swiglu_grad(s, None, None, codes, scales, drows, rows, y.new_empty(R, H), h)
+    g = (codes[-1].float() * scales[-1].repeat_interleave(128)).cpu()
+    want = ref.swiglu_grad(g[:H], g[H:], drows[-1].cpu())[2]
+    within(h[-1], want, want.abs() * (2.0 ** -20 + 2.0 ** -8 * 1.01) + TINY, "far h")
+
+
+@pytest.mark.parametrize("T,k", [(64, 2), (129, 1), (43, 3), (341, 3), (4096, 1), (4097, 1), (1365, 3), (21845, 3), (65537, 1)])
+@pytest.mark.parametrize("E", [1, 3, 64, 1024])
+def test_dispatch_at_the_borders_of_its_ways(T, k, E):
+    """Up to 128 pairs, 4 and 64 blocks of whole tokens, and more."""
+    g = gen(T + E)
+    idx = torch.randint(-1, E, (T, k), generator=g).to(torch.int32)  # repeated experts, empty slots
+    x = randn(g, T, 9, dtype=torch.bfloat16).cuda()
+    check_dispatch(idx, x, E)
+
+
 # ---- together -------------------------------------------------------------------
 
 class Layer:
