@@ -249,12 +249,19 @@ constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.5
 // The shape that takes least time.  Groups whose balanced rows (1.4 standard
 // deviations above the mean) fit into a tile have one, larger ones leave half a tile
 // empty.
+//
+// Groups of a few rows read their weights once, from memory, and tiles of 16 columns
+// keep more of it busy than those of 64, unless c is so short that the tiles' ends
+// count: 48 rows of 256 groups with N=768, K=2048 34 us against 38, 2048 rows 162
+// against 187, but 48 rows with N=2048, K=768 47 against 39.
 template <int N>
 int mm16_shape(const Mm16Args &a, const Shape (&shapes)[N])
 {
     int best = 0;
     double least = 1e300;
     const double per = (double)a.M / a.G;
+    if (a.way == MM_Y && a.G > 1 && a.C >= 1024 && per + 1.4 * std::sqrt(per) <= shapes[N - 1].bp)
+        return N - 1;
     for (int i = 0; i < N; ++i) {
         const Shape &s = shapes[i];
         const double tq = (double)((a.Q + s.bq - 1) / s.bq);
