@@ -66,11 +66,9 @@ __global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
         float l[PER], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = lane + 64 * i;
-            float v = -INFINITY;
-            if (e < a.E)
-                v = BF16 ? bf2f(((const uint16_t *)a.logits)[t * a.ld + e]) : ((const float *)a.logits)[t * a.ld + e];
-            l[i] = v > -INFINITY ? fminf(v, LARGEST) : -INFINITY;  // NaN: masked
+            const int64_t at = t * a.ld + min(lane + 64 * i, a.E - 1);  // without a branch: all reads together
+            const float v = BF16 ? bf2f(((const uint16_t *)a.logits)[at]) : ((const float *)a.logits)[at];
+            l[i] = v > -INFINITY && lane + 64 * i < a.E ? fminf(v, LARGEST) : -INFINITY;  // NaN: masked
             top = fmaxf(top, l[i]);
         }
         // lane j < k: slot j, its expert's logit, masked if it or the bias is
@@ -133,9 +131,9 @@ __global__ __launch_bounds__(256) void select_grad_rows(SelectGradArgs a)
             if (a.dscore)
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int x = lane + 64 * i;
-                    if (x < a.E && l[i] > -INFINITY && !(a.bias && !(a.bias[x] > -INFINITY)))
-                        g[i] += a.dscore[x];
+                    const int x = min(lane + 64 * i, a.E - 1);
+                    const float d = a.dscore[x], b = a.bias ? a.bias[x] : 0.0f;
+                    g[i] += l[i] > -INFINITY && b > -INFINITY ? d : 0.0f;
                 }
             if (a.softmax) {
                 float s[PER], sum = 0.0f, mean = 0.0f, ref = 0.0f;
