@@ -19,11 +19,11 @@ using moe::overlap;
 
 namespace {
 
-// Largest stride, number of pairs and size of a row (or of rows that are summed
-// over): every offset in bytes then stays below 2^63, and every count of columns
-// that a kernel rounds up below 2^31.
+// Largest stride, number of pairs, number of rows and size of a row: every offset in
+// bytes then stays below 2^63, and every count of columns that a kernel rounds up
+// below 2^31.
 constexpr int64_t MAX_LD = (int64_t)1 << 31, MAX_PAIRS = (int64_t)1 << 30;
-constexpr int32_t MAX_COLS = 1 << 30;
+constexpr int32_t MAX_COLS = 1 << 30, MAX_ROWS = 1 << 30;
 
 bool float_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 
@@ -130,8 +130,8 @@ const char *combine_sizes(const moe_combine_t *s)
 {
     if (!s)
         return "combine is NULL";
-    if (s->T < 0 || s->R < 0 || s->H < 1 || s->H > MAX_COLS)
-        return "T, R >= 0 and H in 1..2^30";
+    if (s->T < 0 || s->R < 0 || s->R > MAX_ROWS || s->H < 1 || s->H > MAX_COLS)
+        return "T >= 0, R in 0..2^30 and H in 1..2^30";
     if (s->top_k < 1 || s->top_k > 16)
         return "top_k must be in 1..16";
     if ((int64_t)s->T * s->top_k > MAX_PAIRS)
@@ -162,8 +162,8 @@ const char *swiglu_sizes(const moe_swiglu_t *s)
 {
     if (!s)
         return "swiglu is NULL";
-    if (s->R < 0 || s->I < 1 || s->I > MAX_COLS)
-        return "R >= 0 and I in 1..2^30";
+    if (s->R < 0 || s->R > MAX_ROWS || s->I < 1 || s->I > MAX_COLS)
+        return "R in 0..2^30 and I in 1..2^30";
     if (!float_type(s->dtype))
         return "dtype must be MOE_F32 or MOE_BF16";
     if (!stride_ok(s->ld, s->I) || !stride_ok(s->ldh, s->I))
@@ -191,7 +191,7 @@ int matmul_bf16(const char *entry, int way, const moe_matmul_bf16_t *s, const vo
 {
     if (!s)
         return fail(entry, "matmul is NULL");
-    if (s->M < 0 || s->M > MAX_COLS || s->N < 1 || s->N > MAX_COLS || s->K < 1 || s->K > MAX_COLS || s->G < 1 ||
+    if (s->M < 0 || s->M > MAX_ROWS || s->N < 1 || s->N > MAX_COLS || s->K < 1 || s->K > MAX_COLS || s->G < 1 ||
         s->G > 65535)
         return fail(entry, "M in 0..2^30, N and K in 1..2^30 and G in 1..65535");
     if (!float_type(s->out_dtype))
@@ -459,8 +459,8 @@ int moe_select_grad(const moe_select_t *s, const void *logits, const float *bias
     const char *entry = "moe_select_grad";
     if (!s)
         return fail(entry, "select is NULL");
-    if (s->T < 0)
-        return fail(entry, "T < 0");
+    if (s->T < 0 || s->T > MAX_ROWS)
+        return fail(entry, "T must be in 0..2^30");
     if (s->E < 1 || s->E > 1024)
         return fail(entry, "E must be in 1..1024");
     if (s->top_k < 1 || s->top_k > s->E || s->top_k > 16)

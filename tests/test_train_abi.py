@@ -207,3 +207,14 @@ def test_matmul_bf16_of_no_rows():
     assert call_matmul("moe_matmul_bf16", M=0, a=0, b=0, out=0) == moe.MOE_OK
     assert call_matmul("moe_matmul_bf16_dx", M=0, a=0, b=0, out=0) == moe.MOE_OK
     fails(call_matmul("moe_matmul_bf16_dw", M=0, a=0, b=0, out=0), "moe_matmul_bf16_dw")
+
+
+# ---- largest sizes ----------------------------------------------------------------
+
+def test_more_rows_than_offsets_in_bytes_hold():
+    rows, ld = (1 << 31) - 1, 1 << 31  # of 4 bytes: 2^64 - 2^33 bytes, a negative number of 64 bits
+    fails(call_combine(R=rows, ldr=ld, dtype=0), "2^30")
+    fails(call_combine_grad(R=rows, ldr=ld, dtype=0), "2^30")
+    fails(call_swiglu(R=rows, I=8, ld=ld, ldh=ld, dtype=0), "2^30")
+    fails(call_swiglu_grad(R=rows, I=8, ld=ld, ldh=ld, dtype=0), "2^30")
+    fails(call_select_grad(T=rows, ld=ld), "2^30")
