@@ -324,7 +324,7 @@ int moe_matmul_fp8(const moe_matmul_t *matmul, const void *a, const float *sa, c
  * and scales of moe_quant_fp8 in 1 x 128 blocks (an 8-bit checkpoint of x), which
  * are multiplied in fp32 and rounded once to row_dtype. */
 typedef struct {
-    int32_t T, H;        /* tokens and columns (at most 2^30, as in all of these) */
+    int32_t T, H;        /* tokens and columns (at most 2^30, as every number of rows, tokens and columns here) */
     int32_t E, top_k;    /* experts, 1..1024; slots of a token, 1..16           */
     int32_t x_dtype;     /* MOE_F32, MOE_BF16 or MOE_FP8                        */
     int32_t row_dtype;   /* x_dtype; MOE_F32 or MOE_BF16 where x is MOE_FP8     */
@@ -417,7 +417,8 @@ int moe_select_grad(const moe_select_t *select, const void *logits, const float 
  * belong to group g; groups may be empty (their dw is 0, or add).  Rows of y and dx
  * outside offsets[0] .. offsets[G] - 1 stay as they were, those of x and dy are not
  * used.  offsets is a device array, not decreasing; parts of it outside 0..M are cut
- * off; with G = 1 NULL takes all rows.  Any sizes, strides and element alignment are
+ * off (of offsets that decrease it is not defined which rows are taken, but nothing
+ * outside 0..M is); with G = 1 NULL takes all rows.  Any sizes, strides and element alignment are
  * taken; strides that are multiples of 8 elements with pointers aligned to 16 bytes
  * are fast. */
 typedef struct {

@@ -10,6 +10,18 @@
 //
 // Combine with weights of 1 is the gradient of gather, so the pair of them is
 // closed under differentiation.
+//
+// Sums over a token's slots in j order and over its columns by a fixed tree, in fp32:
+// no atomics but integer counts, the same bits in every call.  16 to 256 threads a
+// token, 8 columns each: rows are read token by token, so that x, y and dy move once,
+// and a token's rows are in flight together.
+//
+// Bound by memory.  T=8192, H=4096, k=6: dispatch 104 us, of which the copy of 67 MB to
+// 395 is 94 (4.9 TB/s, a large copy's rate) and the order 10; combine's gradient 177 (856
+// MB, 4.8 TB/s).  T=2048, H=2048, k=8: combine 13.4 us (75 MB, partly from the infinity
+// cache).  One token's dispatch 3.7 us on the GPU, 7.4 from Python: the host's call.  The gradient
+// of 7 tokens, k=10, H=980: 8.4 us, 17.8 while a tail went element by element and the sums
+// through LDS.
 #include <algorithm>
 #include <type_traits>
 

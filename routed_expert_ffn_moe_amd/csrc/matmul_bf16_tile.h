@@ -10,6 +10,17 @@
 // Pieces of 16 bytes are rotated (XOR) by their row so that the lanes of one read
 // fall on distinct banks: 2.3 cycles for a wave's 512 bytes transposed (15.8
 // unrotated), 4.1 for its 1024 bytes in rows.
+//
+// Bound by the matrix cores, at the clock that they leave, where there are many rows:
+// 8192 x 4096 x 4096 193 to 211 us (boxes differ; 1.30 to 1.42 PFLOP/s), MFMAs in 75% of
+// the cycles at 1.79 GHz, where the products below run at 2.1 to 2.3.  Hence the
+// largest tiles that registers and LDS hold.  MFMAs of 32 x 32 x 16 in place of 16 x 16 x 32
+// are slower (dx 212 us against 197, dw 212 against 205); four waves of 128 x 128 in place of
+// eight (y 215 to 223 against 212 to 229) and raised priority around the MFMAs (dx 202
+// against 197, dw 204 against 205) make no difference beyond the runs' own.
+// Bound by memory where groups have few rows, N=768, K=2048: 48 rows of 256 groups 29 to 32
+// us, 4.7 to 5.2 TB/s; 16384 rows (Zipf) of 256 groups back to dx 181 us, 5.0 TB/s; their dw with
+// an fp32 addend 668 us, 5.0 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -74,7 +85,7 @@ __device__ __forceinline__ void stage_wait()
 }
 
 constexpr int TAB_GROUPS = 512;  // groups that the table has room for
-constexpr int TAB_BYTES = 2 * 4 * (TAB_GROUPS + 1) + 64;
+constexpr int TAB_BYTES = 2 * 4 * TAB_GROUPS + 64;
 
 template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX, int WK>
 struct Tiling {
@@ -96,7 +107,8 @@ struct Tiling {
     static_assert((ST - 1) * L + EX * PI < 64 && (ST - 2) * L + EX * PI + NS < 64, "the counter of outstanding operations holds 63");
 };
 
-// Persistent workgroups.
+// Persistent workgroups: the copies run on into the next tile while the results of
+// this one are stored.
 template <int WAY, bool F32, int BP, int BQ, int WP, int WQ, int ST, int EX, int WK>
 __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_tile(Mm16Args a, int mtiles)
 {
@@ -116,10 +128,10 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_tile(Mm16Args a, int m
     // Panels of 4 row tiles by all column tiles, so that what an XCD works on at
     // a time is about square.
     const int ntq = (a.Q + BQ - 1) / BQ;
-    int *const tab = (int *)(smem + C::O_TAB), *const ends = tab + TAB_GROUPS + 1;
+    int *const tab = (int *)(smem + C::O_TAB), *const start = tab + TAB_GROUPS;  // first tile and row of each group
     const bool listed = C::TAB && a.offsets && a.G <= TAB_GROUPS;
     if (listed) {
-        int *const part = ends + TAB_GROUPS + 1;  // of each wave
+        int *const part = start + TAB_GROUPS;  // of each wave
         constexpr int NT = 64 * C::NW * WK;
         int run = 0;
         for (int g0 = 0; g0 < a.G; g0 += NT) {
@@ -140,9 +152,7 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_tile(Mm16Args a, int m
             }
             if (g < a.G) {
                 tab[g] = before + inc - n;
-                ends[g] = lo;
-                if (g == a.G - 1)
-                    ends[a.G] = hi;
+                start[g] = lo;
             }
             __syncthreads();
         }
@@ -158,8 +168,11 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_tile(Mm16Args a, int m
             else
                 hi = mid - 1;
         }
-        const int row0 = __builtin_amdgcn_readfirstlane(ends[lo]) + (mt - __builtin_amdgcn_readfirstlane(tab[lo])) * BP;
+        const int row = __builtin_amdgcn_readfirstlane(start[lo]);
+        const int row0 = row + (mt - __builtin_amdgcn_readfirstlane(tab[lo])) * BP;
         const int end = min(uniform_load(a.offsets + lo + 1), a.M);
+        if (row0 < row || row0 >= end)  // not with offsets that do not decrease
+            return Where{-1, 0, 0, 0, 0};
         return Where{lo, row0, min(BP, end - row0), 0, 0};
     };
     const int total = mtiles * ntq, per = (total + 7) / 8;

@@ -64,7 +64,6 @@ inline int64_t mm16_tile_count(const Mm16Args &a, int bp, int bq)
     return (a.G > 1 ? a.M / bp + a.G : ((int64_t)a.M + bp - 1) / bp) * ntq;
 }
 
-
 constexpr int STEP = 64;  // depth of a stage
 
 // The element that row r of block b of 16 holds where the two are not alike: pairs

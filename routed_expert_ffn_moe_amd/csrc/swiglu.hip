@@ -8,6 +8,14 @@
 // (the definition of moe_quant_fp8): half of what bf16 rows take.  The backward
 // pass decodes them in registers and gives h again, which the gradient of the
 // next matrix needs, so that h need not be kept at all.
+//
+// The exponential and 1 + e in fp32, the reciprocal by the hardware (1 ulp): some
+// 2^-24 of the results, far below their rounding to bf16.  16 lanes a block of 128 columns,
+// as the codes' scales need them.
+//
+// Bound by memory: 16384 x 768 with the checkpoint 19 to 21 us (101 MB, 4.8 to 5.4 TB/s);
+// the gradient of 48169 x 2048 from codes 169 (993 MB, 5.9 TB/s: more than a copy's 4.9, with
+// three parts in five of it written).
 #include <algorithm>
 
 #include "common.h"

@@ -580,6 +580,30 @@ def test_matmul_groups(name, way, N, K):
 
 
 @pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("N,K,pad", [(768, 1024, 0), (64, 1032, 0), (256, 136, 0), (33, 72, 1)])
+@pytest.mark.parametrize("copies", [1, 40, 200])
+def test_matmul_offsets_that_decrease_stay_inside(way, N, K, pad, copies):
+    """Groups of every tile height in an order that is not allowed (in the table of row tiles and without it):
+    the rows that no offset reaches and what lies behind the last row stay as they were."""
+    M, ends = 2000, [100, 1900, 300, 310, 120, 900, 100, 1800] * copies
+    G = len(ends) - 1
+    m = moe.make_matmul_bf16(M, N, K, G=G, ldx=K + pad, ldw=K, ldy=N + pad)
+    cols = {"y": N + pad, "dx": K + pad, "dw": K}[way]
+    rows = G * N if way == "dw" else M
+    out = torch.full((rows + 300, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = torch.ones(M, K + pad, dtype=torch.bfloat16, device="cuda")[:, :K]
+    dy = torch.ones(M, N + pad, dtype=torch.bfloat16, device="cuda")[:, :N]
+    w = torch.ones(G, N, K, dtype=torch.bfloat16, device="cuda")
+    p, q = {"y": (x, w), "dx": (dy, w), "dw": (dy, x)}[way]
+    res = out[:rows] if way == "dw" else out[:rows, :cols - pad]
+    run_matmul(way, m, p, q, res, torch.tensor(ends, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert (out[rows:] == 7).all()
+    if way != "dw":
+        assert (out[:100] == 7).all() and (out[1900:] == 7).all() and (out[:, cols - pad:] == 7).all()
+
+
+@pytest.mark.parametrize("way", WAYS)
 @pytest.mark.parametrize("M,G,N,K", [(300, 65, 64, 128), (2000, 130, 136, 72), (1500, 5, 264, 520), (70, 300, 24, 40),
                                      (5000, 1000, 16, 8), (900, 8, 768, 256)])
 def test_matmul_many_groups(M, G, N, K, way):
