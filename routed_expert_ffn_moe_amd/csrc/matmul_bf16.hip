@@ -225,11 +225,12 @@ void launch_any(const Mm16Args &a, hipStream_t st)
 namespace {
 
 // Tiles of the variants for whole pieces of 16 bytes (matmul_bf16_tile.h), with what
-// 64 of c cost in us: a tile alone, and on all CUs each of 256 tiles (several small
-// ones share a CU).
+// a step of `deep` of c costs in us: a tile alone, and on all CUs each of 256 tiles
+// (several small ones share a CU).
 struct Shape {
     int bp, bq;
     double alone, busy, end;
+    int deep = 64;
 };
 
 // Fitted to 56 products of each way, of 1 to 65536 rows in 1 to 256 groups, N and K
@@ -238,13 +239,17 @@ struct Shape {
 // list: 8192 x 4096 x 4096 201 against 1456 (y), 48 rows of 256 groups, N=768, K=2048
 // 138 against 59.  dx has no tiles of 16 columns, whose rows of c would be 32 bytes;
 // of dw, whose depth is the group's rows, the small tiles' outputs cost most (`end`):
-// 256 groups of 64 rows 236 against 388.
+// 256 groups of 64 rows 236 against 388.  Few tiles of dw are bound by what a CU
+// reads (34 to 40 GB/s).  There two groups of waves take 64 of c each: 52 against 61 for
+// 8192 rows, N=256, K=2048 (128 tiles; 63 with three groups of two stages) and 28 against 34 for
+// 4096 x 512 x 512, but 93 against 84 for 4096 x 2048 x 2048 (1024 tiles).
 constexpr Shape SHAPES_Y[] = {{256, 256, 1.4, 1.9, 0}, {128, 256, 1.0, 1.08, 0}, {64, 256, 0.89, 0.8, 0},
                               {64, 128, 0.64, 0.44, 0}, {64, 64, 0.40, 0.34, 0}, {16, 64, 0.29, 0.21, 0},
                               {16, 16, 0.166, 0.08, 0}};
 constexpr Shape SHAPES_DX[] = {{256, 256, 1.6, 1.95, 0}, {128, 256, 1.1, 1.15, 0}, {64, 256, 0.95, 0.87, 0},
                                {64, 128, 0.73, 0.48, 0}, {64, 64, 0.50, 0.41, 0}, {16, 64, 0.44, 0.28, 0}};
-constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.57, 1.8}, {64, 64, 0.51, 0.275, 0.66}};
+constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.57, 1.8}, {64, 64, 0.51, 0.275, 0.66},
+                               {64, 64, 0.73, 0.72, 1.1, 128}};
 
 // The shape that takes least time.  Groups whose balanced rows (1.4 standard
 // deviations above the mean) fit into a tile have one, larger ones leave half a tile
@@ -268,12 +273,12 @@ int mm16_shape(const Mm16Args &a, const Shape (&shapes)[N])
         double tiles, steps;
         if (a.way == MM_DW) {
             tiles = a.G * tq * ((a.P + s.bp - 1) / s.bp);
-            steps = std::max(1.0, std::ceil(per / 64));
+            steps = std::max(1.0, std::ceil(per / s.deep));
         } else {
             tiles = tq * (a.G == 1                                ? (double)((a.M + s.bp - 1) / s.bp)
                           : per + 1.4 * std::sqrt(per) <= s.bp ? (double)std::min(a.M, a.G)
                                                                   : (double)a.M / s.bp + 0.5 * a.G);
-            steps = std::ceil(a.C / 64.0);
+            steps = std::ceil(a.C / (double)s.deep);
         }
         const double t = steps * std::max(s.alone, s.busy * tiles / 256) + s.end * std::max(1.0, tiles / 256);
         if (t < least) {

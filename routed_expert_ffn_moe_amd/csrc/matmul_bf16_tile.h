@@ -521,7 +521,8 @@ void launch_shape(const Mm16Args &a, int shape, hipStream_t st)
         switch (shape) {
         case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
         case 1: launch_tiling<WAY, F32, 128, 128, 2, 2, 2, 1, 1>(a, st); break;
-        default: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 1>(a, st); break;
+        case 2: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 1>(a, st); break;
+        default: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
         }
     } else {
         switch (shape) {

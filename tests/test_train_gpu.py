@@ -711,6 +711,21 @@ def test_matmul_of_every_depth(C, way):
     check_matmul(way, M, N, K, [0, M // 3, M // 3, 2 * (M // 3), M], out="f32")
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("N,K", [(64, 64), (72, 136), (136, 264), (256, 520)])
+@pytest.mark.parametrize("lengths", [[193], [256], [1001], [0, 1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 3000, 0],
+                                     [700, 0, 0, 650], [5, 1400, 64, 1]])
+def test_matmul_dw_of_few_tiles_and_many_rows(lengths, N, K, out):
+    """Groups whose rows are few tiles of dw: two groups of waves share the depth, of which the second may have none."""
+    ends = [3]
+    for n in lengths:
+        ends.append(ends[-1] + n)
+    check_matmul("dw", ends[-1] + 2, N, K, ends, out=out)
+    check_matmul("dw", ends[-1] + 2, N, K, ends, out=out, add=True, pad=(8, 16, 24))
+    if len(lengths) == 1:
+        check_matmul("dw", lengths[0], N, K, out=out)
+
+
 @pytest.mark.parametrize("way", WAYS)
 def test_matmul_odd_sizes_of_many_tiles(way):
     check_matmul(way, 2111, 2049, 131, out="bf16")
