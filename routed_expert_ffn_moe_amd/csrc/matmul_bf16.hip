@@ -203,7 +203,9 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_any(Mm16Args a, int ti
 }
 
 // Tiles of 128 x 128 where they give every CU one, else of 64 x 64 by two groups of
-// waves.
+// waves, or by four where the tiles leave CUs without one and c is long: 3000 x 333 x 501
+// (dw, fp32) 67 us by two, 47 by four, 101 x 333 x 2050 (y) 18.5 and 13.7 to 15.7, but 73 x 204 x 141 (dw) 5.8
+// and 6.8; at c of 500 the two are alike.
 template <int WAY>
 void launch_any(const Mm16Args &a, hipStream_t st)
 {
@@ -214,8 +216,10 @@ void launch_any(const Mm16Args &a, hipStream_t st)
         constexpr bool F32 = decltype(f32)::value;
         if (large >= 256)
             mm16_any<WAY, F32, 128, 128, 2, 2, 1><<<grid, 256, 0, st>>>(a, (int)tiles);
-        else
+        else if (small > 256 || (a.way == MM_DW ? a.C / a.G : a.C) < 512)
             mm16_any<WAY, F32, 64, 64, 2, 2, 2><<<grid, 512, 0, st>>>(a, (int)tiles);
+        else
+            mm16_any<WAY, F32, 64, 64, 2, 2, 4><<<grid, 1024, 0, st>>>(a, (int)tiles);
     };
     a.out_f32 ? run(std::true_type{}) : run(std::false_type{});
 }

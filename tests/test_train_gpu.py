@@ -727,6 +727,17 @@ def test_matmul_dw_of_few_tiles_and_many_rows(lengths, N, K, out):
 
 
 @pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("C", [511, 512, 513, 575, 639, 641, 705, 769, 1023, 1025, 1281, 2050])
+def test_matmul_odd_sizes_of_few_tiles_and_long_sums(C, way):
+    M, N, K = {"y": (37, 77, C), "dx": (37, C, 77), "dw": (C, 37, 77)}[way]
+    check_matmul(way, M, N, K, out="bf16", pad=(1, 0, 3))
+    check_matmul(way, M, N, K, add=True)
+    cut = M // 3
+    ends = [1, cut, cut, M - 1] if way != "dw" else [0, 1600 * C // 1601, C - 1, C]
+    check_matmul(way, M, N, K, ends)
+
+
+@pytest.mark.parametrize("way", WAYS)
 def test_matmul_odd_sizes_of_many_tiles(way):
     check_matmul(way, 2111, 2049, 131, out="bf16")
     check_matmul(way, 1501, 1311, 77, [3, 3, 700, 1111, 1490], out="f32", add=True)
