@@ -13,7 +13,7 @@
 //
 // Bound by the matrix cores, at the clock that they leave, where there are many rows:
 // 8192 x 4096 x 4096 193 to 211 us (boxes differ; 1.30 to 1.42 PFLOP/s), MFMAs in 75% of
-// the cycles at 1.79 GHz, where the products below run at 2.1 to 2.3.  Hence the
+// the cycles at 1.7 to 1.8 GHz, where the products below run at 2.1 to 2.3.  Hence the
 // largest tiles that registers and LDS hold.  MFMAs of 32 x 32 x 16 in place of 16 x 16 x 32
 // are slower (dx 212 us against 197, dw 212 against 205); four waves of 128 x 128 in place of
 // eight (y 215 to 223 against 212 to 229) and raised priority around the MFMAs (dx 202
