@@ -524,17 +524,23 @@ void launch_shape(const Mm16Args &a, int shape, hipStream_t st)
         case 2: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 1>(a, st); break;
         default: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
         }
-    } else {
+    } else if constexpr (WAY == MM_DX) {
         switch (shape) {
         case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
         case 1: launch_tiling<WAY, F32, 128, 256, 2, 4, 3, 0, 1>(a, st); break;
         case 2: launch_tiling<WAY, F32, 64, 256, 2, 4, 3, 0, 1>(a, st); break;
         case 3: launch_tiling<WAY, F32, 64, 128, 2, 2, 3, 0, 1>(a, st); break;
         case 4: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
-        case 5: launch_tiling<WAY, F32, 16, 64, 1, 2, 3, 0, 4>(a, st); break;
-        default:
-            if constexpr (WAY == MM_Y)
-                launch_tiling<WAY, F32, 16, 16, 1, 1, 4, 0, 4>(a, st);
+        default: launch_tiling<WAY, F32, 16, 64, 1, 2, 3, 0, 4>(a, st); break;
+        }
+    } else {
+        switch (shape) {
+        case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
+        case 1: launch_tiling<WAY, F32, 128, 256, 2, 4, 3, 0, 1>(a, st); break;
+        case 2: launch_tiling<WAY, F32, 64, 128, 2, 2, 3, 0, 1>(a, st); break;
+        case 3: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
+        case 4: launch_tiling<WAY, F32, 16, 64, 1, 2, 3, 0, 4>(a, st); break;
+        default: launch_tiling<WAY, F32, 16, 16, 1, 1, 4, 0, 4>(a, st); break;
         }
     }
 }

@@ -690,6 +690,15 @@ SHAPED = {
 }
 
 
+# The same for sums that are short, whose tiles' ends count.
+SHAPED["y"] += [(9000, 1056, 64, 3), (5000, 2080, 64, 1), (9000, 1352, 64, 40), (5000, 1512, 72, 3), (4100, 2056, 520, 1),
+                (200, 544, 72, 40), (1030, 1032, 8, 1), (1200, 160, 80, 40), (200, 1056, 64, 9), (200, 104, 64, 40),
+                (330, 520, 16, 1), (200, 72, 64, 9), (200, 64, 120, 1), (200, 88, 200, 40)]
+SHAPED["dx"] += [(9000, 64, 1472, 40), (9000, 80, 1448, 40), (5000, 64, 960, 40), (4100, 8, 2056, 1), (200, 72, 1992, 40),
+                 (2060, 520, 2056, 1), (200, 72, 528, 40), (1030, 8, 1032, 1), (200, 72, 984, 9), (2500, 72, 88, 40),
+                 (200, 64, 80, 9), (200, 96, 112, 3), (330, 16, 520, 1)]
+
+
 @pytest.mark.parametrize("way,M,N,K,G", [(w,) + c for w in WAYS for c in SHAPED[w]])
 def test_matmul_of_every_tile_shape(way, M, N, K, G):
     ends = None
@@ -709,6 +718,13 @@ def test_matmul_of_every_depth(C, way):
         check_matmul(way, M, N, K, out="f32")
     M, N, K = {"y": (40, 136, C), "dx": (40, C, 136), "dw": (3 * C, 72, 136)}[way]
     check_matmul(way, M, N, K, [0, M // 3, M // 3, 2 * (M // 3), M], out="f32")
+
+
+@pytest.mark.parametrize("way", ["y", "dx"])
+@pytest.mark.parametrize("C", [8, 64, 72, 136, 200, 264])
+def test_matmul_of_large_outputs_and_every_depth(C, way):
+    for P, Q in ((2060, 2056), (4100, 2056), (4360, 4104)):
+        check_matmul(way, P, *((Q, C) if way == "y" else (C, Q)), out="bf16")
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
