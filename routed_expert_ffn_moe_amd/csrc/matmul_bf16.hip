@@ -242,9 +242,12 @@ struct Shape {
 // `end` is what a tile's sums and output cost, also once a round of tiles.
 //
 // Fitted to products of 1 to 65536 rows in 1 to 256 groups, each with all tiles: 116 of y
-// and of dx, N and K from 8 to 4096, where the pick's time is on average 0.5% (y) and 0.2%
-// (dx) above the best tile's (80 others are 5% faster than without `end`), and 56 of dw (2%).  In us, largest against smallest tiles of that
-// list: 8192 x 4096 x 4096 201 against 1456 (y), 48 rows of 256 groups, N=768, K=2048
+// and of dx, N and K from 8 to 4096, where the pick's time is on average 0.5% (y) and 0.3%
+// (dx) above the best tile's (80 others are 5% faster than without `end`), and 56 of dw
+// (2%).  dx's 64 x 256 counts for a little more than fitted, so that close cases take
+// 128 x 256, which groups of unequal size prefer: 16384 Zipf rows of 256 groups 184 against
+// 192, as many rows in equal groups 171 and 170.  In us, largest against smallest tiles of
+// that list: 8192 x 4096 x 4096 201 against 1456 (y), 48 rows of 256 groups, N=768, K=2048
 // 138 against 59; of K=8 16384 rows of 256 groups, N=2048 61 against 762 (64 x 128 40).
 // dx has no tiles of 16 columns, whose rows of c would be 32 bytes;
 // of dw, whose depth is the group's rows, the small tiles' outputs cost most (`end`):
@@ -254,7 +257,7 @@ struct Shape {
 // 4096 x 512 x 512, but 93 against 84 for 4096 x 2048 x 2048 (1024 tiles).
 constexpr Shape SHAPES_Y[] = {{256, 256, 1.3, 1.5, 7.8}, {128, 256, 1.1, 0.84, 5.9}, {64, 128, 0.49, 0.44, 1.4},
                               {64, 64, 0.29, 0.48, 1.5}, {16, 64, 0.19, 0.27, 1.4}, {16, 16, 0.036, 0.06, 1.4}};
-constexpr Shape SHAPES_DX[] = {{256, 256, 1.2, 2.2, 10}, {128, 256, 0.96, 1.1, 5.3}, {64, 256, 0.93, 0.69, 3.6},
+constexpr Shape SHAPES_DX[] = {{256, 256, 1.2, 2.2, 10}, {128, 256, 0.96, 1.1, 5.3}, {64, 256, 0.93, 0.78, 3.6},
                                {64, 128, 0.75, 0.48, 1.6}, {64, 64, 0.52, 0.59, 1.6}, {16, 64, 0.4, 0.5, 1.5}};
 constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.57, 1.8}, {64, 64, 0.51, 0.275, 0.66},
                                {64, 64, 0.73, 0.72, 1.1, 128}};
