@@ -252,15 +252,16 @@ struct Shape {
 // dx has no tiles of 16 columns, whose rows of c would be 32 bytes;
 // of dw, whose depth is the group's rows, the small tiles' outputs cost most (`end`):
 // 256 groups of 64 rows 236 against 388.  Few tiles of dw are bound by what a CU
-// reads (34 to 40 GB/s).  There two groups of waves take 64 of c each: 52 against 61 for
-// 8192 rows, N=256, K=2048 (128 tiles; 63 with three groups of two stages) and 28 against 34 for
-// 4096 x 512 x 512, but 93 against 84 for 4096 x 2048 x 2048 (1024 tiles).
+// reads.  There two groups of waves take 64 of c each: 52 against 61 for 8192 rows, N=256,
+// K=2048 (128 tiles; 63 with three groups of two stages), but 93 against 84 for 4096 x 2048 x
+// 2048 (1024 tiles); and where 32 x 32 gives no more tiles than CUs, each reads half as
+// much: 22 against 28 for 4096 x 512 x 512, but 61 against 52 for the 512 tiles of 8192 x 256 x 2048.
 constexpr Shape SHAPES_Y[] = {{256, 256, 1.3, 1.5, 7.8}, {128, 256, 1.1, 0.84, 5.9}, {64, 128, 0.49, 0.44, 1.4},
                               {64, 64, 0.29, 0.48, 1.5}, {16, 64, 0.19, 0.27, 1.4}, {16, 16, 0.036, 0.06, 1.4}};
 constexpr Shape SHAPES_DX[] = {{256, 256, 1.2, 2.2, 10}, {128, 256, 0.96, 1.1, 5.3}, {64, 256, 0.93, 0.78, 3.6},
                                {64, 128, 0.75, 0.48, 1.6}, {64, 64, 0.52, 0.59, 1.6}, {16, 64, 0.4, 0.5, 1.5}};
 constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.57, 1.8}, {64, 64, 0.51, 0.275, 0.66},
-                               {64, 64, 0.73, 0.72, 1.1, 128}};
+                               {64, 64, 0.73, 0.72, 1.1, 128}, {32, 32, 1.05, 0.88, 1.2, 256}};
 
 // The shape that takes least time.  Groups whose balanced rows (1.4 standard
 // deviations above the mean) fit into a tile have one, larger ones leave half a tile

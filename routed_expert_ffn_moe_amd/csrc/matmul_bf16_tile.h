@@ -522,7 +522,8 @@ void launch_shape(const Mm16Args &a, int shape, hipStream_t st)
         case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
         case 1: launch_tiling<WAY, F32, 128, 128, 2, 2, 2, 1, 1>(a, st); break;
         case 2: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 1>(a, st); break;
-        default: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
+        case 3: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
+        default: launch_tiling<WAY, F32, 32, 32, 1, 1, 4, 0, 4>(a, st); break;
         }
     } else if constexpr (WAY == MM_DX) {
         switch (shape) {

@@ -82,14 +82,15 @@ struct Operand {
     static constexpr int BYTES = XN * STEP * 2, COPIES = BYTES / 1024;
     static constexpr int ROW = ADJ ? 128 : XN * 2;     // bytes of a row in LDS
     static constexpr int PER = 1024 / ROW;             // rows of a copy
-    static_assert(XN % (PAIR ? 32 : 16) == 0 && (ADJ || (PAIR && XN % 64 == 0)), "whole blocks, and whole rotations");
+    static_assert(XN % (PAIR ? 32 : 16) == 0 && (ADJ || PAIR), "whole blocks");
 
     // What the pieces of a row are rotated by.
     __device__ static __forceinline__ int key(int row)
     {
         if (ADJ)
             return (row >> 1) & 7;
-        return XN >= 128 ? (row & 3) << 2 | ((row >> 3) & 1) : (row & 2) << 1 | ((row >> 3) & 1);
+        const int half = (row >> 3) & 1;
+        return XN >= 128 ? (row & 3) << 2 | half : XN >= 64 ? (row & 2) << 1 | half : (row & 2) | half;
     }
     // Copy i of the tile: the lane's element and c.
     struct Piece {

@@ -720,6 +720,15 @@ def test_matmul_of_every_depth(C, way):
     check_matmul(way, M, N, K, [0, M // 3, M // 3, 2 * (M // 3), M], out="f32")
 
 
+@pytest.mark.parametrize("N,K", [(8, 8), (16, 40), (32, 32), (40, 64), (64, 200), (184, 192), (512, 512)])
+@pytest.mark.parametrize("C", [192, 193, 255, 256, 257, 320, 321, 449, 512, 513, 577, 700, 1030, 2049])
+def test_matmul_dw_of_smallest_tiles(C, N, K):
+    """Four groups of waves share the depth of tiles of 32 x 32; rows outside the groups hold NaN."""
+    check_matmul("dw", C, N, K, out="bf16", add=True)
+    check_matmul("dw", C, N, K, out="f32", pad=(8, 0, 16))
+    check_matmul("dw", 3 * C, N, K, [5, 5 + C, 5 + C, 7 + 2 * C, 3 * C - 4])
+
+
 @pytest.mark.parametrize("way", ["y", "dx"])
 @pytest.mark.parametrize("C", [8, 64, 72, 136, 200, 264])
 def test_matmul_of_large_outputs_and_every_depth(C, way):
