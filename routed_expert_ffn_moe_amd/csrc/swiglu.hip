@@ -9,9 +9,12 @@
 // pass decodes them in registers and gives h again, which the gradient of the
 // next matrix needs, so that h need not be kept at all.
 //
-// The exponential and 1 + e in fp32, the reciprocal by the hardware (1 ulp): some
-// 2^-24 of the results, far below their rounding to bf16.  16 lanes a block of 128 columns,
-// as the codes' scales need them.
+// s and 1 - s come from e = exp(-|g|) and r = 1 / (1 + e), as r and e r, or e r and r of a
+// negative gate: both to 2^-21 of themselves (the exponential and the hardware's reciprocal
+// are off by an ulp each), where a difference from 1 would lose 1 - s of large gates
+// (dg 2^-20 off at g = 17) and 1 / (1 + exp(-g)) what is left of s below the normal numbers
+// (h was 0 from g = -87.4 on; now from -104 on, where e is).  16 lanes a block of 128
+// columns, as the codes' scales need them.
 //
 // Bound by memory: 16384 x 768 with the checkpoint 19 to 21 us (101 MB, 4.8 to 5.4 TB/s);
 // the gradient of 48169 x 2048 from codes 169 (993 MB, 5.9 TB/s: more than a copy's 4.9, with
@@ -96,7 +99,16 @@ __device__ __forceinline__ void decode8(float (&v)[8], const uint8_t *codes, flo
     }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+// s and 1 - s of a gate.
+struct Sigmoid {
+    float s, rest;
+};
+
+__device__ __forceinline__ Sigmoid sigmoid(float z)
+{
+    const float e = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    return z < 0.0f ? Sigmoid{e * r, r} : Sigmoid{r, e * r};
+}
 
 template <bool BF16, bool KEEP>
 __global__ __launch_bounds__(256) void swiglu_rows(SwigluArgs a)
@@ -115,7 +127,7 @@ __global__ __launch_bounds__(256) void swiglu_rows(SwigluArgs a)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            h[i] = g[i] * sigmoid(g[i]) * u[i];
+            h[i] = g[i] * sigmoid(g[i]).s * u[i];
         store8<BF16>(h, a.h, k.row * a.ldh + k.c, a.I - k.c);
     }
 }
@@ -142,9 +154,10 @@ __global__ __launch_bounds__(256) void swiglu_rows_grad(SwigluArgs a)
         float h[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float s = sigmoid(g[i]), z = g[i] * s;
+            const Sigmoid s = sigmoid(g[i]);
+            const float z = g[i] * s.s;
             h[i] = z * u[i];
-            const float slope = fmaf(z, 1.0f - s, s);  // s (1 + g (1 - s))
+            const float slope = fmaf(z, s.rest, s.s);  // s (1 + g (1 - s))
             g[i] = d[i] * u[i] * slope;
             u[i] = d[i] * z;
         }
