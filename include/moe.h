@@ -435,6 +435,13 @@ int moe_matmul_bf16_dx(const moe_matmul_bf16_t *matmul, const void *dy, const vo
 int moe_matmul_bf16_dw(const moe_matmul_bf16_t *matmul, const void *dy, const void *x, const int32_t *offsets,
                        const void *add, void *dw, void *stream);
 
+/* The tile that such a product takes, for analysis and tests (nothing is launched): way
+ * 0, 1 or 2 for y, dx or dw, off16 not 0 where a pointer is not at a multiple of 16
+ * bytes.  tile[0], tile[1]: rows and columns of the output; tile[2]: groups of waves that
+ * share the depth of the sums; tile[3]: 1 if the operands are copied in pieces of 16
+ * bytes, 0 for the tiles of any alignment. */
+int moe_matmul_bf16_tile(const moe_matmul_bf16_t *matmul, int way, int off16, int32_t *tile);
+
 /* Repack E MXFP4 matrices of N rows and K columns (N a multiple of 16, K of
  * 128) from the OCP row-major form (codes [E, N, K/2], scales [E, N, K/32])
  * into the layout moe_forward reads (above); E * N * K / 2 code bytes and

@@ -28,7 +28,7 @@ __all__ = [
     "moe_dispatch_t", "moe_combine_t", "moe_swiglu_t", "moe_matmul_bf16_t", "make_dispatch", "make_combine",
     "make_swiglu", "make_matmul_bf16", "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_gather",
     "moe_combine", "moe_combine_grad", "moe_swiglu", "moe_swiglu_grad", "moe_select_grad", "moe_matmul_bf16",
-    "moe_matmul_bf16_dx", "moe_matmul_bf16_dw",
+    "moe_matmul_bf16_dx", "moe_matmul_bf16_dw", "moe_matmul_bf16_tile",
     "lib_path", "load",
 ]
 
@@ -169,6 +169,7 @@ def load() -> ctypes.CDLL:
         lib.moe_select_grad.argtypes = [P] * 7 + [ctypes.c_int, P]
         for name in ("moe_matmul_bf16", "moe_matmul_bf16_dx", "moe_matmul_bf16_dw"):
             getattr(lib, name).argtypes = [P] * 7
+        lib.moe_matmul_bf16_tile.argtypes = [P, ctypes.c_int, ctypes.c_int, P]
         _lib = lib
     return _lib
 
@@ -723,6 +724,14 @@ def moe_matmul_bf16_dw(matmul, dy, x, dw, offsets=None, add=None, stream=None) -
                                 pw(dw, "dw", out), st)
     if rc:
         _check(rc)
+
+
+def moe_matmul_bf16_tile(matmul, way, off16=False):
+    """(rows, columns, groups of waves, 1 if copied in pieces of 16 bytes) of the tile that a product
+    takes, way "y", "dx" or "dw"; off16: a pointer is not at a multiple of 16 bytes."""
+    tile = (ctypes.c_int32 * 4)()
+    _check(load().moe_matmul_bf16_tile(ctypes.byref(matmul), ("y", "dx", "dw").index(way), int(off16), tile))
+    return tuple(tile)
 
 
 STAGES = ("router", "permute", "gate_up", "down", "combine")

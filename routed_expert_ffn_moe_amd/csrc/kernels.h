@@ -323,6 +323,13 @@ struct Mm16Args {
 };
 int64_t mm16_most_tiles(const Mm16Args &a);  // bound of the tiles of any variant
 void launch_mm16(const Mm16Args &a, hipStream_t st);
+// What launch_mm16 takes: tiles of rows x cols by `groups` groups of waves, each of which
+// takes its share of c; whole: the copies of the next line, with this number of the shape.
+struct Mm16Pick {
+    int rows, cols, groups, shape;
+    bool whole;
+};
+Mm16Pick mm16_pick(const Mm16Args &a);
 // Operands whose rows can be copied in pieces of 16 bytes, by tiles of a shape
 // (matmul_bf16_y.hip, _dx.hip, _dw.hip).
 void launch_mm16_y(const Mm16Args &a, int shape, hipStream_t st);

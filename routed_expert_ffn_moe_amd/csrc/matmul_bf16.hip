@@ -208,17 +208,24 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_any(Mm16Args a, int ti
 // waves, or by four where the tiles leave CUs without one and c is long: 3000 x 333 x 501
 // (dw, fp32) 67 us by two, 47 by four, 101 x 333 x 2050 (y) 18.5 and 13.7 to 15.7, but 73 x 204 x 141 (dw) 5.8
 // and 6.8; at c of 500 the two are alike.
-template <int WAY>
-void launch_any(const Mm16Args &a, hipStream_t st)
+Mm16Pick any_pick(const Mm16Args &a)
 {
-    const int64_t large = mm16_tile_count(a, 128, 128), small = mm16_tile_count(a, 64, 64);
-    const int64_t tiles = large >= 256 ? large : small;
+    if (mm16_tile_count(a, 128, 128) >= 256)
+        return Mm16Pick{128, 128, 1, 0, false};
+    const bool few = mm16_tile_count(a, 64, 64) <= 256 && (a.way == MM_DW ? a.C / a.G : a.C) >= 512;
+    return Mm16Pick{64, 64, few ? 4 : 2, 0, false};
+}
+
+template <int WAY>
+void launch_any(const Mm16Args &a, Mm16Pick t, hipStream_t st)
+{
+    const int64_t tiles = mm16_tile_count(a, t.rows, t.cols);
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
     auto run = [&](auto f32) {
         constexpr bool F32 = decltype(f32)::value;
-        if (large >= 256)
+        if (t.groups == 1)
             mm16_any<WAY, F32, 128, 128, 2, 2, 1><<<grid, 256, 0, st>>>(a, (int)tiles);
-        else if (small > 256 || (a.way == MM_DW ? a.C / a.G : a.C) < 512)
+        else if (t.groups == 2)
             mm16_any<WAY, F32, 64, 64, 2, 2, 2><<<grid, 512, 0, st>>>(a, (int)tiles);
         else
             mm16_any<WAY, F32, 64, 64, 2, 2, 4><<<grid, 1024, 0, st>>>(a, (int)tiles);
@@ -230,13 +237,10 @@ void launch_any(const Mm16Args &a, hipStream_t st)
 
 namespace {
 
-// Tiles of the variants for whole pieces of 16 bytes (matmul_bf16_tile.h), with what
-// a step of `deep` of c costs in us: a tile alone, and on all CUs each of 256 tiles
-// (several small ones share a CU).
-struct Shape {
-    int bp, bq;
+// What a step of 64 of c (dw: of 64 for each group of waves) costs in us with the tiles
+// of mm16.h: a tile alone, and on all CUs each of 256 tiles (several small ones share a CU).
+struct Cost {
     double alone, busy, end;
-    int deep = 64;
 };
 
 // `end` is what a tile's sums and output cost, also once a round of tiles.
@@ -256,12 +260,12 @@ struct Shape {
 // K=2048 (128 tiles; 63 with three groups of two stages), but 93 against 84 for 4096 x 2048 x
 // 2048 (1024 tiles); and where 32 x 32 gives no more tiles than CUs, each reads half as
 // much: 22 against 28 for 4096 x 512 x 512, but 61 against 52 for the 512 tiles of 8192 x 256 x 2048.
-constexpr Shape SHAPES_Y[] = {{256, 256, 1.3, 1.5, 7.8}, {128, 256, 1.1, 0.84, 5.9}, {64, 128, 0.49, 0.44, 1.4},
-                              {64, 64, 0.29, 0.48, 1.5}, {16, 64, 0.19, 0.27, 1.4}, {16, 16, 0.036, 0.06, 1.4}};
-constexpr Shape SHAPES_DX[] = {{256, 256, 1.2, 2.2, 10}, {128, 256, 0.96, 1.1, 5.3}, {64, 256, 0.93, 0.78, 3.6},
-                               {64, 128, 0.75, 0.48, 1.6}, {64, 64, 0.52, 0.59, 1.6}, {16, 64, 0.4, 0.5, 1.5}};
-constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.57, 1.8}, {64, 64, 0.51, 0.275, 0.66},
-                               {64, 64, 0.73, 0.72, 1.1, 128}, {32, 32, 1.05, 0.88, 1.2, 256}};
+constexpr Cost COST_Y[MM16_NY] = {{1.3, 1.5, 7.8}, {1.1, 0.84, 5.9}, {0.49, 0.44, 1.4},
+                                  {0.29, 0.48, 1.5}, {0.19, 0.27, 1.4}, {0.036, 0.06, 1.4}};
+constexpr Cost COST_DX[MM16_NDX] = {{1.2, 2.2, 10}, {0.96, 1.1, 5.3}, {0.93, 0.78, 3.6},
+                                    {0.75, 0.48, 1.6}, {0.52, 0.59, 1.6}, {0.4, 0.5, 1.5}};
+constexpr Cost COST_DW[MM16_NDW] = {{1.19, 1.69, 5.7}, {0.84, 0.57, 1.8}, {0.51, 0.275, 0.66},
+                                    {0.73, 0.72, 1.1}, {1.05, 0.88, 1.2}};
 
 // The shape that takes least time.  Groups whose balanced rows (1.4 standard
 // deviations above the mean) fit into a tile have one, larger ones leave half a tile
@@ -272,7 +276,7 @@ constexpr Shape SHAPES_DW[] = {{256, 256, 1.19, 1.69, 5.7}, {128, 128, 0.84, 0.5
 // count: 48 rows of 256 groups with N=768, K=2048 34 us against 38, 2048 rows 162
 // against 187, but 48 rows with N=2048, K=768 47 against 39.
 template <int N>
-int mm16_shape(const Mm16Args &a, const Shape (&shapes)[N])
+int mm16_shape(const Mm16Args &a, const Mm16Shape (&shapes)[N], const Cost (&costs)[N])
 {
     int best = 0;
     double least = 1e300;
@@ -280,19 +284,20 @@ int mm16_shape(const Mm16Args &a, const Shape (&shapes)[N])
     if (a.way == MM_Y && a.G > 1 && a.C >= 1024 && per + 1.4 * std::sqrt(per) <= shapes[N - 1].bp)
         return N - 1;
     for (int i = 0; i < N; ++i) {
-        const Shape &s = shapes[i];
+        const Mm16Shape &s = shapes[i];
         const double tq = (double)((a.Q + s.bq - 1) / s.bq);
         double tiles, steps;
         if (a.way == MM_DW) {
             tiles = a.G * tq * ((a.P + s.bp - 1) / s.bp);
-            steps = std::max(1.0, std::ceil(per / s.deep));
+            steps = std::max(1.0, std::ceil(per / (STEP * s.wk)));
         } else {
             tiles = tq * (a.G == 1                                ? (double)((a.M + s.bp - 1) / s.bp)
                           : per + 1.4 * std::sqrt(per) <= s.bp ? (double)std::min(a.M, a.G)
                                                                   : (double)a.M / s.bp + 0.5 * a.G);
-            steps = std::ceil(a.C / (double)s.deep);
+            steps = std::ceil(a.C / (double)STEP);
         }
-        const double t = steps * std::max(s.alone, s.busy * tiles / 256) + s.end * std::max(1.0, tiles / 256);
+        const Cost &c = costs[i];
+        const double t = steps * std::max(c.alone, c.busy * tiles / 256) + c.end * std::max(1.0, tiles / 256);
         if (t < least) {
             least = t;
             best = i;
@@ -316,15 +321,25 @@ bool whole_pieces(const Mm16Args &a)
 
 int64_t mm16_most_tiles(const Mm16Args &a) { return mm16_tile_count(a, 16, 16); }
 
+Mm16Pick mm16_pick(const Mm16Args &a)
+{
+    if (!whole_pieces(a))
+        return any_pick(a);
+    const int n = a.way == MM_Y ? mm16_shape(a, MM16_Y, COST_Y) : a.way == MM_DX ? mm16_shape(a, MM16_DX, COST_DX)
+                                                                : mm16_shape(a, MM16_DW, COST_DW);
+    const Mm16Shape &s = (a.way == MM_Y ? MM16_Y : a.way == MM_DX ? MM16_DX : MM16_DW)[n];
+    return Mm16Pick{s.bp, s.bq, s.wk, n, true};
+}
+
 void launch_mm16(const Mm16Args &a, hipStream_t st)
 {
-    const bool whole = whole_pieces(a);
+    const Mm16Pick t = mm16_pick(a);
     if (a.way == MM_Y)
-        whole ? launch_mm16_y(a, mm16_shape(a, SHAPES_Y), st) : launch_any<MM_Y>(a, st);
+        t.whole ? launch_mm16_y(a, t.shape, st) : launch_any<MM_Y>(a, t, st);
     else if (a.way == MM_DX)
-        whole ? launch_mm16_dx(a, mm16_shape(a, SHAPES_DX), st) : launch_any<MM_DX>(a, st);
+        t.whole ? launch_mm16_dx(a, t.shape, st) : launch_any<MM_DX>(a, t, st);
     else
-        whole ? launch_mm16_dw(a, mm16_shape(a, SHAPES_DW), st) : launch_any<MM_DW>(a, st);
+        t.whole ? launch_mm16_dw(a, t.shape, st) : launch_any<MM_DW>(a, t, st);
 }
 
 }  // namespace moe

@@ -513,36 +513,18 @@ void launch_tiling(const Mm16Args &a, hipStream_t st)
 
 }  // namespace
 
-// The tiles of mm16_shape() by their number.
-template <int WAY, bool F32>
+// The tiles of the lists in mm16.h by their number.
+template <int WAY, bool F32, int I = 0>
 void launch_shape(const Mm16Args &a, int shape, hipStream_t st)
 {
-    if constexpr (WAY == MM_DW) {
-        switch (shape) {
-        case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
-        case 1: launch_tiling<WAY, F32, 128, 128, 2, 2, 2, 1, 1>(a, st); break;
-        case 2: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 1>(a, st); break;
-        case 3: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
-        default: launch_tiling<WAY, F32, 32, 32, 1, 1, 4, 0, 4>(a, st); break;
-        }
-    } else if constexpr (WAY == MM_DX) {
-        switch (shape) {
-        case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
-        case 1: launch_tiling<WAY, F32, 128, 256, 2, 4, 3, 0, 1>(a, st); break;
-        case 2: launch_tiling<WAY, F32, 64, 256, 2, 4, 3, 0, 1>(a, st); break;
-        case 3: launch_tiling<WAY, F32, 64, 128, 2, 2, 3, 0, 1>(a, st); break;
-        case 4: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
-        default: launch_tiling<WAY, F32, 16, 64, 1, 2, 3, 0, 4>(a, st); break;
-        }
-    } else {
-        switch (shape) {
-        case 0: launch_tiling<WAY, F32, 256, 256, 2, 4, 2, 1, 1>(a, st); break;
-        case 1: launch_tiling<WAY, F32, 128, 256, 2, 4, 3, 0, 1>(a, st); break;
-        case 2: launch_tiling<WAY, F32, 64, 128, 2, 2, 3, 0, 1>(a, st); break;
-        case 3: launch_tiling<WAY, F32, 64, 64, 2, 2, 3, 0, 2>(a, st); break;
-        case 4: launch_tiling<WAY, F32, 16, 64, 1, 2, 3, 0, 4>(a, st); break;
-        default: launch_tiling<WAY, F32, 16, 16, 1, 1, 4, 0, 4>(a, st); break;
-        }
+    constexpr int N = WAY == MM_Y ? MM16_NY : WAY == MM_DX ? MM16_NDX : MM16_NDW;
+    if constexpr (I < N) {
+        constexpr Mm16Shape S = WAY == MM_Y ? MM16_Y[I < MM16_NY ? I : 0]
+                                : WAY == MM_DX ? MM16_DX[I < MM16_NDX ? I : 0] : MM16_DW[I < MM16_NDW ? I : 0];
+        if (shape == I || I + 1 == N)
+            launch_tiling<WAY, F32, S.bp, S.bq, S.wp, S.wq, S.st, S.ex, S.wk>(a, st);
+        else
+            launch_shape<WAY, F32, I + 1>(a, shape, st);
     }
 }
 

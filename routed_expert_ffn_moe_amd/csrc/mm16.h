@@ -66,6 +66,20 @@ inline int64_t mm16_tile_count(const Mm16Args &a, int bp, int bq)
 
 constexpr int STEP = 64;  // depth of a stage
 
+// Tiles of the kernel for whole pieces of 16 bytes (matmul_bf16_tile.h, where the fields
+// are explained), from the largest to the smallest.
+struct Mm16Shape {
+    int bp, bq, wp, wq, st, ex, wk;
+};
+constexpr Mm16Shape MM16_Y[] = {{256, 256, 2, 4, 2, 1, 1}, {128, 256, 2, 4, 3, 0, 1}, {64, 128, 2, 2, 3, 0, 1},
+                                {64, 64, 2, 2, 3, 0, 2}, {16, 64, 1, 2, 3, 0, 4}, {16, 16, 1, 1, 4, 0, 4}};
+constexpr Mm16Shape MM16_DX[] = {{256, 256, 2, 4, 2, 1, 1}, {128, 256, 2, 4, 3, 0, 1}, {64, 256, 2, 4, 3, 0, 1},
+                                 {64, 128, 2, 2, 3, 0, 1}, {64, 64, 2, 2, 3, 0, 2}, {16, 64, 1, 2, 3, 0, 4}};
+constexpr Mm16Shape MM16_DW[] = {{256, 256, 2, 4, 2, 1, 1}, {128, 128, 2, 2, 2, 1, 1}, {64, 64, 2, 2, 3, 0, 1},
+                                 {64, 64, 2, 2, 3, 0, 2}, {32, 32, 1, 1, 4, 0, 4}};
+constexpr int MM16_NY = sizeof MM16_Y / sizeof *MM16_Y, MM16_NDX = sizeof MM16_DX / sizeof *MM16_DX,
+              MM16_NDW = sizeof MM16_DW / sizeof *MM16_DW;
+
 // The element that row r of block b of 16 holds where the two are not alike: pairs
 // of blocks share 32 elements such that a lane's results of a pair are 8 adjacent
 // ones, and the rows of a block read both halves of the pieces of 8 elements (so

@@ -186,53 +186,68 @@ moe::SwigluArgs swiglu_args(const moe_swiglu_t *s, const int32_t *used)
     return a;
 }
 
+// nullptr and the sizes of a product, or what is wrong with them.
+struct Product {
+    moe::Mm16Args a;
+    int64_t np, nq, no;  // elements from the first to the last of p, q and the output
+};
+
+const char *matmul_args(const moe_matmul_bf16_t *s, int way, bool grouped, Product &r)
+{
+    if (!s)
+        return "matmul is NULL";
+    if (s->M < 0 || s->M > MAX_ROWS || s->N < 1 || s->N > MAX_COLS || s->K < 1 || s->K > MAX_COLS || s->G < 1 ||
+        s->G > 65535)
+        return "M in 0..2^30, N and K in 1..2^30 and G in 1..65535";
+    if (!float_type(s->out_dtype))
+        return "out_dtype must be MOE_F32 or MOE_BF16";
+    if (!stride_ok(s->ldx, s->K) || !stride_ok(s->ldw, s->K) || !stride_ok(s->ldy, s->N))
+        return "ldx and ldw must be 0 or at least K, ldy 0 or at least N, and at most 2^31";
+    if (s->G > 1 && !grouped)
+        return "G > 1 needs offsets";
+    const int64_t ldx = s->ldx ? s->ldx : s->K, ldw = s->ldw ? s->ldw : s->K, ldy = s->ldy ? s->ldy : s->N;
+    if ((double)s->G * s->N * (double)ldw >= 1e18)
+        return "the matrices w take more than 10^18 elements";
+    moe::Mm16Args &a = r.a;
+    a = {};
+    a.M = s->M;
+    a.G = s->G;
+    a.way = way;
+    a.out_f32 = s->out_dtype == MOE_F32;
+    const int64_t nx = span(s->M, s->K, ldx, 1), nw = span((int64_t)s->G * s->N, s->K, ldw, 1),
+                  ny = span(s->M, s->N, ldy, 1);
+    if (way == moe::MM_Y) {
+        a.P = s->M, a.Q = s->N, a.C = s->K;
+        a.ldp = ldx, a.ldq = ldw, a.ldo = ldy;
+        r.np = nx, r.nq = nw, r.no = ny;
+    } else if (way == moe::MM_DX) {
+        a.P = s->M, a.Q = s->K, a.C = s->N;
+        a.ldp = ldy, a.ldq = ldw, a.ldo = ldx;
+        r.np = ny, r.nq = nw, r.no = nx;
+    } else {
+        a.P = s->N, a.Q = s->K, a.C = s->M;
+        a.ldp = ldy, a.ldq = ldx, a.ldo = ldw;
+        r.np = ny, r.nq = nx, r.no = nw;
+    }
+    a.qstride = a.ostride = s->N * ldw;
+    if (moe::mm16_most_tiles(a) >= (int64_t)1 << 31)
+        return "too many tiles of 16 x 16";
+    return nullptr;
+}
+
 int matmul_bf16(const char *entry, int way, const moe_matmul_bf16_t *s, const void *p, const void *q,
                 const int32_t *offsets, const void *add, void *out, void *stream)
 {
-    if (!s)
-        return fail(entry, "matmul is NULL");
-    if (s->M < 0 || s->M > MAX_ROWS || s->N < 1 || s->N > MAX_COLS || s->K < 1 || s->K > MAX_COLS || s->G < 1 ||
-        s->G > 65535)
-        return fail(entry, "M in 0..2^30, N and K in 1..2^30 and G in 1..65535");
-    if (!float_type(s->out_dtype))
-        return fail(entry, "out_dtype must be MOE_F32 or MOE_BF16");
-    if (!stride_ok(s->ldx, s->K) || !stride_ok(s->ldw, s->K) || !stride_ok(s->ldy, s->N))
-        return fail(entry, "ldx and ldw must be 0 or at least K, ldy 0 or at least N, and at most 2^31");
-    if (s->G > 1 && !offsets)
-        return fail(entry, "G > 1 needs offsets");
-    const int64_t ldx = s->ldx ? s->ldx : s->K, ldw = s->ldw ? s->ldw : s->K, ldy = s->ldy ? s->ldy : s->N;
-    if ((double)s->G * s->N * (double)ldw >= 1e18)
-        return fail(entry, "the matrices w take more than 10^18 elements");
-    moe::Mm16Args a{};
+    Product r;
+    if (const char *what = matmul_args(s, way, offsets, r))
+        return fail(entry, what);
+    moe::Mm16Args &a = r.a;
     a.p = (const uint16_t *)p;
     a.q = (const uint16_t *)q;
     a.offsets = offsets;
     a.add = add;
     a.out = out;
-    a.M = s->M;
-    a.G = s->G;
-    a.way = way;
-    a.out_f32 = s->out_dtype == MOE_F32;
-    const int64_t esz = size_of(s->out_dtype);
-    const int64_t nx = span(s->M, s->K, ldx, 1), nw = span((int64_t)s->G * s->N, s->K, ldw, 1),
-                  ny = span(s->M, s->N, ldy, 1);
-    int64_t np, nq, no;
-    if (way == moe::MM_Y) {
-        a.P = s->M, a.Q = s->N, a.C = s->K;
-        a.ldp = ldx, a.ldq = ldw, a.ldo = ldy;
-        np = nx, nq = nw, no = ny;
-    } else if (way == moe::MM_DX) {
-        a.P = s->M, a.Q = s->K, a.C = s->N;
-        a.ldp = ldy, a.ldq = ldw, a.ldo = ldx;
-        np = ny, nq = nw, no = nx;
-    } else {
-        a.P = s->N, a.Q = s->K, a.C = s->M;
-        a.ldp = ldy, a.ldq = ldx, a.ldo = ldw;
-        np = ny, nq = nx, no = nw;
-    }
-    a.qstride = a.ostride = s->N * ldw;
-    if (moe::mm16_most_tiles(a) >= (int64_t)1 << 31)
-        return fail(entry, "too many tiles of 16 x 16");
+    const int64_t esz = size_of(s->out_dtype), np = r.np, nq = r.nq, no = r.no;
     if (s->M == 0 && way != moe::MM_DW)
         return MOE_OK;
     if (!out || (s->M > 0 && (!p || !q)))
@@ -510,6 +525,21 @@ int moe_matmul_bf16(const moe_matmul_bf16_t *matmul, const void *x, const void *
                     const void *add, void *y, void *stream)
 {
     return matmul_bf16("moe_matmul_bf16", moe::MM_Y, matmul, x, w, offsets, add, y, stream);
+}
+
+int moe_matmul_bf16_tile(const moe_matmul_bf16_t *matmul, int way, int off16, int32_t *tile)
+{
+    const char *entry = "moe_matmul_bf16_tile";
+    if (way < moe::MM_Y || way > moe::MM_DW || !tile)
+        return fail(entry, "way must be 0, 1 or 2 and tile not NULL");
+    Product r;
+    if (const char *what = matmul_args(matmul, way, true, r))
+        return fail(entry, what);
+    r.a.p = (const uint16_t *)(uintptr_t)(off16 ? 2 : 0);
+    const moe::Mm16Pick t = moe::mm16_pick(r.a);
+    const int32_t v[] = {t.rows, t.cols, t.groups, t.whole};
+    std::copy(v, v + 4, tile);
+    return MOE_OK;
 }
 
 int moe_matmul_bf16_dx(const moe_matmul_bf16_t *matmul, const void *dy, const void *w, const int32_t *offsets,
