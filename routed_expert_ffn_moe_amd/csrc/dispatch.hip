@@ -28,6 +28,7 @@
 #include "common.h"
 #include "fp8.h"
 #include "kernels.h"
+#include "place.h"
 #include "quant_fp8.h"
 
 namespace moe {
@@ -40,18 +41,13 @@ namespace {
 // workgroup of the launch that also copies the rows.
 constexpr int TINY_PAIRS = 128;
 // Most blocks of pairs that each placing workgroup counts by itself, and whose
-// histograms it sums by itself; that work grows with the square of their number.
+// histograms it sums by itself; that work grows with the square of their number.  The
+// order alone on the GPU, with 4 blocks counted against 16: 136 pairs 4.0 us and 4.9,
+// 4096 5.2 and 6.0, 5120 6.4 (in two launches) and 6.2, 8192 6.4 and 6.7, 16384 6.7 and 8.1.
 constexpr int COUNT_BLOCKS = 4, SUM_BLOCKS = 64;
 
 // Pairs of a block: whole tokens, at most 1024.
 int block_pairs(int k) { return 1024 / k * k; }
-
-// Expert of pair p, or -1 if its slot is empty or p is behind the last pair.
-__device__ __forceinline__ int expert_of(const int32_t *__restrict__ idx, int p, int n, int E)
-{
-    const int e = p < n ? idx[p] : -1;
-    return (unsigned)e < (unsigned)E ? e : -1;
-}
 
 // Pairs of each block and expert: blk[b, e].
 __global__ __launch_bounds__(1024) void sort_hist(SortArgs a, int n, int per)
@@ -60,7 +56,7 @@ __global__ __launch_bounds__(1024) void sort_hist(SortArgs a, int n, int per)
     s_cnt[threadIdx.x] = 0;
     __syncthreads();
     const int p = (int)blockIdx.x * per + threadIdx.x;
-    const int e = (int)threadIdx.x < per ? expert_of(a.idx, p, n, a.E) : -1;
+    const int e = (int)threadIdx.x < per ? pair_expert(a.idx, p, n, a.E) : -1;
     if (e >= 0)
         atomicAdd(&s_cnt[e], 1);  // integer counts: order-free
     __syncthreads();
@@ -97,107 +93,23 @@ __global__ __launch_bounds__(1024) void sort_prefix(SortArgs a, int nblk)
         a.blk[(int64_t)nblk * a.E + e] = run;
 }
 
-// Places one block's pairs, a pair a thread.  Its first place with an expert is
-// the expert's offset (prefix over the experts' totals) plus the expert's pairs
-// in earlier blocks; inside the block the waves follow in order, and a wave's
-// lanes of one expert are ranked by a mask that ballots on the expert's bits
-// build.  Totals and earlier blocks' pairs are counted here from all pairs (COUNT),
-// summed here over the blocks' histograms (SUM), or come from sort_prefix.
-enum { COUNT = 0, SUM = 1, PREFIX = 2 };
-
+// Places one block's pairs (place.h), and the experts' offsets.
 template <int FROM>
 __global__ __launch_bounds__(1024) void sort_place(SortArgs a, int n, int per, int nblk)
 {
-    __shared__ int32_t s_start[1024];
-    __shared__ uint16_t s_wave[16][1024];  // pairs of a wave and expert, then those of the waves before
-    __shared__ int32_t s_wsum[16];
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, b = blockIdx.x;
-    const int p = b * per + tid;
-    const bool mine = tid < per && p < n;
-    const int e = mine ? expert_of(a.idx, p, n, a.E) : -1;
-    int total = 0, before = 0;
-    if constexpr (FROM == COUNT) {
-        __shared__ int32_t s_before[1024], s_rest[1024];
-        s_before[tid] = s_rest[tid] = 0;
-        __syncthreads();
-        int ev[COUNT_BLOCKS];  // all reads in flight together
-#pragma unroll
-        for (int i = 0; i < COUNT_BLOCKS; ++i)
-            ev[i] = tid < per ? expert_of(a.idx, i * per + tid, n, a.E) : -1;
-#pragma unroll
-        for (int i = 0; i < COUNT_BLOCKS; ++i)
-            if (ev[i] >= 0)
-                atomicAdd(i < b ? &s_before[ev[i]] : &s_rest[ev[i]], 1);  // integer counts: order-free
-        __syncthreads();
-        before = s_before[tid];
-        total = before + s_rest[tid];
-    } else if (tid < a.E) {
-        if constexpr (FROM == SUM) {
-            constexpr int AT = 16;
-            for (int b0 = 0; b0 < nblk; b0 += AT) {
-                int c[AT];
-#pragma unroll
-                for (int i = 0; i < AT; ++i)  // all reads in flight together
-                    c[i] = b0 + i < nblk ? a.blk[(int64_t)(b0 + i) * a.E + tid] : 0;
-#pragma unroll
-                for (int i = 0; i < AT; ++i) {
-                    total += c[i];
-                    before += b0 + i < b ? c[i] : 0;
-                }
-            }
-        } else {
-            total = a.blk[(int64_t)nblk * a.E + tid];
-            before = a.blk[(int64_t)b * a.E + tid];
-        }
-    }
-#pragma unroll
-    for (int w = 0; w < 16; ++w)
-        s_wave[w][tid] = 0;
-    const int inc = wave_scan_add(total);
-    if (lane == 63)
-        s_wsum[wv] = inc;
-    __syncthreads();
-    int first = inc - total;
-#pragma unroll
-    for (int w = 0; w < 16; ++w)
-        first += w < wv ? s_wsum[w] : 0;
-    if (tid < a.E)
-        s_start[tid] = first + before;
+    const int tid = threadIdx.x, b = blockIdx.x, p = b * per + tid;
+    const Placed r = place_pair<FROM, COUNT_BLOCKS>(a.idx, a.blk, nblk, b, per, n, a.E);
     if (b == 0) {
         if (tid < a.E)
-            a.offsets[tid] = first;
+            a.offsets[tid] = r.first;
         if (tid == a.E - 1)
-            a.offsets[a.E] = first + total;
+            a.offsets[a.E] = r.first + r.total;
     }
-    uint64_t same = __ballot(e >= 0);
-    for (int bit = 0; bit < 10; ++bit) {
-        const bool on = (e >> bit) & 1;
-        const uint64_t ones = __ballot(e >= 0 && on);
-        same &= on ? ones : ~ones;
-    }
-    const int rank = __popcll(same & (lane == 0 ? 0ull : ~0ull >> (64 - lane)));
-    if (e >= 0 && rank == 0)  // one writer per wave and expert
-        s_wave[wv][e] = (uint16_t)__popcll(same);
-    __syncthreads();
-    if (tid < a.E) {
-        int run = 0;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            const int c = s_wave[w][tid];
-            s_wave[w][tid] = (uint16_t)run;
-            run += c;
-        }
-    }
-    __syncthreads();
-    if (!mine)
+    if (tid >= per || p >= n)
         return;
-    int at = -1;
-    if (e >= 0) {
-        at = s_start[e] + s_wave[wv][e] + rank;
-        if (a.row_src)
-            a.row_src[at] = p;
-    }
-    a.row_of[p] = at;
+    if (r.at >= 0 && a.row_src)
+        a.row_src[r.at] = p;
+    a.row_of[p] = r.at;
 }
 
 // ---- rows -------------------------------------------------------------------
@@ -335,7 +247,7 @@ __global__ __launch_bounds__(256) void dispatch_tiny(SortArgs s, GatherArgs a)
     __shared__ int s_at[TINY_PAIRS];
     const int n = s.T * s.k, n4 = (n + 3) & ~3, tid = threadIdx.x;
     for (int p = tid; p < n4; p += 256) {
-        const int e = expert_of(s.idx, p, n, s.E);
+        const int e = pair_expert(s.idx, p, n, s.E);
         s_e[p] = e < 0 ? s.E : e;  // empty slots (and what fills up a word) behind all others
     }
     __syncthreads();
@@ -629,14 +541,14 @@ void launch_dispatch(const SortArgs &s, const GatherArgs &a, hipStream_t st)
     }
     const int per = block_pairs(s.k), nblk = (n + per - 1) / per;
     if (nblk <= COUNT_BLOCKS) {
-        sort_place<COUNT><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+        sort_place<PLACE_COUNT><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
     } else {
         sort_hist<<<nblk, 1024, 0, st>>>(s, n, per);
         if (nblk <= SUM_BLOCKS) {
-            sort_place<SUM><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+            sort_place<PLACE_SUM><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
         } else {
             sort_prefix<<<(s.E + 63) / 64, 1024, 0, st>>>(s, nblk);
-            sort_place<PREFIX><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
+            sort_place<PLACE_PREFIX><<<nblk, 1024, 0, st>>>(s, n, per, nblk);
         }
     }
     if (a.x)

@@ -18,6 +18,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "place.h"
 #include "quant_fp8.h"
 
 namespace moe {
@@ -29,8 +30,9 @@ constexpr int FUSED_HIST = 8192;
 // Most permutation blocks placed by permute_place (see launch_permute).
 constexpr int PLACE_MAX_BLOCKS = 256;
 
-// Most blocks whose pairs each placing workgroup counts by itself: that work
-// grows with the square of their number, and a thread holds a pair of each.
+// Most blocks whose pairs each placing workgroup counts by itself (place.h).  More
+// than where the dispatch operator turns to histograms (4): here a launch for these
+// would stand before the one that also quantises x, which hides the counting.
 constexpr int COUNT_MAX_BLOCKS = 16;
 
 // Orders one wave's LDS accesses across its lanes (no other wave shares
@@ -40,14 +42,6 @@ __device__ __forceinline__ void wave_lds_sync()
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-}
-
-// Expert of pair p, or -1 if its slot is empty (an index outside 0..E-1: given
-// routing may leave slots empty) or p is behind the last pair.
-__device__ __forceinline__ int pair_expert(const int32_t *__restrict__ idx, int p, int n_pairs, int E)
-{
-    const int e = p < n_pairs ? idx[p] : -1;
-    return (unsigned)e < (unsigned)E ? e : -1;
 }
 
 int permute_blocks(int n_pairs)
@@ -293,16 +287,10 @@ __global__ __launch_bounds__(1024) void permute_scan(
                       nblk, E, n_pairs, T, shared, items_a, ntn_a, wrows_a, items_b, ntn_b, wrows_b);
 }
 
-// One block of PAIRS_PER_BLOCK pairs placed by 1024 threads, one pair each,
-// without a separate scan pass: the block's first position in each expert's
-// range is the expert's offset (exclusive prefix over the experts of the
-// column sums of the block histograms) plus that expert's pairs in the
-// earlier blocks, both formed here from the histograms; inside the block the
-// waves follow in order and a wave's lanes with equal experts are ranked by
-// a ballot-built match mask.  The same grouped order as permute_scatter (t,
-// then j, within every expert).  COUNT: the sums of the histograms are counted
-// from the pairs (all of them; COUNT_MAX_BLOCKS bounds that work) instead.
-template <bool COUNT>
+// One block of PAIRS_PER_BLOCK pairs placed by 1024 threads without a separate scan
+// pass (place.h), in the same grouped order as permute_scatter, with what the experts
+// hold summed over the block histograms or counted from the pairs (FROM).
+template <int FROM>
 __device__ __forceinline__ void place_block(const int32_t *__restrict__ idx,
                                             const int32_t *__restrict__ blk, int nblk, int b,
                                             int32_t *__restrict__ row_src,
@@ -311,91 +299,14 @@ __device__ __forceinline__ void place_block(const int32_t *__restrict__ idx,
                                             int T, int k, int shared)
 {
     static_assert(PAIRS_PER_BLOCK == 1024, "one pair per thread");
-    __shared__ int32_t s_start[1024];
-    __shared__ uint16_t s_wc[16][1024];  // per wave and expert: pairs, then pairs in earlier waves
-    __shared__ int32_t s_wsum[16];
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int p = b * PAIRS_PER_BLOCK + tid;
-    const int e = pair_expert(idx, p, n_pairs, E);
-    constexpr int SCH = 16;
-    // column sums over all blocks (the expert's rows) and over those before b
-    int tot = 0, pre = 0;
-    if constexpr (COUNT) {
-        __shared__ int32_t s_tot[1024], s_pre[1024];
-        s_tot[tid] = s_pre[tid] = 0;
-        __syncthreads();
-        int ev[COUNT_MAX_BLOCKS];  // all reads in flight together
-#pragma unroll
-        for (int i = 0; i < COUNT_MAX_BLOCKS; ++i)
-            ev[i] = pair_expert(idx, i * PAIRS_PER_BLOCK + tid, n_pairs, E);
-#pragma unroll
-        for (int i = 0; i < COUNT_MAX_BLOCKS; ++i)
-            if (ev[i] >= 0) {
-                atomicAdd(&s_tot[ev[i]], 1);  // integer counts: order-free
-                if (i < b)
-                    atomicAdd(&s_pre[ev[i]], 1);
-            }
-        __syncthreads();
-        tot = s_tot[tid];
-        pre = s_pre[tid];
-    } else if (tid < E) {
-        for (int b0 = 0; b0 < nblk; b0 += SCH) {
-            int c[SCH];
-#pragma unroll
-            for (int i = 0; i < SCH; ++i)  // all reads in flight together
-                c[i] = b0 + i < nblk ? blk[(int64_t)(b0 + i) * E + tid] : 0;
-#pragma unroll
-            for (int i = 0; i < SCH; ++i) {
-                tot += c[i];
-                pre += b0 + i < b ? c[i] : 0;
-            }
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 16; ++q)
-        s_wc[q][tid] = 0;
-    // exclusive prefix of the experts' rows
-    const int inc = wave_scan_add(tot);
-    if (lane == 63)
-        s_wsum[wv] = inc;
-    __syncthreads();
-    int before = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w)
-        before += w < wv ? s_wsum[w] : 0;
-    if (tid < E)
-        s_start[tid] = before + inc - tot + pre;
-    // rank among this wave's earlier pairs of the same expert
-    const bool valid = e >= 0;
-    uint64_t same = __ballot(valid);
-    for (int bit = 0; bit < 10; ++bit) {
-        const bool on = (e >> bit) & 1;
-        const uint64_t ones = __ballot(valid && on);
-        same &= on ? ones : ~ones;
-    }
-    const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
-    const int rank = __popcll(same & below);
-    if (valid && rank == 0)  // one writer per wave and expert
-        s_wc[wv][e] = (uint16_t)__popcll(same);
-    __syncthreads();
-    if (tid < E) {
-        int run = 0;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            const int c = s_wc[w][tid];
-            s_wc[w][tid] = (uint16_t)run;
-            run += c;
-        }
-    }
-    __syncthreads();
-    if (valid) {
-        const int pos = s_start[e] + s_wc[wv][e] + rank;
+    const int tid = threadIdx.x, p = b * PAIRS_PER_BLOCK + tid;
+    const int pos = place_pair<FROM, COUNT_MAX_BLOCKS>(idx, blk, nblk, b, PAIRS_PER_BLOCK, n_pairs, E).at;
+    if (pos >= 0) {
         row_src[pos] = p;
         row_tok[pos] = p / k;
-        row_of[p] = pos;
-    } else if (p < n_pairs) {
-        row_of[p] = -1;
     }
+    if (p < n_pairs)
+        row_of[p] = pos;
     // shared-expert rows follow the routed ones, in token order
     if (shared && b == 0) {
         for (int t = tid; t < T; t += 1024) {
@@ -424,7 +335,7 @@ __global__ __launch_bounds__(1024) void permute_place(
                            items_b, ntn_b, wrows_b);
         return;
     }
-    place_block<false>(idx, blk, nblk, blockIdx.x, row_src, row_tok, row_of, n_pairs, E, T, k, shared);
+    place_block<PLACE_SUM>(idx, blk, nblk, blockIdx.x, row_src, row_tok, row_of, n_pairs, E, T, k, shared);
 }
 
 // The permutation of a short pass and the codes of its rows of x, in one launch:
@@ -441,7 +352,7 @@ __global__ __launch_bounds__(1024) void permute_quant(PermuteArgs a, QuantArgs q
                            a.ntiles_b, a.bm_a, a.bm_b, nblk, a.E, n_pairs, a.T, 0, nullptr, 0, 0, nullptr,
                            0, 0);
     else if (b < nblk)
-        place_block<true>(a.idx, nullptr, nblk, b, a.row_src, a.row_tok, a.row_of, n_pairs, a.E, a.T, a.k, 0);
+        place_block<PLACE_COUNT>(a.idx, nullptr, nblk, b, a.row_src, a.row_tok, a.row_of, n_pairs, a.E, a.T, a.k, 0);
     else
         quant_row_blocks<true, true>(q, (int64_t)(b - nblk) * 64 + (threadIdx.x >> 4),
                                      (int64_t)(gridDim.x - 1 - nblk) * 64);
