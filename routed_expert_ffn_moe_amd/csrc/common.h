@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
@@ -130,6 +132,25 @@ __device__ __forceinline__ int wave_scan_add(int v)
     v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
     v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
     v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
+}
+
+// Sum over each 1 << shift lanes (16, 32 or 64), in the last of them.
+__device__ __forceinline__ float lanes_sum(float v, int shift)
+{
+    auto add = [&](auto ctrl, auto rows) {
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
+                                                        decltype(rows)::value, 0xf, false));
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    if (shift > 4)
+        add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+    if (shift > 5)
+        add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
     return v;
 }
 

@@ -193,16 +193,9 @@ __device__ __forceinline__ void gather_columns(const GatherArgs &a, int64_t t, i
     Raw8<F32> v;
     int left = a.H - c;
     if constexpr (SRC == GATHER_FP8) {
-        const uint2 u = *(const uint2 *)((const uint8_t *)a.x + t * a.ldx + c);  // whole blocks: no tail
-        const float f = a.sx[t * ((a.H + FP8_BLOCK - 1) / FP8_BLOCK) + c / FP8_BLOCK];
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = i < 2 ? u.x : u.y;
-            const auto two = i & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-            x[2 * i] = two[0] * f;
-            x[2 * i + 1] = two[1] * f;
-        }
+        float x[8];  // whole blocks: no tail
+        decode8(x, (const uint8_t *)a.x + t * a.ldx + c,
+                a.sx[t * ((a.H + FP8_BLOCK - 1) / FP8_BLOCK) + c / FP8_BLOCK]);
         v = make_raw<F32>(x);
     } else if (a.H >= 8) {
         c = inside(c, a.H);
@@ -361,25 +354,6 @@ __global__ __launch_bounds__(256) void combine_rows(CombineRowsArgs a, int shift
             }
         }
     }
-}
-
-// Sum over each 1 << shift lanes (16, 32 or 64), in the last of them.
-__device__ __forceinline__ float lanes_sum(float v, int shift)
-{
-    auto add = [&](auto ctrl, auto rows) {
-        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
-                                                        decltype(rows)::value, 0xf, false));
-    };
-    using std::integral_constant;
-    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-    if (shift > 4)
-        add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
-    if (shift > 5)
-        add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
-    return v;
 }
 
 template <int KM, bool F32>

@@ -49,7 +49,8 @@ __device__ __forceinline__ words4 fetch(const uint16_t *base, int64_t ld, int x,
     return v;
 }
 
-// 8 adjacent results, `left` of them inside the output.
+// 8 adjacent results, `left` of them inside the output.  (load8 and store8 in its place
+// cost the tiles of 128 x 128 a third of their rate: 5000 x 1001 x 777 with an addend 50 us, so 34.)
 template <bool F32>
 __device__ __forceinline__ void put8(const Mm16Args &a, int64_t at, float (&v)[8], int left)
 {

@@ -35,21 +35,11 @@ namespace moe {
 
 namespace {
 
-constexpr int DROP = (int)0x80000000;  // an offset outside every buffer: loads give 0, stores do nothing
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// Buffer of the bytes from p on.
+// The words of buffer_from(p), for the copies.
 __device__ __forceinline__ intx4 buffer_words(const void *p)
 {
     const uint64_t b = (uint64_t)(uintptr_t)p;
     return intx4{(int)b, (int)(b >> 32) & 0xFFFF, 0x7FFFFFFF, 0x00027000};
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rsrc(const void *p)
-{
-    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00027000);
 }
 
 // As dma16 (fp8.h), through a buffer: an offset of DROP writes zeros to LDS.
@@ -424,8 +414,8 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_tile(Mm16Args a, int m
         int e16 = lane & 15, eg = lane >> 4;  // hidden as in next_p()
         asm volatile("" : "+v"(e16), "+v"(eg));
         constexpr int esz = F32 ? 4 : 2, V = F32 ? 2 : 1;  // 16-byte stores of a pair
-        const auto ro = out_rsrc((const char *)a.out + cur.out * esz);
-        const auto ra = out_rsrc((const char *)(a.add ? a.add : a.out) + cur.out * esz);
+        const auto ro = buffer_from((const char *)a.out + cur.out * esz);
+        const auto ra = buffer_from((const char *)(a.add ? a.add : a.out) + cur.out * esz);
         const int pitch = (int)a.ldo * esz;
         if constexpr (NB == 1) {  // 4 adjacent columns of a row
             if (kg == 0)

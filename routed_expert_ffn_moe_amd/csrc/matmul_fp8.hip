@@ -53,17 +53,7 @@ constexpr int MAX_KB = FP8_MAX_K / FP8_BLOCK;  // scale blocks along K whose wei
 // Results as they are, h = silu(gate) * up as codes, or staging rows (fp8.h).
 enum { EPI_PLAIN = 0, EPI_SWIGLU = 1, EPI_STAGE = 2 };
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
-// Buffer of the bytes from p on; an offset of DROP is out of its range, where
-// stores do nothing.
-constexpr int DROP = (int)0x80000000;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(void *p)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(p, 0, 0x7FFFFFFF, 0x00027000);
-}
 
 template <int NBW, int BM_, int WN, int WM, int ST, int EPI>
 struct Cfg {
@@ -448,7 +438,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
         const int n = n0 + wn * (NBW * 16) + eg * (4 * NBW);
         const int esz = p.out_f32 ? 4 : 2;
         const int pitch = (int)p.ldy * esz;  // checked by the host where p.vec
-        const auto rsrc = tile_rsrc((char *)p.y + (int64_t)row0 * p.ldy * esz);
+        const auto rsrc = buffer_from((char *)p.y + (int64_t)row0 * p.ldy * esz);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int rr = (m * WM + wm) * 16 + e16;
@@ -505,8 +495,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
     } else if constexpr (EPI == EPI_STAGE) {
         static_assert(NBW == 4, "a lane holds the columns under two exponents");
         const int n = n0 + wn * 64 + eg * 16;
-        const auto rsrc = tile_rsrc((uint16_t *)p.y + (int64_t)row0 * p.N);
-        const auto rexp = tile_rsrc(p.exps + (int64_t)row0 * (p.N / 8));
+        const auto rsrc = buffer_from((uint16_t *)p.y + (int64_t)row0 * p.N);
+        const auto rexp = buffer_from(p.exps + (int64_t)row0 * (p.N / 8));
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int rr = (m * WM + wm) * 16 + e16;
@@ -559,8 +549,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile(Fp8Args p)
                 s_max[wn * BM + (m * WM + wm) * 16 + e16] = mx;
         }
         lds_barrier();
-        const auto rh = tile_rsrc(p.hq + (int64_t)row0 * p.N);
-        const auto rs = tile_rsrc(p.hs + (int64_t)row0 * (p.N >> 7));
+        const auto rh = buffer_from(p.hq + (int64_t)row0 * p.N);
+        const auto rs = buffer_from(p.hs + (int64_t)row0 * (p.N >> 7));
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int rr = (m * WM + wm) * 16 + e16, at = min(rr, BM - 1);

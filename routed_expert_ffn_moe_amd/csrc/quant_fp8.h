@@ -47,6 +47,46 @@ __device__ __forceinline__ void load8(float (&v)[8], const void *x, int64_t row,
     }
 }
 
+// The same the other way: the first `left` of 8 values, rounded once.
+template <bool BF16>
+__device__ __forceinline__ void store8(const float (&v)[8], void *p, int64_t at, int left)
+{
+    if (left >= 8) {
+        if constexpr (BF16) {
+            *(words4 *)((uint16_t *)p + at) =
+                words4{cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7])};
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *(words4 *)((float *)p + at + 4 * q) =
+                    words4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < left) {
+            if constexpr (BF16)
+                ((uint16_t *)p)[at + i] = (uint16_t)cvt_bf2(v[i], 0.0f);
+            else
+                ((float *)p)[at + i] = v[i];
+        }
+}
+
+// The values of 8 codes under the scale f.
+__device__ __forceinline__ void decode8(float (&v)[8], const uint8_t *codes, float f)
+{
+    const uint2 u = *(const uint2 *)codes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? u.x : u.y;
+        const auto two = i & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+        v[2 * i] = two[0] * f;
+        v[2 * i + 1] = two[1] * f;
+    }
+}
+
 __device__ __forceinline__ float amax8(const float (&v)[8])
 {
     float m = 0.0f;

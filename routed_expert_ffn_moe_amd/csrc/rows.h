@@ -13,6 +13,17 @@ __device__ __forceinline__ T uniform_load(const T *p)
     return *(const __attribute__((address_space(4))) T *)(uintptr_t)p;
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Buffer of the bytes from p on; an offset of DROP is out of its range: loads give 0,
+// stores do nothing.
+constexpr int DROP = (int)0x80000000;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_from(const void *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00027000);
+}
+
 // A tile: rows [row0, row0 + nrows) of group g (g = -1: none), columns from n0.
 struct Where {
     int g, row0, nrows, n0, q;

@@ -40,18 +40,7 @@ constexpr float SIGMOID_ZERO = -709.78f, SOFTMAX_ZERO = -745.14f;
 // Sum and maximum over the wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v)
 {
-    auto add = [&](auto ctrl, auto rows) {
-        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
-                                                        decltype(rows)::value, 0xf, false));
-    };
-    using std::integral_constant;
-    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
-    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lanes_sum(v, 6)), 63));
 }
 
 __device__ __forceinline__ float wave_max(float v) { return key_value(wave_max_u32(order_key(v))); }
