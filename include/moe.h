@@ -343,7 +343,7 @@ int moe_dispatch(const moe_dispatch_t *dispatch, const int32_t *topk_idx, const 
                  void *stream);
 
 /* The rows alone, by a row_of [T, top_k] that moe_dispatch has made: places outside
- * 0 .. T * top_k - 1 take no row.  (E is not used.) */
+ * 0 .. T * top_k - 1 take no row.  (E has to be in its range, and is not used.) */
 int moe_gather(const moe_dispatch_t *dispatch, const int32_t *row_of, const void *x, const float *sx, void *rows,
                void *stream);
 
@@ -397,7 +397,8 @@ int moe_swiglu_grad(const moe_swiglu_t *swiglu, const void *gate, const void *up
 /* Gradient of moe_select to the logits: dlogits [T, E] (dense, dlogit_dtype MOE_F32 or
  * MOE_BF16) of a loss whose gradient to the weights is dtopk_w [T, top_k] and to every
  * token's score s_e is dscore[e] (NULL: none; a balance loss c * sum_e f_e * mean_t
- * s_te has dscore[e] = c * f_e / T).  The selection itself, the bias and the groups are
+ * s_te has dscore[e] = c * f_e / T; one over scores that each token divides by their sum
+ * has gradients that differ from token to token and is not covered).  The selection itself, the bias and the groups are
  * constants: T, E, top_k, score, renorm, logit_dtype, scale and ld of `select` are
  * used.  topk_idx as moe_select wrote it.  Masked experts (by logit or bias) have
  * score 0 and pass no gradient from dtopk_w or dscore, nor do experts whose score is
@@ -419,8 +420,8 @@ int moe_select_grad(const moe_select_t *select, const void *logits, const float 
  * used.  offsets is a device array, not decreasing; parts of it outside 0..M are cut
  * off (of offsets that decrease it is not defined which rows are taken, but nothing
  * outside 0..M is); with G = 1 NULL takes all rows.  Any sizes, strides and element alignment are
- * taken; strides that are multiples of 8 elements with pointers aligned to 16 bytes
- * are fast. */
+ * taken; sizes and strides that are multiples of 8 elements (rows: any number), strides below
+ * 2^20 and pointers aligned to 16 bytes are fast. */
 typedef struct {
     int32_t M, N, K;     /* rows; rows and columns of each w; at most 2^30 each */
     int32_t G;           /* matrices w, 1..65535                                */

@@ -19,7 +19,9 @@
 // Bound by memory.  T=8192, H=4096, k=6: dispatch 104 us, of which the copy of 67 MB to
 // 395 is 94 (4.9 TB/s, a large copy's rate) and the order 10; combine's gradient 177 (856
 // MB, 4.8 TB/s).  T=2048, H=2048, k=8: combine 13.4 us (75 MB, partly from the infinity
-// cache).  One token's dispatch 3.7 us on the GPU, 7.4 from Python: the host's call.  The gradient
+// cache).  One token's dispatch 3.8 us on the GPU, 7.1 from Python: the host's call; 17, 128
+// and 512 tokens, k=8, H=2048 7.5, 8.3 and 10.9 (9.9 to 11 from Python), of which the order takes
+// 4.0 to 5.2 in a launch of its own.  The gradient
 // of 7 tokens, k=10, H=980: 8.4 us, 17.8 while a tail went element by element and the sums
 // through LDS.
 #include <algorithm>

@@ -28,8 +28,8 @@ namespace {
 // The tiles of mm16.h, staged through registers a step ahead: pieces of 8 elements
 // are read at any element's address, and one by one where they end outside the
 // operand (0 there).  Two stages in LDS, so that a step has one barrier.
-// Bound by what a step waits for: 6900 x 577 x 937 (dw) 55 us, 225 with tiles of 64 x 64 x 32 by
-// one group of waves and 2-byte writes to LDS.  Reads two steps ahead made no difference.
+// Bound by what a step waits for, one round of register loads: 6900 x 577 x 937 (dw) 56 us
+// with warm caches, 75 cold, where its bytes take 4.7.  Reads two steps ahead made no difference.
 
 // Elements of a piece: along c of element x (c adjacent), or elements from x on at c.
 template <bool ADJ>
@@ -205,10 +205,11 @@ __global__ __launch_bounds__(64 * WP * WQ * WK) void mm16_any(Mm16Args a, int ti
     }
 }
 
-// Tiles of 128 x 128 where they give every CU one, else of 64 x 64 by two groups of
-// waves, or by four where the tiles leave CUs without one and c is long: 3000 x 333 x 501
-// (dw, fp32) 67 us by two, 47 by four, 101 x 333 x 2050 (y) 18.5 and 13.7 to 15.7, but 73 x 204 x 141 (dw) 5.8
-// and 6.8; at c of 500 the two are alike.
+// Tiles of 128 x 128 where they give every CU one (5000 x 1001 x 777 (y) 33 us, 40 with
+// 64 x 64), else of 64 x 64 by two groups of waves, or by four where the tiles leave CUs
+// without one and c is long: 3000 x 333 x 501 (dw, fp32) 62 us by two, 43 by four, 101 x 333 x
+// 2050 (y) 15.3 and 13.3, but 73 x 204 x 141 (dw) 5.8 and 6.8; at c of 500 the two are alike
+// (101 x 333 x 501 8.2 and 8.4).  Warm caches.
 Mm16Pick any_pick(const Mm16Args &a)
 {
     if (mm16_tile_count(a, 128, 128) >= 256)
@@ -246,21 +247,22 @@ struct Cost {
 
 // `end` is what a tile's sums and output cost, also once a round of tiles.
 //
-// Fitted to products of 1 to 65536 rows in 1 to 256 groups, each with all tiles: 116 of y
-// and of dx, N and K from 8 to 4096, where the pick's time is on average 0.5% (y) and 0.3%
-// (dx) above the best tile's (80 others are 5% faster than without `end`), and 56 of dw
-// (2%).  dx's 64 x 256 counts for a little more than fitted, so that close cases take
-// 128 x 256, which groups of unequal size prefer: 16384 Zipf rows of 256 groups 184 against
-// 192, as many rows in equal groups 171 and 170.  In us, largest against smallest tiles of
-// that list: 8192 x 4096 x 4096 201 against 1456 (y), 48 rows of 256 groups, N=768, K=2048
-// 138 against 59; of K=8 16384 rows of 256 groups, N=2048 61 against 762 (64 x 128 40).
-// dx has no tiles of 16 columns, whose rows of c would be 32 bytes;
-// of dw, whose depth is the group's rows, the small tiles' outputs cost most (`end`):
-// 256 groups of 64 rows 236 against 388.  Few tiles of dw are bound by what a CU
-// reads.  There two groups of waves take 64 of c each: 52 against 61 for 8192 rows, N=256,
-// K=2048 (128 tiles; 63 with three groups of two stages), but 93 against 84 for 4096 x 2048 x
-// 2048 (1024 tiles); and where 32 x 32 gives no more tiles than CUs, each reads half as
-// much: 22 against 28 for 4096 x 512 x 512, but 61 against 52 for the 512 tiles of 8192 x 256 x 2048.
+// Fitted to products of 1 to 65536 rows in 1 to 256 groups, N and K from 8 to 4096, each with
+// all tiles.  70 others of each way, drawn as they come, take on average 3% (y), 2% (dx)
+// and 3.5% (dw) more than with the best tile (warm caches; 33%, 15% and 48% at most).  In us, warm
+// / cold caches, largest against smallest tiles of the list: 8192 x 4096 x 4096 198 / 193
+// against 1405 / 1433 (y), 48 rows of 256 groups, N=768, K=2048 120 / 138 against 26 / 54; of
+// K=8 16384 rows of 256 groups, N=2048 56 / 56 against 759 / 758 (64 x 128 37 / 38).
+// dx has no tiles of 16 columns, whose rows of c would be 32 bytes.  Its 64 x 256 costs more
+// than the first fit's 0.69 for a step: in 46 products where the two choose apart the tiles
+// that 0.78 takes are 13% faster on average (8% cold), in 44 faster, 7% slower at most; 16384 rows of
+// 256 groups 180 against 190 (Zipf), 163 against 163 (equal).
+// Of dw, whose depth is the group's rows, the small tiles' outputs cost most (`end`): 256
+// groups of 64 rows, N=768, K=2048 227 against 376 with 64 x 64.  Few tiles of dw are bound by
+// what a CU reads.  There two groups of waves take 64 of c each: 28 / 46 against 37 / 55 for
+// 8192 rows, N=256, K=2048 (128 tiles), but 63 / 87 against 60 / 79 for 4096 x 2048 x 2048
+// (1024 tiles); and where 32 x 32 gives no more tiles than CUs, each reads half as much: 12 /
+// 18 against 16 / 24 for 4096 x 512 x 512, but 43 / 59 against 28 / 46 for the 512 tiles of 8192 x 256 x 2048.
 constexpr Cost COST_Y[MM16_NY] = {{1.3, 1.5, 7.8}, {1.1, 0.84, 5.9}, {0.49, 0.44, 1.4},
                                   {0.29, 0.48, 1.5}, {0.19, 0.27, 1.4}, {0.036, 0.06, 1.4}};
 constexpr Cost COST_DX[MM16_NDX] = {{1.2, 2.2, 10}, {0.96, 1.1, 5.3}, {0.93, 0.78, 3.6},
@@ -274,8 +276,11 @@ constexpr Cost COST_DW[MM16_NDW] = {{1.19, 1.69, 5.7}, {0.84, 0.57, 1.8}, {0.51,
 //
 // Groups of a few rows read their weights once, from memory, and tiles of 16 columns
 // keep more of it busy than those of 64, unless c is so short that the tiles' ends
-// count: 48 rows of 256 groups with N=768, K=2048 34 us against 38, 2048 rows 162
-// against 187, but 48 rows with N=2048, K=768 47 against 39.
+// count.  In us, warm / cold: 48 rows of 256 groups with N=768, K=2048 26 / 54 against 30 /
+// 65, 1024 rows 143 / 183 against 149 / 189, but 48 rows with N=2048, K=768 44 / 57 against
+// 30 / 57.  Over 60 products of at most 11 rows a group, N from 256 and c from 1024 on, this
+// choice is on average 4% / 3% above the best of three tiles (27% / 20% at most: Zipf rows, or c of
+// little more than 1024), the costs alone 12% / 15%, 16 x 64 always 10% / 16%.
 template <int N>
 int mm16_shape(const Mm16Args &a, const Mm16Shape (&shapes)[N], const Cost (&costs)[N])
 {

@@ -19,8 +19,12 @@
 // eight (y 215 to 223 against 212 to 229) and raised priority around the MFMAs (dx 202
 // against 197, dw 204 against 205) make no difference beyond the runs' own.
 // Bound by memory where groups have few rows, N=768, K=2048: 48 rows of 256 groups 29 to 32
-// us, 4.7 to 5.2 TB/s; 16384 rows (Zipf) of 256 groups back to dx 181 us, 5.0 TB/s; their dw with
-// an fp32 addend 668 us, 5.0 TB/s.
+// us with inputs that change from call to call (26 warm, 54 cold), 4.7 to 5.2 TB/s; 16384
+// rows (Zipf) of 256 groups back to dx 181 us (180 warm, 212 cold), 5.0 TB/s; their dw with an
+// fp32 addend 668 us, 5.0 TB/s.
+// Bound by the CUs that take part where there are few tiles and c is long, since c is split
+// over the waves of a workgroup only: 8192 x 256 x 2048 (dw) 28 us warm, where its bytes take
+// 8; 512 x 4096 x 4096 (y) 26 warm, where its flops take 11.
 #pragma once
 
 #include <algorithm>

@@ -18,9 +18,11 @@
 // One wave per token, its row of logits in registers; slots are passed round by
 // readlane (LDS shuffles in their place: T=8192 14.4 us).
 //
-// Bound by its instructions: T=8192, E=384, k=6, sigmoid with a
-// balance gradient 12.0 us (its 25 MB take 5.2), T=2048, E=256, k=8, softmax over bf16 logits
-// 4.4, from Python 5.5 to 6, the host's call.
+// Bound by its instructions, as they stand: every slot is compared with every register of
+// the row under a branch of its own, and what a slot needs is computed by a wave of which
+// only k lanes live.  On the GPU, warm: T=8192, E=384, k=6, sigmoid with a balance gradient 12.2
+// us, without one 10.1 (its 25 MB take 5.2), T=2048, E=256, k=8, softmax over bf16 logits 4.6, from
+// Python 5.9, the host's call.
 #include <algorithm>
 #include <type_traits>
 
