@@ -397,13 +397,15 @@ int moe_swiglu_grad(const moe_swiglu_t *swiglu, const void *gate, const void *up
 /* Gradient of moe_select to the logits: dlogits [T, E] (dense, dlogit_dtype MOE_F32 or
  * MOE_BF16) of a loss whose gradient to the weights is dtopk_w [T, top_k] and to every
  * token's score s_e is dscore[e] (NULL: none; a balance loss c * sum_e f_e * mean_t
- * s_te has dscore[e] = c * f_e / T; one over scores that each token divides by their sum
- * has gradients that differ from token to token and is not covered).  The selection itself, the bias and the groups are
- * constants: T, E, top_k, score, renorm, logit_dtype, scale and ld of `select` are
- * used.  topk_idx as moe_select wrote it.  Masked experts (by logit or bias) have
- * score 0 and pass no gradient from dtopk_w or dscore, nor do experts whose score is
- * 0 in 64 bits.  An index outside 0..E-1 counts as no slot: it is left out of
- * the renormalising sum as well (a slot dropped after the selection keeps its index here,
+ * s_te has dscore[e] = c * f_e / T; one over scores that each token divides by their
+ * sum has gradients that differ from token to token and is not covered).  The selection
+ * itself, the bias and the groups are constants: T, E, top_k, score, renorm,
+ * logit_dtype, scale and ld of `select` are used.  topk_idx as moe_select wrote it.
+ * Masked experts (by logit or bias) have score 0 and pass no gradient from dtopk_w or
+ * dscore, nor do experts whose score is 0 in 64 bits; what passes through a score, its
+ * rest to 1 or a ratio of selected scores below 2^-126 loses digits, and below 2^-149 it
+ * is 0 (fp32).  An index outside 0..E-1 counts as no slot: it is left out of the
+ * renormalising sum as well (a slot dropped after the selection keeps its index here,
  * with dtopk_w 0). */
 int moe_select_grad(const moe_select_t *select, const void *logits, const float *bias, const int32_t *topk_idx,
                     const float *dtopk_w, const float *dscore, void *dlogits, int dlogit_dtype, void *stream);
